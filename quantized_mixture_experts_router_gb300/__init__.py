@@ -1,4 +1,5 @@
-"""Python binding of libmoe_v41 (include/moe_v41.h): argument marshalling only.
+"""Python binding of libmoe_v41 (include/moe_v41.h, moe_v41_cache.h and
+moe_v41_ops.h): argument marshalling only.
 
 Every step of the MoE layer runs in the library's sm_103a kernels; this
 module converts torch tensors (device memory) and streams into the C-ABI's
@@ -18,6 +19,9 @@ MOE_SCORE_SQRTSOFTPLUS, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1, 2
 MOE_SHARED_BF16, MOE_SHARED_KQUANT = 0, 1
 MOE_OK, MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_CUDA = 0, 1, 2, 3, 4
 MOE_STATUS_NAN_KEY, MOE_STATUS_MISSING_EXPERT, MOE_STATUS_TIMEOUT = 1, 2, 4
+MOE_T_F32, MOE_T_BF16, MOE_T_F16 = 0, 1, 2
+MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1, 2
+MOE_GATE_NONE, MOE_GATE_ROW, MOE_GATE_TOKEN = 0, 1, 2
 
 
 class MoeError(RuntimeError):
@@ -44,6 +48,24 @@ class moe_v41_cache_stats(ctypes.Structure):
     _fields_ = [("hits", ctypes.c_uint64), ("misses", ctypes.c_uint64), ("evictions", ctypes.c_uint64),
                 ("bytes_copied", ctypes.c_uint64), ("prefetched", ctypes.c_uint64),
                 ("prefetch_hits", ctypes.c_uint64)]
+
+
+class moe_v41_q4_cfg(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("group", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("scale_type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("max_tokens", ctypes.c_int32)]
+
+
+class moe_v41_norm_cfg(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("post_kind", ctypes.c_int32), ("pre_kind", ctypes.c_int32),
+                ("y_type", ctypes.c_int32), ("h_type", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("w_type", ctypes.c_int32), ("gate_kind", ctypes.c_int32), ("gate_type", ctypes.c_int32),
+                ("gate_group", ctypes.c_int32), ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("block_scale", ctypes.c_float)]
+
+
+class moe_v41_logprob_cfg(ctypes.Structure):
+    _fields_ = [("vocab", ctypes.c_int32), ("logit_type", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("temperature", ctypes.c_float)]
 
 
 _lib = None
@@ -83,11 +105,19 @@ def lib():
         L.moe_v41_cache_get_stats.argtypes = [cp, ctypes.POINTER(moe_v41_cache_stats)]
         L.moe_v41_forward_streamed.argtypes = [cfgp, cp, i32, vp, i32, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp,
                                                vp, vp, sz, vp, vp, vp]
+        i64 = ctypes.c_int64
+        q4p, nmp, lpp = (ctypes.POINTER(c) for c in (moe_v41_q4_cfg, moe_v41_norm_cfg, moe_v41_logprob_cfg))
+        L.moe_v41_q4_workspace_bytes.restype = sz
+        L.moe_v41_q4_workspace_bytes.argtypes = [q4p]
+        L.moe_v41_q4_linear.argtypes = [q4p, vp, i32, i64, vp, vp, vp, vp, i64, vp, sz, vp]
+        L.moe_v41_block_norm.argtypes = [nmp, i32, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp]
+        L.moe_v41_token_logprobs.argtypes = [lpp, vp, i32, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
         for f in ("moe_v41_workspace_init", "moe_v41_quantize_q8_1", "moe_v41_select_from_logits", "moe_v41_route",
                   "moe_v41_forward", "moe_v41_read_status", "moe_v41_forward_noalloc",
                   "moe_v41_select_from_logits_vl", "moe_v41_route_vl", "moe_v41_forward_vl", "moe_v41_cache_create",
                   "moe_v41_cache_destroy", "moe_v41_cache_fetch", "moe_v41_cache_wait", "moe_v41_cache_reads",
-                  "moe_v41_cache_slot_of", "moe_v41_cache_get_stats", "moe_v41_forward_streamed"):
+                  "moe_v41_cache_slot_of", "moe_v41_cache_get_stats", "moe_v41_forward_streamed",
+                  "moe_v41_q4_linear", "moe_v41_block_norm", "moe_v41_token_logprobs"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -280,3 +310,44 @@ def moe_v41_forward_streamed(cfg, cache: ExpertCache, layer, x, m, router_w, bia
                                           _p(sh_w3), _p(sh_w2), _p(out), _p(topk_w), _p(topk_idx), _p(ws),
                                           _nbytes(ws), _p(host_picks), _s(stream), _s(copy_stream)),
            "moe_v41_forward_streamed")
+
+
+# ------------------------------------- operators around the MoE layer (moe_v41_ops.h)
+
+def make_q4_cfg(n, k, group=128, x_type=MOE_T_BF16, scale_type=MOE_T_F16, out_type=MOE_T_F32,
+                max_tokens=1) -> moe_v41_q4_cfg:
+    return moe_v41_q4_cfg(n, k, group, x_type, scale_type, out_type, max_tokens)
+
+
+def moe_v41_q4_workspace_bytes(cfg: moe_v41_q4_cfg) -> int:
+    return int(lib().moe_v41_q4_workspace_bytes(ctypes.byref(cfg)))
+
+
+def moe_v41_q4_linear(cfg, x, m, ldx, w, scales, zeros, out, ldo, ws, stream=None):
+    _check(lib().moe_v41_q4_linear(ctypes.byref(cfg), _p(x), m, ldx, _p(w), _p(scales), _p(zeros), _p(out), ldo,
+                                   _p(ws), _nbytes(ws), _s(stream)), "moe_v41_q4_linear")
+
+
+def make_norm_cfg(dim, post_kind=MOE_NORM_RMS, pre_kind=MOE_NORM_RMS, y_type=MOE_T_F32, h_type=MOE_T_BF16,
+                  x_type=MOE_T_BF16, w_type=MOE_T_F32, gate_kind=MOE_GATE_NONE, gate_type=MOE_T_F32, gate_group=1,
+                  eps=1e-6, residual_scale=1.0, block_scale=1.0) -> moe_v41_norm_cfg:
+    return moe_v41_norm_cfg(dim, post_kind, pre_kind, y_type, h_type, x_type, w_type, gate_kind, gate_type,
+                            gate_group, eps, residual_scale, block_scale)
+
+
+def moe_v41_block_norm(cfg, m, y, ldy, post_w, post_b, gate, ldg, h, ldh, h_out, ldh_out, pre_w, pre_b, x_out, ldx,
+                       stream=None):
+    _check(lib().moe_v41_block_norm(ctypes.byref(cfg), m, _p(y), ldy, _p(post_w), _p(post_b), _p(gate), ldg, _p(h),
+                                    ldh, _p(h_out), ldh_out, _p(pre_w), _p(pre_b), _p(x_out), ldx, _s(stream)),
+           "moe_v41_block_norm")
+
+
+def make_logprob_cfg(vocab, logit_type=MOE_T_F32, top_k=0, temperature=1.0) -> moe_v41_logprob_cfg:
+    return moe_v41_logprob_cfg(vocab, logit_type, top_k, temperature)
+
+
+def moe_v41_token_logprobs(cfg, logits, m, ld, allowed, ld_allowed, target, logprob, rank, lse, entropy,
+                           top_logprob, top_id, stream=None):
+    _check(lib().moe_v41_token_logprobs(ctypes.byref(cfg), _p(logits), m, ld, _p(allowed), ld_allowed, _p(target),
+                                        _p(logprob), _p(rank), _p(lse), _p(entropy), _p(top_logprob), _p(top_id),
+                                        _s(stream)), "moe_v41_token_logprobs")

@@ -1,0 +1,88 @@
+// Parameter blocks and launchers of the operators around the MoE layer
+// (include/moe_v41_ops.h), shared by their kernels and the C entry points.
+#pragma once
+
+#include "../../include/moe_v41_ops.h"
+#include "common.cuh"
+
+namespace moe {
+
+struct Q4Params {
+  int m, n, k, group, ng;    // ng = ceil(k / group)
+  int x_type, scale_type, out_type;
+  const uint16_t* x;
+  long long ldx;
+  const uint8_t* w;          // [n][k / 2]
+  const uint16_t* scales;    // [n][ng]
+  const uint8_t* zeros;      // [n][ng] or NULL
+  void* out;
+  long long ldo;
+};
+
+struct NormParams {
+  moe_v41_norm_cfg c;
+  int m;
+  const void *y, *post_w, *post_b, *gate, *h, *pre_w, *pre_b;
+  void *h_out, *x_out;
+  long long ldy, ldg, ldh, ldh_out, ldx;
+};
+
+struct LogprobParams {
+  moe_v41_logprob_cfg c;
+  int m;
+  const void* logits;
+  long long ld;
+  const uint32_t* allowed;
+  long long ld_allowed;
+  const int* target;
+  float* logprob;
+  int* rank;
+  float* lse;
+  float* entropy;
+  float* top_logprob;
+  int* top_id;
+};
+
+int launch_q4_linear(const Q4Params& p, void* ws, cudaStream_t s);
+size_t q4_workspace_bytes(const moe_v41_q4_cfg& c);
+int launch_block_norm(const NormParams& p, cudaStream_t s);
+int launch_token_logprobs(const LogprobParams& p, cudaStream_t s);
+
+__host__ __device__ inline int type_bytes(int t) { return t == MOE_T_F32 ? 4 : 2; }
+
+// One element of a tensor of type T (MOE_T_*) as f32, and back with one
+// rounding to nearest.
+template <int T>
+struct Elem;
+template <>
+struct Elem<MOE_T_F32> {
+  using type = float;
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <>
+struct Elem<MOE_T_BF16> {
+  using type = __nv_bfloat16;
+  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<MOE_T_F16> {
+  using type = __half;
+  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+};
+
+// The same with the type known at run time only.
+__device__ __forceinline__ float load_elem(const void* p, long long i, int t) {
+  if (t == MOE_T_F32) return static_cast<const float*>(p)[i];
+  if (t == MOE_T_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void store_elem(void* p, long long i, int t, float v) {
+  if (t == MOE_T_F32) static_cast<float*>(p)[i] = v;
+  else if (t == MOE_T_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+}  // namespace moe
