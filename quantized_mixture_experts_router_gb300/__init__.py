@@ -136,10 +136,27 @@ def _p(t):
     return t.data_ptr()
 
 
+_raw = None
+
+
+def _current_stream() -> int:
+    """torch's current stream as an address; without the stream object that
+    torch.cuda.current_stream() builds, which costs as much as a launch"""
+    global _raw
+    if _raw is None:
+        import torch
+        torch.cuda.init()
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if get is None:
+            _raw = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            _raw = lambda: get(torch.cuda.current_device())  # noqa: E731
+    return _raw()
+
+
 def _s(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -50,6 +50,28 @@ int launch_token_logprobs(const LogprobParams& p, cudaStream_t s);
 
 __host__ __device__ inline int type_bytes(int t) { return t == MOE_T_F32 ? 4 : 2; }
 
+// Programmatic dependent launch: the next kernel of the stream may be set up
+// from here on; and the wait for everything the stream ran before.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch of a kernel that calls grid_wait() before it touches global memory:
+// its blocks may be set up while the stream's previous kernel ends.
+template <class P>
+int launch_overlapped(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const P& p) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = grid;
+  lc.blockDim = block;
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 // One element of a tensor of type T (MOE_T_*) as f32, and back with one
 // rounding to nearest.
 template <int T>
