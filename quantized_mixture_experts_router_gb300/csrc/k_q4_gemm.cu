@@ -1,0 +1,551 @@
+// Products with 4-bit weights and group scales for many tokens, as a
+// persistent tcgen05 kernel over tiles of 128 weight rows x up to 256 tokens:
+//   out[t, r] = sum_groups s[r, j] sum_{k in j} (q[r, k] - z[r, j]) x[t, k]
+//
+//   A  q - z, exact in bf16 and fp16, written by the dequantising warps into
+//      tensor memory (lane = row), so that shared memory carries B alone.
+//   B  x as it is, by TMA (128-byte swizzle), 128 k a stage.
+// A group's products accumulate into a fresh tensor-memory accumulator; the
+// epilogue warps drain it, multiply by the row's f32 scale and add it to
+// running sums in registers.  So no weight is rounded and the scale costs one
+// FMA per group and output.  Two accumulators of 128 tokens alternate: a tile
+// of more than 128 tokens is two halves that share each A stage, one drained
+// while the tensor cores fill the other.
+//
+// x, at 256 tokens a tile, is the larger operand by far (a weight has four
+// bits): a cluster of two blocks takes consecutive row tiles of the same
+// tokens, each block loads its half of the tile's x and multicasts it to both.
+//
+// The running sums of 128 outputs per thread need more registers than an even
+// split of the register file: the warpgroups trade them (setmaxnreg).
+#include <cudaTypedefs.h>
+
+#include "internal.h"
+#include "ops.h"
+#include "tc.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int TM = 128;            // weight rows per tile
+constexpr int TN = 256;            // tokens per tile, at most
+constexpr int HALF = 128;          // tokens per accumulator
+constexpr int KC = 128;            // k per stage
+constexpr int KS = 64;             // k per swizzled 128-byte row: a stage of B is two such tiles
+constexpr int BBOX = 64;           // tokens per B copy
+constexpr uint32_t B_HALF = TN * KS * 2;
+constexpr uint32_t B_STAGE = 2 * B_HALF;
+constexpr uint32_t RAW_STAGE = TM * KC / 2;
+constexpr int NS = 3;              // stages of the A and B rings, which move together
+constexpr int NSR = 4;             // raw stages
+constexpr uint32_t A_COL0 = 2 * HALF;      // tensor-memory columns of the A ring, 64 a stage
+constexpr int NEW = 8;             // epilogue warps 0-7: tokens 0-63 (0-3) and 64-127 (4-7) of each half
+constexpr int NDW = 8;             // dequantising warps 8-15: the first (8-11) and second 64 k (12-15) of a stage
+constexpr int W_TMA = 16, W_MMA = 17, W_RAW = 18;
+constexpr int NTHR = 640;
+// Registers per thread: 96 at launch; the shares add up to the launch's total.
+constexpr int REG_LAUNCH = 96, REG_EPI = 176, REG_DEQ = 40, REG_REST = 48;
+static_assert(256 * REG_EPI + 256 * REG_DEQ + 128 * REG_REST <= NTHR * REG_LAUNCH, "register shares exceed the launch's");
+
+struct Q4GemmArgs {
+  CUtensorMap map_w;               // w as bytes [n][k / 2], box {64 bytes, 128 rows}
+  CUtensorMap map_x;               // x [m][k], box {64 values, 64 rows}
+  Q4Params p;
+  int tn;                          // tokens per tile: 64, 128 or 256
+  int cl;                          // blocks per cluster: consecutive row tiles, the same tokens
+  int nt, tiles;                   // token tiles; tiles of cl row tiles x one token tile
+  unsigned* status;
+  unsigned long long timeout_ns;
+};
+
+struct GemmCtl {
+  unsigned long long full[NS];    // a stage's A and B are there
+  unsigned long long empty[NS];   // every block of the cluster is done with them
+  unsigned long long r_full[NSR], r_empty[NSR];
+  unsigned long long acc_full[2], acc_empty[2];
+  unsigned long long done;
+  uint32_t tmem;
+  uint32_t abort;
+};
+
+constexpr uint32_t SMEM_BYTES = 1024 + NS * B_STAGE + NSR * RAW_STAGE + ((sizeof(GemmCtl) + 15) & ~15u);
+static_assert(SMEM_BYTES <= 232448, "stages exceed the shared memory of a block");
+
+__device__ __forceinline__ uint64_t* bp(unsigned long long& b) { return reinterpret_cast<uint64_t*>(&b); }
+
+// Bounded wait of one thread; on a timeout the block's abort flag is set and
+// every later wait of the block returns false at once.
+struct Waiter {
+  GemmCtl& C;
+  uint64_t deadline;
+  unsigned* status;
+  __device__ __forceinline__ bool one(unsigned long long& bar, uint32_t parity) const {
+    if (mbar_try_wait(bp(bar), parity)) return true;
+    if (*reinterpret_cast<volatile uint32_t*>(&C.abort)) return false;
+    if (mbar_wait_bounded(bp(bar), parity, deadline, status)) return true;
+    *reinterpret_cast<volatile uint32_t*>(&C.abort) = 1u;
+    return false;
+  }
+  __device__ __forceinline__ bool warp(unsigned long long& bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, one(bar, parity));
+  }
+};
+
+__device__ __forceinline__ void warp_arrive(unsigned long long& b) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bp(b));
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// tma_load_2d into the same place of every block in `mask`, completing on each one's barrier.
+__device__ __forceinline__ void tma_load_2d_multi(uint32_t dst, const void* map, int x, int y, uint64_t* bar,
+                                                  uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(mask)
+      : "memory");
+}
+
+// umma_commit on the same barrier of every block in `mask`.
+__device__ __forceinline__ void umma_commit_multi(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(mask)
+      : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
+struct Tile {
+  int row0, tok0, n;  // n: tokens, rounded up to 16; rows past the end compute zeros
+};
+__device__ __forceinline__ Tile tile_of(const Q4GemmArgs& a, int t) {
+  Tile T;
+  const int mt = t / a.nt, nt = t - mt * a.nt;  // neighbouring clusters share weight rows
+  T.row0 = (mt * a.cl + (int)cluster_rank()) * TM;
+  T.tok0 = nt * a.tn;
+  T.n = (min(a.tn, a.p.m - T.tok0) + 15) & ~15;
+  return T;
+}
+
+// ------------------------------------------------------------ TMA issuers
+__device__ void run_raw(const Q4GemmArgs& a, GemmCtl& C, uint32_t raw_smem, const Waiter& wt) {
+  const int chunks = (a.p.k + KC - 1) / KC;
+  uint32_t u = 0;
+  for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
+    const Tile T = tile_of(a, t);
+    for (int c = 0; c < chunks; ++c, ++u) {
+      const uint32_t st = u % NSR;
+      if (u >= NSR && !wt.one(C.r_empty[st], (u / NSR - 1) & 1u)) goto out;
+      mbar_arrive_expect_tx(bp(C.r_full[st]), RAW_STAGE);
+      tma_load_2d(raw_smem + st * RAW_STAGE, &a.map_w, c * (KC / 2), T.row0, bp(C.r_full[st]));
+    }
+  }
+out:
+  // copies still in flight land before the block can exit
+  const uint64_t d2 = globaltimer_ns() + a.timeout_ns;
+  for (uint32_t v = u > NSR ? u - NSR : 0u; v < u; ++v)
+    mbar_wait_bounded(bp(C.r_full[v % NSR]), (v / NSR) & 1u, d2, a.status);
+}
+
+// A and B stage j of the ring holds chunks j, j + NS, ... of every tile, so that
+// the roles' loops unroll to fixed stages; `par` holds a stage's phase in bit j.
+__device__ void run_x(const Q4GemmArgs& a, GemmCtl& C, uint32_t b_smem, const Waiter& wt) {
+  const int chunks = (a.p.k + KC - 1) / KC, rank = (int)cluster_rank();
+  const uint16_t mask = (uint16_t)((1u << a.cl) - 1u);
+  uint32_t par = 0, used = 0;
+  for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
+    const Tile T = tile_of(a, t);
+    const int nbox = (T.n + BBOX - 1) / BBOX;
+    uint32_t st = 0;
+    for (int c = 0; c < chunks; ++c) {
+      if (!wt.one(C.empty[st], ((par >> st) & 1u) ^ 1u)) goto out;  // passes at once the first time
+      mbar_arrive_expect_tx(bp(C.full[st]), (uint32_t)nbox * BBOX * KC * 2);
+      for (int r = rank; r < 2 * nbox; r += a.cl) {  // (tokens 64 (r / 2) .., k 64 (r % 2) ..)
+        const uint32_t dst = b_smem + st * B_STAGE + (uint32_t)(r & 1) * B_HALF + (uint32_t)(r >> 1) * (BBOX * 128);
+        const int x = c * KC + (r & 1) * KS, y = T.tok0 + (r >> 1) * BBOX;
+        if (a.cl > 1) tma_load_2d_multi(dst, &a.map_x, x, y, bp(C.full[st]), mask);
+        else tma_load_2d(dst, &a.map_x, x, y, bp(C.full[st]));
+      }
+      par ^= 1u << st;
+      used |= 1u << st;
+      st = st + 1 == NS ? 0 : st + 1;
+    }
+  }
+out:
+  const uint64_t d2 = globaltimer_ns() + a.timeout_ns;
+  for (uint32_t st = 0; st < NS; ++st) {
+    if (!((used >> st) & 1u)) continue;
+    mbar_wait_bounded(bp(C.full[st]), ((par >> st) & 1u) ^ 1u, d2, a.status);
+    // and so do the other blocks' commits to this one's barriers
+    if (!*reinterpret_cast<volatile uint32_t*>(&C.abort))
+      mbar_wait_bounded(bp(C.empty[st]), ((par >> st) & 1u) ^ 1u, d2, a.status);
+  }
+}
+
+// ------------------------------------------------------------ MMA issuer
+// The whole warp walks the loop, so that addresses and descriptors are uniform
+// values, and one elected thread issues.  The instructions of this warp per
+// MMA bound the kernel: a round of NS chunks is unrolled, with fixed stages
+// and offsets.  Accumulator of a use: its half (two halves), or the use's
+// lowest bit (one).
+template <bool BF, int G, int NH>
+__device__ __forceinline__ bool mma_tile(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, uint64_t bdesc0,
+                                         const Waiter& wt, int n, int chunks, uint16_t mask, uint32_t& full_par,
+                                         uint32_t& acc_par) {
+  constexpr int GPC = KC / G;        // groups per chunk
+  constexpr int STEPS = G / 16;      // MMA steps of a group
+  const uint32_t id0 = umma_idesc(min(n, HALF), BF), id1 = umma_idesc(NH == 2 ? n - HALF : 16, BF);
+  const int last_groups = (a.p.k - (chunks - 1) * KC + G - 1) / G;  // groups of the last chunk
+#pragma unroll 1
+  for (int c0 = 0; c0 < chunks; c0 += NS) {
+    asm volatile("" : "+l"(bdesc0), "+r"(tmem));  // offsets are added in place, not kept in registers over the loop
+#pragma unroll
+    for (int st = 0; st < NS; ++st) {
+      if (c0 + st >= chunks) break;
+      const int groups = c0 + st == chunks - 1 ? last_groups : GPC;
+#pragma unroll
+      for (int gi = 0; gi < GPC; ++gi) {
+        if (GPC > 1 && gi >= groups) break;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const int reg = NH == 2 ? h : (GPC == 1 ? (c0 + st) & 1 : gi & 1);
+          if (h == 0 && gi == 0 && !wt.warp(C.full[st], (full_par >> st) & 1u)) return false;
+          if (!wt.warp(C.acc_empty[reg], ((acc_par >> reg) & 1u) ^ 1u)) return false;
+          acc_par ^= 1u << reg;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t d = tmem + reg * HALF, id = h ? id1 : id0;
+            // k past the end of the row meets zeros of x (the copies fill them in)
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+              const int step = gi * STEPS + i;
+              umma_f16_ta(d, tmem + A_COL0 + st * 64 + step * 8,
+                          bdesc0 + (uint64_t)((st * B_STAGE + (step / 4) * B_HALF + h * HALF * 128) >> 4) +
+                              2u * (step % 4),
+                          id, i > 0);
+            }
+            umma_commit(bp(C.acc_full[reg]));
+            if (h == NH - 1 && (GPC == 1 || gi + 1 == groups)) {  // the stage is free once these are done
+              if (a.cl > 1) umma_commit_multi(bp(C.empty[st]), mask);
+              else umma_commit(bp(C.empty[st]));
+            }
+          }
+        }
+      }
+      full_par ^= 1u << st;
+    }
+  }
+  return true;
+}
+
+template <bool BF, int G>
+__device__ void run_mma(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, uint32_t b_smem, const Waiter& wt) {
+  const int chunks = (a.p.k + KC - 1) / KC;
+  const uint64_t bdesc0 = umma_desc(b_smem);
+  const uint16_t mask = (uint16_t)((1u << a.cl) - 1u);
+  uint32_t full_par = 0, acc_par = 0;
+  for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
+    const Tile T = tile_of(a, t);
+    const bool ok = T.n > HALF ? mma_tile<BF, G, 2>(a, C, tmem, bdesc0, wt, T.n, chunks, mask, full_par, acc_par)
+                               : mma_tile<BF, G, 1>(a, C, tmem, bdesc0, wt, T.n, chunks, mask, full_par, acc_par);
+    if (!ok) break;
+  }
+  __syncwarp();
+  if (elect_one()) umma_commit(bp(C.done));  // after every MMA this thread issued
+}
+
+// --------------------------------------------------------- dequantisers
+__device__ __forceinline__ uint32_t h2_sub(uint32_t v, uint32_t z, bool bf) {
+  if (bf) {
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), *reinterpret_cast<__nv_bfloat162*>(&z));
+    return *reinterpret_cast<const uint32_t*>(&d);
+  }
+  const __half2 d = __hsub2(*reinterpret_cast<__half2*>(&v), *reinterpret_cast<__half2*>(&z));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// Eight codes of a word as four pairs (k, k + 1) of q - z: the code in the
+// mantissa of 128 (bf16) or 1024 (fp16), whose unit step holds it, minus
+// zz = that base + z in both halves.
+template <bool BF>
+__device__ __forceinline__ void expand8(uint32_t w, uint32_t zz, uint32_t* o) {
+  constexpr uint32_t BASE = BF ? 0x43434343u : 0x64646464u;
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+  const uint32_t a = __byte_perm(lo, hi, 0x5140u), b = __byte_perm(lo, hi, 0x7362u);  // codes 0-3, 4-7 in order
+  o[0] = h2_sub(__byte_perm(a, BASE, 0x4140u), zz, BF);
+  o[1] = h2_sub(__byte_perm(a, BASE, 0x4342u), zz, BF);
+  o[2] = h2_sub(__byte_perm(b, BASE, 0x4140u), zz, BF);
+  o[3] = h2_sub(__byte_perm(b, BASE, 0x4342u), zz, BF);
+}
+
+// Warps 8-11 write the first 64 k of every stage, warps 12-15 the second;
+// thread = weight row.
+template <bool BF>
+__device__ void run_dequant(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, const uint8_t* raw, const Waiter& wt) {
+  const Q4Params& p = a.p;
+  const int w = (threadIdx.x >> 5) - NEW, lane = threadIdx.x & 31;
+  const int hi = w >> 2, quarter = w & 3, r = quarter * 32 + lane;
+  const int chunks = (p.k + KC - 1) / KC;
+  const uint32_t base = BF ? 0x43004300u : 0x64006400u;
+  const uint32_t acol = tmem + ((uint32_t)(quarter * 32) << 16) + A_COL0 + (uint32_t)hi * 32u;
+  uint32_t ru = 0, par = 0;  // raw stages walked; phases of the A stages
+  for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
+    const Tile T = tile_of(a, t);
+    const uint8_t* zrow = p.zeros && T.row0 + r < p.n ? p.zeros + (size_t)(T.row0 + r) * p.ng : nullptr;
+    uint32_t as = 0;
+    for (int c = 0; c < chunks; ++c, ++ru) {
+      const uint32_t rs = ru % NSR;
+      uint32_t zz[2];  // 32 k each: one group at most
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int k = c * KC + hi * KS + 32 * j;
+        zz[j] = base + (p.zeros ? (zrow && k < p.k ? (uint32_t)__ldg(zrow + k / p.group) : 0u) : 8u) * 0x00010001u;
+      }
+      if (!wt.warp(C.r_full[rs], (ru / NSR) & 1u)) return;
+      // 64-byte rows, 16-byte piece j of row r at j ^ (r / 2 % 4)
+      const uint8_t* row = raw + rs * RAW_STAGE + r * 64;
+      uint4 v[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) v[j] = *reinterpret_cast<const uint4*>(row + (((2 * hi + j) ^ ((r >> 1) & 3)) << 4));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bp(C.r_empty[rs]));
+      if (!wt.warp(C.empty[as], ((par >> as) & 1u) ^ 1u)) return;
+      par ^= 1u << as;
+      tc_fence_after();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t o[16];
+        expand8<BF>(v[j].x, zz[j], o);
+        expand8<BF>(v[j].y, zz[j], o + 4);
+        expand8<BF>(v[j].z, zz[j], o + 8);
+        expand8<BF>(v[j].w, zz[j], o + 12);
+        tmem_st8(acol + as * 64 + j * 16, o);
+        tmem_st8(acol + as * 64 + j * 16 + 8, o + 8);
+      }
+      tmem_wait_st();
+      warp_arrive(C.full[as]);
+      as = as + 1 == NS ? 0 : as + 1;
+    }
+  }
+}
+
+// ------------------------------------------------------------- epilogue
+// 32 consecutive columns of the warp's lanes; complete after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// R[p] += s * accumulator column col + p for this warp's 64 columns, if it has
+// any (columns past the tile's tokens hold leftovers, and are never stored);
+// the accumulator is handed back as soon as it has been read.
+__device__ __forceinline__ void drain(uint32_t col, int np, float s, float (&R)[64], unsigned long long& empty) {
+  if (np > 0) {
+    uint32_t v[32];
+    tmem_ld32(col, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) R[j] = fmaf(s, __uint_as_float(v[j]), R[j]);
+    tmem_ld32(col + 32u, v);
+    tmem_wait_ld();
+    warp_arrive(empty);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) R[32 + j] = fmaf(s, __uint_as_float(v[j]), R[32 + j]);
+  } else {
+    warp_arrive(empty);
+  }
+}
+
+__device__ __forceinline__ void store_cols(const Q4Params& p, int row, int tok0, int np, const float (&R)[64]) {
+#pragma unroll
+  for (int j = 0; j < 64; ++j)
+    if (j < np && tok0 + j < p.m && row < p.n) store_elem(p.out, (tok0 + j) * p.ldo + row, p.out_type, R[j]);
+}
+
+__device__ void run_epilogue(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, const Waiter& wt) {
+  const Q4Params& p = a.p;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int set = w >> 2, quarter = w & 3;
+  const uint32_t col = tmem + ((uint32_t)(quarter * 32) << 16) + 64u * set;
+  uint32_t par = 0;  // phases of the two accumulators
+  for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
+    const Tile T = tile_of(a, t);
+    const int row = T.row0 + quarter * 32 + lane;
+    const uint16_t* srow = p.scales + (size_t)min(row, p.n - 1) * p.ng;
+    const int np0 = min(64, min(T.n, HALF) - 64 * set), np1 = min(64, T.n - HALF - 64 * set);  // <= 0: none
+    float R0[64], R1[64];
+#pragma unroll
+    for (int j = 0; j < 64; ++j) R0[j] = R1[j] = 0.f;
+    uint32_t next = __ldg(srow);
+    for (int g = 0; g < p.ng; ++g) {
+      const float s = p.scale_type == MOE_T_BF16 ? __uint_as_float(next << 16) : half_bits_to_float(next);
+      if (g + 1 < p.ng) next = __ldg(srow + g + 1);
+      const uint32_t r0 = T.n > HALF ? 0u : (uint32_t)g & 1u;  // as the MMA issuer picks them
+      if (!wt.warp(C.acc_full[r0], (par >> r0) & 1u)) return;
+      par ^= 1u << r0;
+      tc_fence_after();
+      drain(col + r0 * HALF, np0, s, R0, C.acc_empty[r0]);
+      if (T.n > HALF) {
+        if (!wt.warp(C.acc_full[1], (par >> 1) & 1u)) return;
+        par ^= 2u;
+        tc_fence_after();
+        drain(col + HALF, np1, s, R1, C.acc_empty[1]);
+      }
+    }
+    store_cols(p, row, T.tok0 + 64 * set, np0, R0);
+    if (T.n > HALF) store_cols(p, row, T.tok0 + HALF + 64 * set, np1, R1);
+  }
+}
+
+// ---------------------------------------------------------------- kernel
+template <bool BF, int G>
+__global__ void __launch_bounds__(NTHR, 1) k_q4_gemm(const __grid_constant__ Q4GemmArgs a) {
+  extern __shared__ __align__(1024) uint8_t raw_smem[];
+  uint8_t* sm = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+  uint8_t* raw = sm + NS * B_STAGE;
+  GemmCtl& C = *reinterpret_cast<GemmCtl*>(raw + NSR * RAW_STAGE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bp(C.full[i]), 1 + NDW);  // the copy of x and the warps that write A
+      mbar_init(bp(C.empty[i]), (uint32_t)a.cl);
+    }
+    for (int i = 0; i < NSR; ++i) {
+      mbar_init(bp(C.r_full[i]), 1);
+      mbar_init(bp(C.r_empty[i]), NDW);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bp(C.acc_full[i]), 1);
+      mbar_init(bp(C.acc_empty[i]), NEW);
+    }
+    mbar_init(bp(C.done), 1);
+    C.abort = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(&C.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // every block's barriers are ready for the others' copies and commits
+  tc_fence_after();
+  const uint32_t tmem = C.tmem;
+  const uint32_t b_smem = smem_u32(sm), r_smem = smem_u32(raw);
+  grid_wait();
+  const Waiter wt{C, globaltimer_ns() + a.timeout_ns, a.status};
+
+  if (warp < NEW) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_EPI));
+    run_epilogue(a, C, tmem, wt);
+  } else if (warp < NEW + NDW) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_DEQ));
+    run_dequant<BF>(a, C, tmem, raw, wt);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_REST));
+    if (warp == W_MMA) run_mma<BF, G>(a, C, tmem, b_smem, wt);
+    else if (warp == W_TMA && lane == 0) run_x(a, C, b_smem, wt);
+    else if (warp == W_RAW && lane == 0) run_raw(a, C, r_smem, wt);
+  }
+  __syncwarp();
+  // no MMA may still be writing tensor memory when it is freed: the issuer's
+  // final commit follows its last MMA (bounded wait, a fresh deadline)
+  if (warp == 0 && lane == 0) mbar_wait_bounded(bp(C.done), 0u, globaltimer_ns() + a.timeout_ns, a.status);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no other block still copies into this one's memory or commits to its barriers
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool BF, int G>
+int launch_gemm(Q4GemmArgs& a, int mt, int sms, cudaStream_t s) {
+  static int attr_dev = -1, pairs = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (attr_dev != dev) {
+    // the register trade needs the launch to hold what the shares add up to
+    cudaFuncAttributes fa{};
+    if (cudaFuncGetAttributes(&fa, k_q4_gemm<BF, G>) != cudaSuccess || fa.numRegs != REG_LAUNCH) return MOE_ERR_CUDA;
+    if (cudaFuncSetAttribute(k_q4_gemm<BF, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) !=
+        cudaSuccess)
+      return MOE_ERR_CUDA;
+    // clusters of two that the GPU holds at once
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3((unsigned)(sms / 2 * 2));
+    lc.blockDim = dim3(NTHR);
+    lc.dynamicSmemBytes = SMEM_BYTES;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&pairs, k_q4_gemm<BF, G>, &lc) != cudaSuccess) return MOE_ERR_CUDA;
+    attr_dev = dev;
+  }
+  const int fit = a.cl == 2 ? pairs : sms;
+  a.tiles = (mt + a.cl - 1) / a.cl * a.nt;
+  const int grid = (a.tiles < fit ? a.tiles : fit) * a.cl;
+  if (grid < 1) return MOE_ERR_CUDA;
+  return launch_overlapped(k_q4_gemm<BF, G>, dim3((unsigned)grid), dim3(NTHR), SMEM_BYTES, s, a, a.cl);
+}
+
+}  // namespace
+
+int launch_q4_gemm(const Q4Params& p, unsigned* status, int sms, cudaStream_t s) {
+  Q4GemmArgs a{};
+  if (!make_map_2d(&a.map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, (uint64_t)p.k / 2, (uint64_t)p.n, (uint64_t)p.k / 2,
+                   KC / 2, TM, 64) ||
+      !make_map_2d(&a.map_x, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.x, (uint64_t)p.k, (uint64_t)p.m, (uint64_t)p.ldx * 2, KS,
+                   BBOX, 128))
+    return MOE_ERR_CUDA;
+  a.p = p;
+  a.status = status;
+  a.timeout_ns = 2000000000ull;
+  const int mt = (p.n + TM - 1) / TM;
+  // The widest tile reads and expands each weight row least often, but leaves
+  // SMs idle when there are few tiles.  A chunk costs about as much beside its
+  // MMAs as the MMAs of 256 tokens do, whatever the width.
+  long long best = -1;
+  for (int tn = TN; tn >= 64; tn /= 2) {
+    const int nt = (p.m + tn - 1) / tn;
+    const long long cost = (((long long)mt * nt + sms - 1) / sms) * (tn + 256);
+    if (best < 0 || cost < best) {
+      best = cost;
+      a.tn = tn;
+      a.nt = nt;
+    }
+  }
+  a.cl = mt * a.nt <= sms ? 1 : 2;
+  const bool bf = p.x_type == MOE_T_BF16;
+  if (p.group == 128) return bf ? launch_gemm<true, 128>(a, mt, sms, s) : launch_gemm<false, 128>(a, mt, sms, s);
+  if (p.group == 64) return bf ? launch_gemm<true, 64>(a, mt, sms, s) : launch_gemm<false, 64>(a, mt, sms, s);
+  return bf ? launch_gemm<true, 32>(a, mt, sms, s) : launch_gemm<false, 32>(a, mt, sms, s);
+}
+
+}  // namespace moe

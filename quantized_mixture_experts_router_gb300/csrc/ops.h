@@ -2,6 +2,8 @@
 // (include/moe_v41_ops.h), shared by their kernels and the C entry points.
 #pragma once
 
+#include <cudaTypedefs.h>
+
 #include "../../include/moe_v41_ops.h"
 #include "common.cuh"
 
@@ -43,6 +45,14 @@ struct LogprobParams {
   int* top_id;
 };
 
+// A tensor map of a row-major matrix [rows][cols] with `pitch` bytes from row to
+// row, read in boxes of box_cols x box_rows with the swizzle of box rows of
+// `swizzle` bytes (64 or 128); what lies outside reads zero.
+bool make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t cols, uint64_t rows,
+                 uint64_t pitch, uint32_t box_cols, uint32_t box_rows, int swizzle);
+
+// Many tokens (k_q4_gemm.cu).
+int launch_q4_gemm(const Q4Params& p, unsigned* status, int sms, cudaStream_t s);
 int launch_q4_linear(const Q4Params& p, void* ws, cudaStream_t s);
 size_t q4_workspace_bytes(const moe_v41_q4_cfg& c);
 int launch_block_norm(const NormParams& p, cudaStream_t s);
@@ -58,8 +68,9 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 // Launch of a kernel that calls grid_wait() before it touches global memory:
 // its blocks may be set up while the stream's previous kernel ends.
 template <class P>
-int launch_overlapped(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const P& p) {
-  cudaLaunchAttribute at[1];
+int launch_overlapped(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const P& p,
+                      int cluster = 1) {
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc{};
@@ -67,8 +78,11 @@ int launch_overlapped(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cud
   lc.blockDim = block;
   lc.dynamicSmemBytes = smem;
   lc.stream = s;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   lc.attrs = at;
-  lc.numAttrs = 1;
+  lc.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&lc, kernel, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
