@@ -106,14 +106,14 @@ MOE_API int moe_v41_block_norm(const moe_v41_norm_cfg* cfg, int m, const void* y
  *    rank of a NaN target is 1 + the number of allowed entries that are
  *    numbers). */
 typedef struct {
-  int32_t vocab;       /* 1..2^30 */
+  int32_t vocab;       /* 1..2^28 */
   int32_t logit_type;  /* MOE_T_* */
   int32_t top_k;       /* 0..32 */
   float temperature;   /* > 0, finite */
 } moe_v41_logprob_cfg;
 
 /* logits [m, vocab] (pitch ld, aligned to the element), allowed u32
- * [m, ceil(vocab/32)] (pitch ld_allowed) or NULL, target i32 [m].  Each of
+ * [m, ceil(vocab/32)] (pitch ld_allowed) or NULL, target i32 [m], m <= 2^30.  Each of
  * logprob f32 [m], rank i32 [m], lse f32 [m], entropy f32 [m] may be NULL
  * (target too, when neither logprob nor rank is asked for); top_logprob f32
  * [m, top_k] and top_id i32 [m, top_k] are needed when top_k > 0. */

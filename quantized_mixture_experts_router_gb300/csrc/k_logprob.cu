@@ -6,25 +6,31 @@
 // large common offsets cost no digits).
 //
 // Bound by one read of the logits: everything comes from a single pass.
-//  - A row belongs to a cluster of 1..16 blocks (more when there are few
-//    rows), a contiguous slice each; their results meet in distributed shared
-//    memory.
-//  - Bulk copies bring batches of 32 KB into two buffers of shared memory while
-//    the threads work on the other one, so that the loads in flight cost no
-//    registers.  (Units of eight entries that the row begins or ends inside are
-//    read entry by entry.)
-//  - A thread keeps M, S, U of its own; S and U are packed pairs of f32 (two
-//    sums an instruction).  The entry-wise work beside the sums hides behind
-//    one comparison of the unit's maximum with min(M, the target's logit, the
-//    selection threshold).
+//  - A row belongs to a cluster of 1..16 blocks (the fewer rows the more), a
+//    contiguous slice each, whose results meet in distributed shared memory; a
+//    cluster walks through several rows when there are many.
+//  - Each warp streams its own 2 KB pieces of the slice with bulk copies into a
+//    ring of its own, across the ends of rows, so that the loads in flight cost
+//    no registers and warps meet twice a row only.  (Units of eight entries that
+//    the row begins or ends inside are read entry by entry.)
+//  - A thread keeps S and U of its own, around a reference that moves only when
+//    an entry exceeds it by a factor of 2^8 (the first unit's maximum at first),
+//    so that a warp hardly ever diverges to rescale them; they are packed pairs
+//    of f32 (two sums an instruction).  The entry-wise work beside the sums
+//    hides behind one comparison of the unit's maximum with min(reference + 8
+//    bits, the target's logit, the selection threshold).
 //  - Top entries: each key (value, then lower id) is a 64-bit number.  The
-//    k-th largest of the threads' maxima of the first batch bounds the k-th
-//    largest key from below; the few entries that reach the bound go to a
-//    buffer in shared memory, of which warps sort the best 32.  A batch that
-//    overflows the buffer (rows in ascending order) raises the bound to the
-//    k-th largest of what fitted and is taken again.
+//    threads' maxima so far are distinct entries, so with w warps the least of
+//    the warps' ceil(k / w)-th largest ones bounds the k-th largest key from
+//    below; the few entries that reach the bound go to a buffer in shared
+//    memory, and their places in order are counted at the end of the row (the
+//    bound is renewed after 1, 2, 4, 8 .. pieces).  When
+//    the buffer overflows (a row in ascending order), the k-th largest of what
+//    it holds is a better bound, and the slice is gone through again.
 // Sums follow the fixed order of threads, warps and blocks; the buffer's order
 // varies, its sorted content does not.
+#include <type_traits>
+
 #include "ops.h"
 #include "select.cuh"
 
@@ -34,10 +40,15 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 256;
+constexpr int BLOCKS_PER_SM = 4;
 constexpr int WARPS = THREADS / 32;
-constexpr int CAP = 2048;             // keys of the candidate buffer
+constexpr int CAP = 768;              // keys of the candidate buffer
 constexpr int MAX_CLUSTER = 16;
+constexpr int STAGES = 2;             // pieces of a warp's ring
+constexpr uint32_t PIECE_BYTES = 2048;
+constexpr uint32_t RING_BYTES = WARPS * STAGES * PIECE_BYTES;
+constexpr uint64_t TIMEOUT_NS = 2000000000ull;  // of one wait for a copy
 constexpr float LOWEST = -3.4028234663852886e38f;
 constexpr float FAR = -1.0e30f;       // a difference whose exponential is zero, but whose product with it is not NaN
 
@@ -62,27 +73,23 @@ __device__ __forceinline__ float ex2(float x) {
   return d;
 }
 
-// Two f32 in one register pair.
-__device__ __forceinline__ u64 pack(float a, float b) {
-  u64 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void unpack(u64 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-  u64 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-  u64 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-  u64 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float min3(float a, float b, float c) { return fminf(fminf(a, b), c); }
+
+// S += e, U += e d with e = exp2(d k), d = x - M, for eight entries; CLAMP: an
+// infinite d counts as FAR (the product with its e = 0 is 0 then, not NaN).
+template <bool CLAMP>
+__device__ __forceinline__ void add_unit(const float (&x)[8], float M, float k, float2& S, float2& U) {
+  const float2 nm = make_float2(-M, -M), kk = make_float2(k, k);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    float2 d = __fadd2_rn(make_float2(x[e], x[e + 1]), nm);
+    if (CLAMP) d = make_float2(max_nan(d.x, FAR), max_nan(d.y, FAR));
+    const float2 h = __fmul2_rn(d, kk);
+    const float2 w = make_float2(ex2(h.x), ex2(h.y));
+    S = __fadd2_rn(S, w);
+    U = __ffma2_rn(w, d, U);
+  }
 }
 
 // The running statistics of a set of entries.
@@ -133,19 +140,30 @@ __device__ __forceinline__ u64 warp_merge(u64 a, u64 b) {
   return v;
 }
 
-constexpr uint32_t BATCH_BYTES = 32768;
 template <int T>
-constexpr int BATCH_UNITS = BATCH_BYTES / (8 * (T == MOE_T_F32 ? 4 : 2));
+constexpr int PIECE_UNITS = PIECE_BYTES / (8 * (T == MOE_T_F32 ? 4 : 2));
 
-struct Shared {
-  u64 full[2];               // a batch has landed
-  unsigned failed;           // a wait ran out: the row's results are NaN
-  int pushed[3];             // keys pushed in a batch, by batch number mod 3
-  u64 buf[CAP];
-  u64 lists[WARPS][32];
-  u64 best[32];              // the block's list, read by the cluster's first block
+// f32 as an unsigned number of the same order (0 for "none").
+__device__ __forceinline__ unsigned ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// What one row leaves in shared memory; two rows' worth alternate.
+struct RowState {
+  alignas(16) u64 buf[CAP];
+  u64 best[32];              // the block's list, descending
   Stat stat[WARPS];
   Stat total;                // the block's, read by the cluster's first block
+  unsigned bound[WARPS];     // ordered bits of each warp's bound
+  int n;                     // keys pushed (counted past CAP)
+};
+
+struct Shared {
+  u64 full[WARPS][STAGES];   // a piece has landed
+  u64 lists[WARPS][32];
+  RowState row[2];
+  unsigned failed;           // a wait ran out: the results are NaN
 };
 
 // The 32 largest of n keys (n >= 0) by the whole block, in lists[0],
@@ -201,15 +219,19 @@ struct RowView {
   // the units that lie wholly inside the row
   __device__ __forceinline__ int inner_begin() const { return off ? 1 : 0; }
   __device__ __forceinline__ int inner_end() const { return (off + V) / 8; }
+  __device__ __forceinline__ Unit<T> inner(const uint8_t* at) const {
+    Unit<T> r;
+#pragma unroll
+    for (int i = 0; i < Unit<T>::NV; ++i) r.v[i] = reinterpret_cast<const uint4*>(at)[i];
+    r.ok = 0xFFu;
+    return r;
+  }
   // unit u; `at`: its place in shared memory, for inner units
   __device__ __forceinline__ Unit<T> load(int u, const uint8_t* at) const {
     Unit<T> r;
     const int j0 = 8 * u - off;
     if (j0 >= 0 && j0 + 8 <= V) {
-      const uint4* q = reinterpret_cast<const uint4*>(at);
-#pragma unroll
-      for (int i = 0; i < Unit<T>::NV; ++i) r.v[i] = q[i];
-      r.ok = 0xFFu;
+      r = inner(at);
       if (MASK) {  // bits j0 .. j0 + 7, of one word or two
         const int w = j0 >> 5, s = j0 & 31;
         const uint32_t lo = __ldg(bits + w), hi = s > 24 ? __ldg(bits + w + 1) : 0u;
@@ -255,209 +277,11 @@ __device__ __forceinline__ const P* in_block(const P* p, uint32_t rank) {
 
 struct LogprobArgs {
   LogprobParams p;
-  int cl;      // blocks per row
+  int cl, cl_log2;  // blocks per row, a power of two
 };
 
-template <int T, bool MASK>
-__global__ void __launch_bounds__(THREADS, 2) k_token_logprobs(const LogprobArgs a) {
-  extern __shared__ __align__(128) uint8_t batches[];  // two of BATCH_BYTES
-  __shared__ Shared sh;
-  const LogprobParams& p = a.p;
-  constexpr int BU = BATCH_UNITS<T>, B = BU / THREADS;
-  constexpr uint32_t UB = BATCH_BYTES / BU;  // bytes of a unit
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int K = p.c.top_k;
-  const long long r = (long long)blockIdx.x / a.cl;
-  const uint32_t rank = a.cl > 1 ? cluster_rank() : 0u;
-  grid_launch_dependents();
-  const RowView<T, MASK> row(p, r);
-  const int units = row.units(), in0 = row.inner_begin(), in1 = row.inner_end();
-  const int u0 = (int)((long long)units * rank / a.cl), u1 = (int)((long long)units * (rank + 1) / a.cl);
-  const int nb = (u1 - u0 + BU - 1) / BU;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sh.full);
-  auto inner = [&](int b, int& lo, int& hi) {  // the inner units of batch b
-    lo = max(u0 + b * BU, in0);
-    hi = min(min(u0 + (b + 1) * BU, u1), in1);
-  };
-  auto fetch = [&](int b) {  // one thread
-    int lo, hi;
-    inner(b, lo, hi);
-    if (b >= nb || lo >= hi) return;
-    const uint32_t bytes = (uint32_t)(hi - lo) * UB;
-    mbar_arrive_expect_tx(full + (b & 1), bytes);
-    bulk_g2s(batches + (uint32_t)(b & 1) * BATCH_BYTES + (uint32_t)(lo - u0 - b * BU) * UB,
-             row.row + (8ll * lo - row.off), bytes, full + (b & 1));
-  };
-  if (tid == 0) {
-    mbar_init(full, 1);
-    mbar_init(full + 1, 1);
-    fence_mbar_init();
-    sh.failed = 0u;
-    sh.pushed[0] = sh.pushed[1] = sh.pushed[2] = 0;
-  }
-  grid_wait();
-  if (tid == 0) {
-    fetch(0);
-    fetch(1);
-  }
-  const uint64_t deadline = globaltimer_ns() + 2000000000ull;
-  const int t = p.target ? p.target[r] : -1;
-  const bool scored = t >= 0 && t < row.V;
-  const float rt = 1.0f / p.c.temperature;
-  const float k = 1.4426950408889634f * rt;
-  const u64 k2 = pack(k, k);
-  // the target's logit; +inf (nothing is above it) where no rank is asked for
-  float xt = -pos_inf();
-  if (scored && row.allowed(t)) xt = Elem<T>::get(row.row[t]);
-  const float xr = scored && p.rank ? xt : pos_inf();
-  __syncthreads();
-
-  float M = LOWEST;
-  u64 S2 = pack(0.f, 0.f), U2 = S2;
-  int above = 0, n = 0;  // n: keys in the buffer
-  u64 thr = 0;           // keys below it are not among the top k
-  float tf = K > 0 ? -pos_inf() : pos_inf();
-  for (int b = 0; b < nb; ++b) {
-    const int b0 = u0 + b * BU;
-    const uint8_t* batch = batches + (uint32_t)(b & 1) * BATCH_BYTES;
-    {
-      int lo, hi;
-      inner(b, lo, hi);
-      if (lo < hi && !mbar_try_wait(full + (b & 1), (uint32_t)(b >> 1) & 1u))
-        mbar_wait_bounded(full + (b & 1), (uint32_t)(b >> 1) & 1u, deadline, &sh.failed);
-    }
-    if (b == 0 && K > 0) {
-      // a first lower bound of the k-th largest key: that of the threads' maxima
-      u64 best = 0;
-#pragma unroll 1
-      for (int i = 0; i < B; ++i) {
-        const int u = b0 + i * THREADS + tid;
-        if (u >= u1) break;
-        const Unit<T> c = row.load(u, batch + (uint32_t)(i * THREADS + tid) * UB);
-        float x[8];
-        c.to_f32(x);
-        float m = -pos_inf();
-        int at = -1;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (((c.ok >> e) & 1u) && x[e] >= m && (at < 0 || x[e] > m)) {
-            m = x[e];
-            at = e;
-          }
-        if (at >= 0) {
-          const u64 key = rank_key(m, 8 * u - row.off + at);
-          best = key > best ? key : best;
-        }
-      }
-      sh.buf[tid] = best;
-      __syncthreads();
-      block_top(sh, sh.buf, THREADS);
-      thr = sh.lists[0][K - 1];
-      tf = thr >> 32 ? key_value(thr) : -pos_inf();
-      __syncthreads();
-    }
-    // a unit whose maximum stays below `lim` adds to the sums alone
-    float lim = fminf(M, fminf(tf, xr));
-    uint32_t again = 0;  // units with candidates for the top
-#pragma unroll 1
-    for (int i = 0; i < B; ++i) {
-      const int u = b0 + i * THREADS + tid;
-      if (u >= u1) break;
-      const Unit<T> c = row.load(u, batch + (uint32_t)(i * THREADS + tid) * UB);
-      float x[8];
-      c.to_f32(x);
-      if (c.ok != 0xFFu) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = (c.ok >> e) & 1u ? x[e] : -pos_inf();
-      }
-      const float mv = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      if (mv >= lim || thr >> 32 == 0) {
-        if (mv > M) {
-          const float d = fmaxf(M - mv, FAR), e = ex2(d * k);
-          U2 = mul2(fma2(S2, pack(d, d), U2), pack(e, e));
-          S2 = mul2(S2, pack(e, e));
-          M = mv;
-          lim = fminf(M, fminf(tf, xr));
-        }
-        if (mv > xr) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) above += x[e] > xr;
-        }
-        if (K > 0 && (mv >= tf || thr >> 32 == 0)) again |= 1u << i;
-      }
-      const u64 nm = pack(-M, -M);
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        float d0, d1, a0, a1;
-        unpack(add2(pack(x[e], x[e + 1]), nm), d0, d1);
-        const u64 d = pack(max_nan(d0, FAR), max_nan(d1, FAR));
-        unpack(mul2(d, k2), a0, a1);
-        const u64 ee = pack(ex2(a0), ex2(a1));
-        S2 = add2(S2, ee);
-        U2 = fma2(ee, d, U2);
-      }
-    }
-    if (K > 0) {
-      if (tid == 0) sh.pushed[(b + 1) % 3] = 0;  // last read two barriers ago
-      int* pushed = &sh.pushed[b % 3];
-      for (;;) {
-        for (uint32_t left = again; left; left &= left - 1) {
-          const int i = __ffs(left) - 1;
-          const int u = b0 + i * THREADS + tid;
-          const Unit<T> c = row.load(u, batch + (uint32_t)(i * THREADS + tid) * UB);
-          float x[8];
-          c.to_f32(x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (!((c.ok >> e) & 1u) || x[e] < tf) continue;
-            const u64 key = rank_key(x[e], 8 * u - row.off + e);
-            if (key < thr) continue;
-            const int at = n + atomicAdd(pushed, 1);
-            if (at < CAP) sh.buf[at] = key;
-          }
-        }
-        __syncthreads();
-        const int now = n + *pushed;
-        if (now <= CAP / 2) {
-          n = now;
-          break;
-        }
-        // the buffer fills up: raise the bound; keep the best, or, where keys
-        // were lost, the bound alone, and take the batch again
-        block_top(sh, sh.buf, min(now, CAP));
-        thr = sh.lists[0][K - 1];
-        tf = thr >> 32 ? key_value(thr) : -pos_inf();
-        if (now <= CAP) {
-          if (tid < 32) sh.buf[tid] = sh.lists[0][tid];
-          n = 32;
-        }
-        if (tid == 0) *pushed = 0;
-        __syncthreads();
-        if (now <= CAP) break;
-      }
-    } else {
-      __syncthreads();
-    }
-    if (tid == 0) fetch(b + 2);  // every thread is done with this batch
-  }
-
-  if (sh.failed && tid == 0) {  // the copies in flight land before the block leaves
-    const uint64_t d2 = globaltimer_ns() + 2000000000ull;
-    for (int b = max(0, nb - 2); b < nb; ++b) {
-      int lo, hi;
-      inner(b, lo, hi);
-      if (lo < hi) mbar_wait_bounded(full + (b & 1), (uint32_t)(b >> 1) & 1u, d2, &sh.failed);
-    }
-  }
-
-  // the block's statistics and list
-  Stat st;
-  {
-    float s0, s1, v0, v1;
-    unpack(S2, s0, s1);
-    unpack(U2, v0, v1);
-    st = Stat{M, s0 + s1, v0 + v1, above};
-  }
+__device__ __forceinline__ Stat warp_join(Stat st, float k) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     Stat w;
@@ -465,141 +289,422 @@ __global__ void __launch_bounds__(THREADS, 2) k_token_logprobs(const LogprobArgs
     w.S = __shfl_xor_sync(0xffffffffu, st.S, o);
     w.U = __shfl_xor_sync(0xffffffffu, st.U, o);
     w.above = __shfl_xor_sync(0xffffffffu, st.above, o);
-    // the same order on both sides
-    st = (lane & o) ? join(w, st, k) : join(st, w, k);
+    st = (lane & o) ? join(w, st, k) : join(st, w, k);  // the same order on both sides
   }
-  if (lane == 0) sh.stat[warp] = st;
-  __syncwarp();
-  if (K > 0) {
-    block_top(sh, sh.buf, n);
-    if (tid < 32) sh.best[tid] = sh.lists[0][tid];
+  return st;
+}
+
+// The slice of a row that a block reads, in pieces of PIECE_UNITS that its
+// warps take in turn.
+template <int T, bool MASK>
+struct Slice {
+  RowView<T, MASK> row;
+  int u0, u1, np;
+  __device__ __forceinline__ Slice(const LogprobArgs& a, long long r, uint32_t rank) : row(a.p, r) {
+    const int units = row.units();
+    u0 = (int)(((long long)units * rank) >> a.cl_log2);
+    u1 = (int)(((long long)units * (rank + 1)) >> a.cl_log2);
+    np = (u1 - u0 + PIECE_UNITS<T> - 1) / PIECE_UNITS<T>;
   }
-  // a NaN target ranks below every number: count those
-  if (scored && p.rank && xt != xt) {
-    int c = 0;
-    for (int j = 8 * u0 - row.off + tid; j < 8 * u1 - row.off; j += THREADS) {
-      if (j < 0 || j >= row.V || !row.allowed(j)) continue;
-      const float x = Elem<T>::get(row.row[j]);
-      c += x == x;
-    }
-    atomicAdd(&sh.stat[warp].above, c);  // lane 0's zero so far: no entry is above a NaN
+};
+
+// Where a warp's copies stand: pieces of the rows its block walks through, as
+// byte offsets from the 16-byte aligned address at or below a row's start.
+struct Cursor {
+  const uint8_t* base;
+  uint32_t at, lo, hi, end;  // the next piece; the inner units; the slice's end
+};
+
+template <int T, bool MASK>
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const LogprobArgs a) {
+  extern __shared__ __align__(128) uint8_t rings[];
+  __shared__ Shared sh;
+  const LogprobParams& p = a.p;
+  constexpr int PU = PIECE_UNITS<T>, B = PU / 32;
+  constexpr uint32_t UB = PIECE_BYTES / PU;  // bytes of a unit
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int K = p.c.top_k;
+  const uint32_t rank = a.cl > 1 ? cluster_rank() : 0u;
+  const int step = (int)gridDim.x / a.cl, r0 = (int)blockIdx.x / a.cl;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sh.full[warp]);
+  uint8_t* ring = rings + warp * STAGES * PIECE_BYTES;
+  grid_launch_dependents();
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(full + i, 1);
+    fence_mbar_init();
+  }
+  if (tid == 0) {
+    sh.failed = 0u;
+    sh.row[0].n = sh.row[1].n = 0;
   }
   __syncthreads();
-  if (warp == 0) {
-    st = sh.stat[lane < WARPS ? lane : 0];
-    if (lane >= WARPS) st = Stat{LOWEST, 0.f, 0.f, 0};
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      Stat w;
-      w.M = __shfl_xor_sync(0xffffffffu, st.M, o);
-      w.S = __shfl_xor_sync(0xffffffffu, st.S, o);
-      w.U = __shfl_xor_sync(0xffffffffu, st.U, o);
-      w.above = __shfl_xor_sync(0xffffffffu, st.above, o);
-      st = (lane & o) ? join(w, st, k) : join(st, w, k);
+  grid_wait();
+  // lane 0 copies STAGES pieces ahead, of row fr next
+  int fr = r0 - step;
+  Cursor cu{nullptr, 0u, 0u, 0u, 0u};
+  uint32_t fetched = 0;
+  auto fetch_next = [&]() {
+    while (cu.at >= cu.end) {  // this row has no more for the warp
+      fr += step;
+      if (fr >= p.m) {
+        fr -= step;
+        return;
+      }
+      const Slice<T, MASK> s(a, fr, rank);
+      cu.base = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(s.row.row) & ~uintptr_t(15));
+      cu.at = (uint32_t)s.u0 * UB + (uint32_t)warp * PIECE_BYTES;
+      cu.end = (uint32_t)s.u1 * UB;
+      cu.lo = (uint32_t)s.row.inner_begin() * UB;
+      cu.hi = min(cu.end, (uint32_t)s.row.inner_end() * UB);
     }
-    if (sh.failed) st.S = __uint_as_float(0x7FC00000u);
-    if (lane == 0) sh.total = st;
-  }
-  if (a.cl > 1) {
-    cluster_sync();
-    if (rank == 0) {
-      if (warp == 0) {
-        st = lane < a.cl ? *in_block(&sh.total, (uint32_t)lane) : Stat{LOWEST, 0.f, 0.f, 0};
+    const uint32_t st = fetched % STAGES;
+    const uint32_t lo = max(cu.at, cu.lo), hi = min(cu.at + PIECE_BYTES, cu.hi);
+    if (lo < hi) {
+      mbar_arrive_expect_tx(full + st, hi - lo);
+      bulk_g2s(ring + st * PIECE_BYTES + (lo - cu.at), cu.base + lo, hi - lo, full + st);
+    } else {
+      mbar_arrive(full + st);  // nothing but units the row begins or ends inside
+    }
+    ++fetched;
+    cu.at += WARPS * PIECE_BYTES;
+  };
+  if (lane == 0)
+    for (int i = 0; i < STAGES; ++i) fetch_next();
+  const float rt = 1.0f / p.c.temperature;
+  const float k = 1.4426950408889634f * rt;
+  const float slack = 8.0f / k;
+
+  uint32_t used = 0;  // pieces so far
+  int parity = 0;
+  for (int r = r0; r < p.m; r += step, parity ^= 1) {
+    RowState& rs = sh.row[parity];
+    const Slice<T, MASK> sl(a, r, rank);
+    const RowView<T, MASK>& row = sl.row;
+    const int u0 = sl.u0, u1 = sl.u1;
+    const int t = p.target ? p.target[r] : -1;
+    const bool scored = t >= 0 && t < row.V;
+    // the target's logit; +inf (nothing is above it) where no rank is asked for
+    float xt = -pos_inf();
+    if (scored && row.allowed(t)) xt = Elem<T>::get(row.row[t]);
+    const float xr = scored && p.rank ? xt : pos_inf();
+    const int busy = min(WARPS, sl.np);      // warps with pieces of this row
+    const int nth = (K + busy - 1) / max(busy, 1);
+
+    float M = LOWEST;       // the largest entry so far
+    float ref = LOWEST;     // S and U are sums around it,
+    float ref_hi = LOWEST;  // and it moves when an entry lies above this
+    float2 S2 = make_float2(0.f, 0.f), U2 = S2;
+    int above = 0;
+    u64 thr = 0;            // keys below it are not among the top k
+    float tf = pos_inf();   // their value, +inf while there is none
+    // this warp's bound: its nth largest thread maximum
+    auto publish = [&]() {
+      unsigned o = M > LOWEST ? ordered(M) : 0u, m = __reduce_max_sync(0xffffffffu, o);
+      for (int i = 1; i < nth; ++i) {
+        const unsigned at = __ballot_sync(0xffffffffu, o == m);
+        if (lane == __ffs(at) - 1) o = 0u;
+        m = __reduce_max_sync(0xffffffffu, o);
+      }
+      if (lane == 0) *reinterpret_cast<volatile unsigned*>(&rs.bound[warp]) = m;
+    };
+    auto raise = [&]() {
+      const unsigned m = __reduce_min_sync(
+          0xffffffffu, lane < busy ? *reinterpret_cast<volatile unsigned*>(&rs.bound[lane]) : 0xFFFFFFFFu);
+      if ((u64)m << 32 > thr) {
+        thr = (u64)m << 32;
+        tf = key_value(thr);
+      }
+    };
+    // the allowed entries of a unit from `from` on join the candidates
+    auto push = [&](const float (&x)[8], uint32_t ok, int u, const uint8_t* at, float from) {
+      uint32_t left = 0;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          Stat w;
-          w.M = __shfl_xor_sync(0xffffffffu, st.M, o);
-          w.S = __shfl_xor_sync(0xffffffffu, st.S, o);
-          w.U = __shfl_xor_sync(0xffffffffu, st.U, o);
-          w.above = __shfl_xor_sync(0xffffffffu, st.above, o);
-          st = (lane & o) ? join(w, st, k) : join(st, w, k);
+      for (int e = 0; e < 8; ++e) left |= (x[e] < from ? 0u : 1u) << e;
+      for (left &= ok; left; left &= left - 1) {
+        const int e = __ffs(left) - 1, j = 8 * u - row.off + e;
+        const float v = at ? Elem<T>::get(reinterpret_cast<const typename Elem<T>::type*>(at)[e])
+                           : Elem<T>::get(row.row[j]);
+        const u64 key = rank_key(v, j);
+        if (key < thr) continue;
+        const int to = atomicAdd(&rs.n, 1);
+        if (to < CAP) rs.buf[to] = key;
+      }
+    };
+    // piece `count` of the warp; FIRST: before any bound is known
+    auto piece = [&](int i0, auto first) {
+      constexpr bool FIRST = decltype(first)::value;
+      const int b0 = u0 + i0 * PU;
+      const uint32_t st = used % STAGES;
+      const uint8_t* mem = ring + st * PIECE_BYTES + lane * UB;
+      if (!mbar_try_wait(full + st, (used / STAGES) & 1u))
+        mbar_wait_for(full + st, (used / STAGES) & 1u, TIMEOUT_NS, &sh.failed);
+      // a unit whose maximum stays below `lim` adds to the sums alone
+      float lim = fminf(ref_hi, fminf(tf, xr));
+      auto work = [&](const float (&x)[8], uint32_t ok, int u, const uint8_t* at) {
+        const float mv = max3(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]), x[0]);
+        const float lo = min3(min3(min3(x[0], x[1], x[2]), x[3], x[4]), min3(x[5], x[6], x[7]), x[0]);
+        M = fmaxf(M, mv);
+        if (mv >= lim) {
+          if (mv > ref_hi) {
+            const float d = fmaxf(ref - mv, FAR), e = ex2(d * k);
+            U2 = make_float2((U2.x + S2.x * d) * e, (U2.y + S2.y * d) * e);
+            S2 = make_float2(S2.x * e, S2.y * e);
+            ref = mv;
+            ref_hi = mv + slack;
+            lim = fminf(ref_hi, fminf(tf, xr));
+          }
+          if (mv > xr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) above += x[e] > xr;
+          }
+          if (!FIRST && mv >= tf) push(x, ok, u, at, tf);
+        }
+        if (lo > FAR && ref < -FAR) add_unit<false>(x, ref, k, S2, U2);
+        else add_unit<true>(x, ref, k, S2, U2);
+      };
+      const bool plain = !MASK && b0 >= row.inner_begin() && b0 + PU <= min(u1, row.inner_end());  // whole units alone
+      if (plain) {
+#pragma unroll 2
+        for (int i = 0; i < B; ++i) {
+          float x[8];
+          row.inner(mem + (uint32_t)i * (32 * UB)).to_f32(x);
+          work(x, 0xFFu, b0 + i * 32 + lane, mem + (uint32_t)i * (32 * UB));
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < B; ++i) {
+          const int u = b0 + i * 32 + lane;
+          if (u >= u1) break;
+          const Unit<T> c = row.load(u, mem + (uint32_t)i * (32 * UB));
+          float x[8];
+          c.to_f32(x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = (c.ok >> e) & 1u ? x[e] : -pos_inf();
+          work(x, c.ok, u, nullptr);
         }
       }
+      __syncwarp();
+    };
+    // every entry from the bound on, of a piece already summed
+    auto push_all = [&](int i0) {
+      const uint8_t* mem = ring + (used % STAGES) * PIECE_BYTES + lane * UB;
+#pragma unroll 1
+      for (int i = 0; i < B; ++i) {
+        const int u = u0 + i0 * PU + i * 32 + lane;
+        if (u >= u1) break;
+        const Unit<T> c = row.load(u, mem + (uint32_t)i * (32 * UB));
+        float x[8];
+        c.to_f32(x);
+        push(x, c.ok, u, nullptr, thr ? tf : -pos_inf());
+      }
+    };
+    auto next = [&]() {  // the warp is done with its piece
+      __syncwarp();
+      if (lane == 0) fetch_next();
+      ++used;
+    };
+    const bool have = warp < sl.np;
+    if (have) piece(warp, std::true_type());
+    if (K > 0) {
+      publish();
+      __syncthreads();
+      raise();
+      if (have && (M >= tf || thr == 0)) push_all(warp);
+    }
+    if (have) next();
+    int count = 1;
+    for (int i0 = warp + WARPS; i0 < sl.np; i0 += WARPS) {
+      piece(i0, std::false_type());
       if (K > 0) {
-        u64 v = warp < a.cl ? in_block(sh.best, (uint32_t)warp)[lane] : 0;
-        sh.lists[warp][lane] = v;
-        for (int s = MAX_CLUSTER / 2; s; s >>= 1) {
-          __syncthreads();
-          if (warp < s) {
-            v = warp_merge(v, sh.lists[warp + s][lane]);
-            sh.lists[warp][lane] = v;
-          }
+        if (thr == 0) push_all(i0);  // no bound: everything is a candidate, NaN included
+        if ((++count & (count - 1)) == 0) {
+          publish();
+          raise();
+        }
+      }
+      next();
+    }
+
+    // the block's statistics and list
+    {
+      Stat st{M, S2.x + S2.y, U2.x + U2.y, above};
+      const float d = max_nan(ref - M, FAR), e = ex2(d * k);
+      st.U = (st.U + st.S * d) * e;
+      st.S *= e;
+      st = warp_join(st, k);
+      if (lane == 0) rs.stat[warp] = st;
+    }
+    // a NaN target ranks below every number: count those
+    if (scored && p.rank && xt != xt) {
+      int c = 0;
+      for (int j = 8 * u0 - row.off + tid; j < 8 * u1 - row.off; j += THREADS) {
+        if (j < 0 || j >= row.V || !row.allowed(j)) continue;
+        const float x = Elem<T>::get(row.row[j]);
+        c += x == x;
+      }
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0) rs.stat[warp].above = c;  // zero so far: no entry is above a NaN
+    }
+    if (K > 0) {
+      if (tid < 32) rs.best[tid] = 0;
+      __syncthreads();
+      int n = rs.n;
+      while (n > CAP) {
+        block_top(sh, rs.buf, CAP);
+        thr = sh.lists[0][K - 1];
+        tf = thr >> 32 ? key_value(thr) : -pos_inf();
+        if (tid == 0) rs.n = 0;
+        __syncthreads();
+        for (int j = max(0, 8 * u0 - row.off) + tid; j < min(row.V, 8 * u1 - row.off); j += THREADS) {
+          if (!row.allowed(j)) continue;
+          const float x = Elem<T>::get(row.row[j]);
+          if (x < tf) continue;
+          const u64 key = rank_key(x, j);
+          if (key < thr) continue;
+          const int at = atomicAdd(&rs.n, 1);
+          if (at < CAP) rs.buf[at] = key;
         }
         __syncthreads();
+        n = rs.n;
+        __syncthreads();
+      }
+      if (n <= THREADS) {  // each key's place is the number of larger ones
+        const u64 key = tid < n ? rs.buf[tid] : 0;
+        if (warp * 32 < n) {
+          int place = 0;
+          for (int j = 0; j + 1 < n; j += 2) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(rs.buf + j);
+            place += (v.x > key) + (v.y > key);
+          }
+          if (n & 1) place += rs.buf[n - 1] > key;
+          if (tid < n && place < 32) rs.best[place] = key;
+        }
+      } else {
+        block_top(sh, rs.buf, n);
+        if (tid < 32) rs.best[tid] = sh.lists[0][tid];
       }
     }
-    cluster_sync();  // no block leaves while its shared memory is read
-    if (rank != 0) return;
+    __syncthreads();
+    Stat st;
+    if (warp == 0) {
+      st = warp_join(lane < WARPS ? rs.stat[lane] : Stat{LOWEST, 0.f, 0.f, 0}, k);
+      if (sh.failed) st.S = __uint_as_float(0x7FC00000u);
+      if (lane == 0) rs.n = 0;  // for the row after the next
+    }
+    if (a.cl > 1) {
+      if (tid == 0) rs.total = st;
+      cluster_sync();
+      if (rank == 0) {
+        if (warp == 0)
+          st = warp_join(lane < a.cl ? *in_block(&rs.total, (uint32_t)lane) : Stat{LOWEST, 0.f, 0.f, 0}, k);
+        if (K > 0) {
+          u64 v = warp < a.cl ? in_block(rs.best, (uint32_t)warp)[lane] : 0;
+          if (warp + WARPS < a.cl) v = warp_merge(v, in_block(rs.best, (uint32_t)(warp + WARPS))[lane]);
+          sh.lists[warp][lane] = v;
+          for (int s = WARPS / 2; s; s >>= 1) {
+            __syncthreads();
+            if (warp < s) {
+              v = warp_merge(v, sh.lists[warp + s][lane]);
+              sh.lists[warp][lane] = v;
+            }
+          }
+          if (warp == 0) rs.best[lane] = v;
+        }
+      }
+      // the others' totals and lists are read before they reach the next row's
+      // cluster_sync, and before they leave
+      if (r + step >= p.m) cluster_sync();
+    }
+    if (rank == 0 && warp == 0) {
+      __syncwarp();
+      const float inf = pos_inf(), nan = __uint_as_float(0x7FC00000u);
+      const bool empty = st.S == 0.f;
+      const float ls = logf(st.S);
+      if (lane == 0) {
+        if (p.lse) p.lse[r] = empty ? -inf : st.M * rt + ls;
+        if (p.entropy) p.entropy[r] = empty ? 0.f : ls - st.U / st.S * rt;
+        if (p.logprob) p.logprob[r] = scored ? (empty ? -inf : (xt - st.M) * rt - ls) : (t == -1 ? 0.f : nan);
+        if (p.rank) p.rank[r] = scored ? st.above + 1 : (t == -1 ? 0 : -1);
+      }
+      if (lane < K) {
+        const u64 key = rs.best[lane];
+        p.top_logprob[(long long)r * K + lane] = key == 0 || empty ? -inf : (key_value(key) - st.M) * rt - ls;
+        p.top_id[(long long)r * K + lane] = key ? key_id(key) : -1;
+      }
+    }
   }
-  if (warp != 0) return;
-  const float inf = pos_inf(), nan = __uint_as_float(0x7FC00000u);
-  const bool empty = st.S == 0.f;
-  const float ls = logf(st.S);
-  if (lane == 0) {
-    if (p.lse) p.lse[r] = empty ? -inf : st.M * rt + ls;
-    if (p.entropy) p.entropy[r] = empty ? 0.f : ls - st.U / st.S * rt;
-    if (p.logprob) p.logprob[r] = scored ? (empty ? -inf : (xt - st.M) * rt - ls) : (t == -1 ? 0.f : nan);
-    if (p.rank) p.rank[r] = scored ? st.above + 1 : (t == -1 ? 0 : -1);
-  }
-  if (lane < K) {
-    const u64 key = sh.lists[0][lane];
-    p.top_logprob[r * K + lane] = key == 0 || empty ? -inf : (key_value(key) - st.M) * rt - ls;
-    p.top_id[r * K + lane] = key ? key_id(key) : -1;
+  if (sh.failed && lane == 0) {  // the copies in flight land before the block leaves
+    const uint64_t d2 = globaltimer_ns() + TIMEOUT_NS;
+    for (uint32_t v = used; v < fetched; ++v)
+      mbar_wait_bounded(full + v % STAGES, (v / STAGES) & 1u, d2, &sh.failed);
   }
 }
 
 template <int T, bool MASK>
-int launch(const LogprobArgs& a, cudaStream_t s) {
+int launch(const LogprobArgs& a, int sms, cudaStream_t s) {
   static int attr_dev = -1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (attr_dev != dev) {
     if (cudaFuncSetAttribute(k_token_logprobs<T, MASK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaFuncSetAttribute(k_token_logprobs<T, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             2 * (int)BATCH_BYTES) != cudaSuccess)
+                             (int)RING_BYTES) != cudaSuccess)
       return MOE_ERR_CUDA;
     attr_dev = dev;
   }
-  return launch_overlapped(k_token_logprobs<T, MASK>, dim3((unsigned)a.p.m * (unsigned)a.cl), dim3(THREADS),
-                           2 * BATCH_BYTES, s, a, a.cl);
+  // four blocks per SM; clusters of more than two blocks leave some SMs out, so
+  // that their number comes from the runtime
+  int clusters = BLOCKS_PER_SM * sms / a.cl;
+  if (a.cl > 2) {
+    static int fit[MAX_CLUSTER + 1] = {}, fit_dev = -1;
+    if (fit_dev != dev) {
+      for (int& f : fit) f = 0;
+      fit_dev = dev;
+    }
+    if (!fit[a.cl]) {
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = (unsigned)a.cl;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t lc{};
+      lc.gridDim = dim3((unsigned)(BLOCKS_PER_SM * sms / a.cl * a.cl));
+      lc.blockDim = dim3(THREADS);
+      lc.dynamicSmemBytes = RING_BYTES;
+      lc.attrs = at;
+      lc.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&fit[a.cl], k_token_logprobs<T, MASK>, &lc) != cudaSuccess || fit[a.cl] < 1)
+        return MOE_ERR_CUDA;
+    }
+    clusters = fit[a.cl];
+  }
+  const int grid = (a.p.m < clusters ? a.p.m : clusters) * a.cl;
+  return launch_overlapped(k_token_logprobs<T, MASK>, dim3((unsigned)grid), dim3(THREADS),
+                           RING_BYTES, s, a, a.cl);
 }
 
 template <int T>
-int launch_m(const LogprobArgs& a, cudaStream_t s) {
-  return a.p.allowed ? launch<T, true>(a, s) : launch<T, false>(a, s);
+int launch_m(const LogprobArgs& a, int sms, cudaStream_t s) {
+  return a.p.allowed ? launch<T, true>(a, sms, s) : launch<T, false>(a, sms, s);
 }
 
 }  // namespace
 
-int launch_token_logprobs(const LogprobParams& p0, cudaStream_t s) {
-  // rows a launch, so that the grid stays below 2^31 blocks
-  constexpr int ROWS = 1 << 26;
-  for (int r0 = 0; r0 < p0.m; r0 += ROWS) {
-    LogprobArgs a{};
-    a.p = p0;
-    LogprobParams& p = a.p;
-    p.m = p0.m - r0 < ROWS ? p0.m - r0 : ROWS;
-    p.logits = static_cast<const char*>(p0.logits) + (size_t)r0 * p0.ld * type_bytes(p0.c.logit_type);
-    if (p.allowed) p.allowed += (size_t)r0 * p0.ld_allowed;
-    if (p.target) p.target += r0;
-    if (p.logprob) p.logprob += r0;
-    if (p.rank) p.rank += r0;
-    if (p.lse) p.lse += r0;
-    if (p.entropy) p.entropy += r0;
-    if (p.top_logprob) p.top_logprob += (size_t)r0 * p0.c.top_k;
-    if (p.top_id) p.top_id += (size_t)r0 * p0.c.top_k;
-    // blocks per row: enough to fill the GPU twice over, while a block's slice
-    // fills its threads
-    const int batch = (int)BATCH_BYTES / type_bytes(p.c.logit_type);
-    a.cl = 1;
-    while (a.cl < MAX_CLUSTER && (long long)p.m * a.cl < 304 && p.c.vocab / (2 * a.cl) >= batch / 2) a.cl *= 2;
-    int rc;
-    if (p.c.logit_type == MOE_T_F32) rc = launch_m<MOE_T_F32>(a, s);
-    else if (p.c.logit_type == MOE_T_BF16) rc = launch_m<MOE_T_BF16>(a, s);
-    else rc = launch_m<MOE_T_F16>(a, s);
-    if (rc) return rc;
-  }
-  return MOE_OK;
+int launch_token_logprobs(const LogprobParams& p, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    return MOE_ERR_CUDA;
+  LogprobArgs a{};
+  a.p = p;
+  // blocks per row: enough to fill the GPU, while a block's slice
+  // has a piece for each of its warps
+  const int piece = (int)PIECE_BYTES / type_bytes(p.c.logit_type);
+  a.cl = 1;
+  while (a.cl < MAX_CLUSTER && (long long)p.m * a.cl < BLOCKS_PER_SM * sms && p.c.vocab / (2 * a.cl) >= WARPS * piece / 2) a.cl *= 2;
+  while ((1 << a.cl_log2) < a.cl) ++a.cl_log2;
+  if (p.c.logit_type == MOE_T_F32) return launch_m<MOE_T_F32>(a, sms, s);
+  if (p.c.logit_type == MOE_T_BF16) return launch_m<MOE_T_BF16>(a, sms, s);
+  return launch_m<MOE_T_F16>(a, sms, s);
 }
 
 }  // namespace moe

@@ -410,7 +410,6 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   if (threadIdx.x == 0) C.bad = 0u;
   __syncthreads();
   grid_wait();
-  const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
   // x first: its few bytes would otherwise queue behind the weights
   copy_x(p, smem_u32(xp));
   auto issue = [&]() {
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
     const int tile1 = wrap ? tile + 1 : tile, b1 = wrap ? 0 : b + 1;
     sat += wrap ? (size_t)(BOX_ROWS * p.ng - b * NGB) : (size_t)NGB;
     if (f + 1 < f1) sc_next.load(p, a.vec, sat, tile1 * BOX_ROWS + g, b1 * NGB);
-    if (!mbar_try_wait(barp + st, phase) && !mbar_wait_bounded(barp + st, phase, deadline, a.status)) ok = false;
+    if (!mbar_try_wait(barp + st, phase) && !mbar_wait_for(barp + st, phase, a.timeout_ns, a.status)) ok = false;
     if (!__all_sync(0xffffffffu, ok)) break;
     const uint32_t buf = ring + (uint32_t)st * BOX_BYTES + alane;
     const uint32_t xb = xlane + (uint32_t)(b * (BOX_K / 32)) * xchunk;

@@ -78,12 +78,12 @@ __device__ __forceinline__ uint64_t* bp(unsigned long long& b) { return reinterp
 // every later wait of the block returns false at once.
 struct Waiter {
   GemmCtl& C;
-  uint64_t deadline;
+  uint64_t timeout_ns;  // of one wait
   unsigned* status;
   __device__ __forceinline__ bool one(unsigned long long& bar, uint32_t parity) const {
     if (mbar_try_wait(bp(bar), parity)) return true;
     if (*reinterpret_cast<volatile uint32_t*>(&C.abort)) return false;
-    if (mbar_wait_bounded(bp(bar), parity, deadline, status)) return true;
+    if (mbar_wait_for(bp(bar), parity, timeout_ns, status)) return true;
     *reinterpret_cast<volatile uint32_t*>(&C.abort) = 1u;
     return false;
   }
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_q4_gemm(const __grid_constant__ Q4G
   const uint32_t tmem = C.tmem;
   const uint32_t b_smem = smem_u32(sm), r_smem = smem_u32(raw);
   grid_wait();
-  const Waiter wt{C, globaltimer_ns() + a.timeout_ns, a.status};
+  const Waiter wt{C, a.timeout_ns, a.status};
 
   if (warp < NEW) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_EPI));

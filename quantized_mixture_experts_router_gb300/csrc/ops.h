@@ -60,6 +60,16 @@ int launch_token_logprobs(const LogprobParams& p, cudaStream_t s);
 
 __host__ __device__ inline int type_bytes(int t) { return t == MOE_T_F32 ? 4 : 2; }
 
+// Wait on an mbarrier phase, at most timeout_ns after its first few tries:
+// false (and the timeout bit in *status) when that ran out.  The timer is read
+// only once a wait is long.
+__device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, uint64_t timeout_ns, unsigned* status) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+  return mbar_wait_bounded(bar, parity, globaltimer_ns() + timeout_ns, status);
+}
+
 // Programmatic dependent launch: the next kernel of the stream may be set up
 // from here on; and the wait for everything the stream ran before.
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

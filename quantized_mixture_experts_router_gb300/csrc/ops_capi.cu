@@ -34,7 +34,7 @@ int check_norm(const moe_v41_norm_cfg* c) {
 
 int check_logprob(const moe_v41_logprob_cfg* c) {
   if (!c) return MOE_ERR_ARG;
-  if (c->vocab < 1 || c->vocab > (1 << 30) || !is_type(c->logit_type)) return MOE_ERR_ARG;
+  if (c->vocab < 1 || c->vocab > (1 << 28) || !is_type(c->logit_type)) return MOE_ERR_ARG;
   if (c->top_k < 0 || c->top_k > 32) return MOE_ERR_ARG;
   if (!(c->temperature > 0.0f) || c->temperature > 3.0e38f) return MOE_ERR_ARG;
   return MOE_OK;
@@ -106,7 +106,7 @@ int moe_v41_token_logprobs(const moe_v41_logprob_cfg* cfg, const void* logits, i
                            void* stream) {
   int rc = check_logprob(cfg);
   if (rc) return rc;
-  if (m < 0) return MOE_ERR_ARG;
+  if (m < 0 || m > (1 << 30)) return MOE_ERR_ARG;
   if (m == 0) return MOE_OK;
   if (!logits || ld < cfg->vocab) return MOE_ERR_ARG;
   if (allowed && ld_allowed < (cfg->vocab + 31) / 32) return MOE_ERR_ARG;
