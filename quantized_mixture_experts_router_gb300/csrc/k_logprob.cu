@@ -5,7 +5,7 @@
 // (differences are taken around M before anything is rounded away, so that
 // large common offsets cost no digits).
 //
-// Bound by one read of the logits: everything comes from a single pass.
+// Bound by one read of the logits.
 //  - A row belongs to a cluster of 1..16 blocks (the fewer rows the more), a
 //    contiguous slice each, whose results meet in distributed shared memory; a
 //    cluster walks through several rows when there are many.
@@ -16,21 +16,18 @@
 //  - A thread keeps S and U of its own, around a reference that moves only when
 //    an entry exceeds it by a factor of 2^8 (the first unit's maximum at first),
 //    so that a warp hardly ever diverges to rescale them; they are packed pairs
-//    of f32 (two sums an instruction).  The entry-wise work beside the sums
-//    hides behind one comparison of the unit's maximum with min(reference + 8
-//    bits, the target's logit, the selection threshold).
-//  - Top entries: each key (value, then lower id) is a 64-bit number.  The
-//    threads' maxima so far are distinct entries, so with w warps the least of
-//    the warps' ceil(k / w)-th largest ones bounds the k-th largest key from
-//    below; the few entries that reach the bound go to a buffer in shared
-//    memory, and their places in order are counted at the end of the row (the
-//    bound is renewed after 1, 2, 4, 8 .. pieces).  When
-//    the buffer overflows (a row in ascending order), the k-th largest of what
-//    it holds is a better bound, and the slice is gone through again.
+//    of f32 (two sums an instruction).  Rank and reference cost one comparison
+//    of the unit's maximum with min(reference + 8 bits, the target's logit).
+//  - Top entries take nothing from the stream but each thread's maximum.  The
+//    maxima are distinct entries, so with w warps the least of the warps'
+//    ceil(k / w)-th largest ones bounds the k-th largest key (value, then lower
+//    id: a 64-bit number) from below, and the top entries belong to the few
+//    threads whose maximum reaches the bound: their units are read again, from
+//    L2, what reaches the bound goes to a buffer, and the places in order are
+//    counted.  Where the buffer overflows (many equal entries), the k-th largest
+//    key of what it holds is a better bound, and the slice is gone through again.
 // Sums follow the fixed order of threads, warps and blocks; the buffer's order
 // varies, its sorted content does not.
-#include <type_traits>
-
 #include "ops.h"
 #include "select.cuh"
 
@@ -92,23 +89,24 @@ __device__ __forceinline__ void add_unit(const float (&x)[8], float M, float k, 
   }
 }
 
+// How many of eight entries are above r (as 1.0 each: set and packed add).
+__device__ __forceinline__ float count_above(const float (&x)[8], float r) {
+  float2 c = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    float2 s;
+    asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(s.x) : "f"(x[e]), "f"(r));
+    asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(s.y) : "f"(x[e + 1]), "f"(r));
+    c = __fadd2_rn(c, s);
+  }
+  return c.x + c.y;
+}
+
 // The running statistics of a set of entries.
 struct Stat {
   float M, S, U;
   int above;
 };
-
-// Two sets' statistics; k: log2(e) / T.
-__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float k) {
-  Stat r;
-  r.M = fmaxf(a.M, b.M);
-  const float da = max_nan(a.M - r.M, FAR), db = max_nan(b.M - r.M, FAR);
-  const float ea = ex2(da * k), eb = ex2(db * k);
-  r.S = a.S * ea + b.S * eb;
-  r.U = (a.U + a.S * da) * ea + (b.U + b.S * db) * eb;
-  r.above = a.above + b.above;
-  return r;
-}
 
 __device__ __forceinline__ u64 shfl_xor_u64(u64 v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
 
@@ -149,6 +147,10 @@ __device__ __forceinline__ unsigned ordered(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ float from_ordered(unsigned o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+
 // What one row leaves in shared memory; two rows' worth alternate.
 struct RowState {
   alignas(16) u64 buf[CAP];
@@ -157,6 +159,8 @@ struct RowState {
   Stat total;                // the block's, read by the cluster's first block
   unsigned bound[WARPS];     // ordered bits of each warp's bound
   int n;                     // keys pushed (counted past CAP)
+  int nhot;
+  uint16_t hot[THREADS];     // threads whose maximum reaches the bound
 };
 
 struct Shared {
@@ -280,17 +284,20 @@ struct LogprobArgs {
   int cl, cl_log2;  // blocks per row, a power of two
 };
 
+// The lanes' statistics joined around the largest M; the sums in a butterfly,
+// whose order is fixed.
 __device__ __forceinline__ Stat warp_join(Stat st, float k) {
-  const int lane = threadIdx.x & 31;
+  const float M = from_ordered(__reduce_max_sync(0xffffffffu, ordered(st.M)));
+  const float d = max_nan(st.M - M, FAR), e = ex2(d * k);
+  st.U = (st.U + st.S * d) * e;
+  st.S *= e;
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
-    Stat w;
-    w.M = __shfl_xor_sync(0xffffffffu, st.M, o);
-    w.S = __shfl_xor_sync(0xffffffffu, st.S, o);
-    w.U = __shfl_xor_sync(0xffffffffu, st.U, o);
-    w.above = __shfl_xor_sync(0xffffffffu, st.above, o);
-    st = (lane & o) ? join(w, st, k) : join(st, w, k);  // the same order on both sides
+    st.S += __shfl_xor_sync(0xffffffffu, st.S, o);
+    st.U += __shfl_xor_sync(0xffffffffu, st.U, o);
   }
+  st.above = (int)__reduce_add_sync(0xffffffffu, (unsigned)st.above);
+  st.M = M;
   return st;
 }
 
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
   }
   if (tid == 0) {
     sh.failed = 0u;
-    sh.row[0].n = sh.row[1].n = 0;
+    sh.row[0].n = sh.row[1].n = sh.row[0].nhot = sh.row[1].nhot = 0;
   }
   __syncthreads();
   grid_wait();
@@ -374,6 +381,14 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
   const float k = 1.4426950408889634f * rt;
   const float slack = 8.0f / k;
 
+  auto target_of = [&](int r) { return p.target && r < p.m ? __ldg(p.target + r) : -1; };
+  auto target_logit = [&](int r, int t) {  // a masked one counts as -inf
+    const RowView<T, MASK> row(p, r);
+    return t >= 0 && t < row.V && row.allowed(t) ? Elem<T>::get(row.row[t]) : -pos_inf();
+  };
+  int t_now = target_of(r0), t_next = target_of(r0 + step);
+  float xt_now = target_logit(r0, t_now);
+
   uint32_t used = 0;  // pieces so far
   int parity = 0;
   for (int r = r0; r < p.m; r += step, parity ^= 1) {
@@ -381,86 +396,47 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
     const Slice<T, MASK> sl(a, r, rank);
     const RowView<T, MASK>& row = sl.row;
     const int u0 = sl.u0, u1 = sl.u1;
-    const int t = p.target ? p.target[r] : -1;
+    const int t = t_now;
     const bool scored = t >= 0 && t < row.V;
-    // the target's logit; +inf (nothing is above it) where no rank is asked for
-    float xt = -pos_inf();
-    if (scored && row.allowed(t)) xt = Elem<T>::get(row.row[t]);
+    const float xt = xt_now;
+    t_now = t_next;  // the next row's, loaded while this one is worked on
+    if (r + step < p.m) xt_now = target_logit(r + step, t_now);
+    t_next = target_of(r + 2 * step);
+    // +inf (nothing is above it) where no rank is asked for
     const float xr = scored && p.rank ? xt : pos_inf();
-    const int busy = min(WARPS, sl.np);      // warps with pieces of this row
-    const int nth = (K + busy - 1) / max(busy, 1);
+    const int busy = max(1, min(WARPS, sl.np));  // warps with pieces of this row
 
     float M = LOWEST;       // the largest entry so far
     float ref = LOWEST;     // S and U are sums around it,
     float ref_hi = LOWEST;  // and it moves when an entry lies above this
     float2 S2 = make_float2(0.f, 0.f), U2 = S2;
-    int above = 0;
-    u64 thr = 0;            // keys below it are not among the top k
-    float tf = pos_inf();   // their value, +inf while there is none
-    // this warp's bound: its nth largest thread maximum
-    auto publish = [&]() {
-      unsigned o = M > LOWEST ? ordered(M) : 0u, m = __reduce_max_sync(0xffffffffu, o);
-      for (int i = 1; i < nth; ++i) {
-        const unsigned at = __ballot_sync(0xffffffffu, o == m);
-        if (lane == __ffs(at) - 1) o = 0u;
-        m = __reduce_max_sync(0xffffffffu, o);
-      }
-      if (lane == 0) *reinterpret_cast<volatile unsigned*>(&rs.bound[warp]) = m;
-    };
-    auto raise = [&]() {
-      const unsigned m = __reduce_min_sync(
-          0xffffffffu, lane < busy ? *reinterpret_cast<volatile unsigned*>(&rs.bound[lane]) : 0xFFFFFFFFu);
-      if ((u64)m << 32 > thr) {
-        thr = (u64)m << 32;
-        tf = key_value(thr);
-      }
-    };
-    // the allowed entries of a unit from `from` on join the candidates
-    auto push = [&](const float (&x)[8], uint32_t ok, int u, const uint8_t* at, float from) {
-      uint32_t left = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) left |= (x[e] < from ? 0u : 1u) << e;
-      for (left &= ok; left; left &= left - 1) {
-        const int e = __ffs(left) - 1, j = 8 * u - row.off + e;
-        const float v = at ? Elem<T>::get(reinterpret_cast<const typename Elem<T>::type*>(at)[e])
-                           : Elem<T>::get(row.row[j]);
-        const u64 key = rank_key(v, j);
-        if (key < thr) continue;
-        const int to = atomicAdd(&rs.n, 1);
-        if (to < CAP) rs.buf[to] = key;
-      }
-    };
-    // piece `count` of the warp; FIRST: before any bound is known
-    auto piece = [&](int i0, auto first) {
-      constexpr bool FIRST = decltype(first)::value;
+    float above = 0.f;      // entries above the target's (at most 2^20 a thread: exact)
+    for (int i0 = warp; i0 < sl.np; i0 += WARPS) {
       const int b0 = u0 + i0 * PU;
       const uint32_t st = used % STAGES;
       const uint8_t* mem = ring + st * PIECE_BYTES + lane * UB;
       if (!mbar_try_wait(full + st, (used / STAGES) & 1u))
         mbar_wait_for(full + st, (used / STAGES) & 1u, TIMEOUT_NS, &sh.failed);
-      // a unit whose maximum stays below `lim` adds to the sums alone
-      float lim = fminf(ref_hi, fminf(tf, xr));
-      auto work = [&](const float (&x)[8], uint32_t ok, int u, const uint8_t* at) {
-        const float mv = max3(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]), x[0]);
-        const float lo = min3(min3(min3(x[0], x[1], x[2]), x[3], x[4]), min3(x[5], x[6], x[7]), x[0]);
+      // where every lane's maximum stays below `lim`, the units add to the
+      // sums alone (the warp decides as one: both ways would cost their sum)
+      float lim = fminf(ref_hi, xr);
+      auto work = [&](const float (&x)[8], unsigned lanes) {
+        const float mv = fmaxf(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]));
+        const float lo = fminf(min3(min3(x[0], x[1], x[2]), x[3], x[4]), min3(x[5], x[6], x[7]));
         M = fmaxf(M, mv);
-        if (mv >= lim) {
+        if (__any_sync(lanes, mv >= lim)) {
           if (mv > ref_hi) {
             const float d = fmaxf(ref - mv, FAR), e = ex2(d * k);
             U2 = make_float2((U2.x + S2.x * d) * e, (U2.y + S2.y * d) * e);
             S2 = make_float2(S2.x * e, S2.y * e);
             ref = mv;
             ref_hi = mv + slack;
-            lim = fminf(ref_hi, fminf(tf, xr));
+            lim = fminf(ref_hi, xr);
           }
-          if (mv > xr) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) above += x[e] > xr;
-          }
-          if (!FIRST && mv >= tf) push(x, ok, u, at, tf);
+          above += count_above(x, xr);
         }
-        if (lo > FAR && ref < -FAR) add_unit<false>(x, ref, k, S2, U2);
-        else add_unit<true>(x, ref, k, S2, U2);
+        if (__any_sync(lanes, lo <= FAR || ref >= -FAR)) add_unit<true>(x, ref, k, S2, U2);
+        else add_unit<false>(x, ref, k, S2, U2);
       };
       const bool plain = !MASK && b0 >= row.inner_begin() && b0 + PU <= min(u1, row.inner_end());  // whole units alone
       if (plain) {
@@ -468,70 +444,33 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
         for (int i = 0; i < B; ++i) {
           float x[8];
           row.inner(mem + (uint32_t)i * (32 * UB)).to_f32(x);
-          work(x, 0xFFu, b0 + i * 32 + lane, mem + (uint32_t)i * (32 * UB));
+          work(x, 0xffffffffu);
         }
       } else {
 #pragma unroll 1
         for (int i = 0; i < B; ++i) {
           const int u = b0 + i * 32 + lane;
-          if (u >= u1) break;
-          const Unit<T> c = row.load(u, mem + (uint32_t)i * (32 * UB));
-          float x[8];
-          c.to_f32(x);
+          const unsigned lanes = __ballot_sync(0xffffffffu, u < u1);
+          if (u < u1) {
+            const Unit<T> c = row.load(u, mem + (uint32_t)i * (32 * UB));
+            float x[8];
+            c.to_f32(x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = (c.ok >> e) & 1u ? x[e] : -pos_inf();
-          work(x, c.ok, u, nullptr);
+            for (int e = 0; e < 8; ++e) x[e] = (c.ok >> e) & 1u ? x[e] : -pos_inf();
+            work(x, lanes);
+          }
+          __syncwarp();
         }
       }
-      __syncwarp();
-    };
-    // every entry from the bound on, of a piece already summed
-    auto push_all = [&](int i0) {
-      const uint8_t* mem = ring + (used % STAGES) * PIECE_BYTES + lane * UB;
-#pragma unroll 1
-      for (int i = 0; i < B; ++i) {
-        const int u = u0 + i0 * PU + i * 32 + lane;
-        if (u >= u1) break;
-        const Unit<T> c = row.load(u, mem + (uint32_t)i * (32 * UB));
-        float x[8];
-        c.to_f32(x);
-        push(x, c.ok, u, nullptr, thr ? tf : -pos_inf());
-      }
-    };
-    auto next = [&]() {  // the warp is done with its piece
-      __syncwarp();
+      __syncwarp();  // the warp is done with this piece
       if (lane == 0) fetch_next();
       ++used;
-    };
-    const bool have = warp < sl.np;
-    if (have) piece(warp, std::true_type());
-    if (K > 0) {
-      publish();
-      __syncthreads();
-      raise();
-      if (have && (M >= tf || thr == 0)) push_all(warp);
-    }
-    if (have) next();
-    int count = 1;
-    for (int i0 = warp + WARPS; i0 < sl.np; i0 += WARPS) {
-      piece(i0, std::false_type());
-      if (K > 0) {
-        if (thr == 0) push_all(i0);  // no bound: everything is a candidate, NaN included
-        if ((++count & (count - 1)) == 0) {
-          publish();
-          raise();
-        }
-      }
-      next();
     }
 
     // the block's statistics and list
     {
-      Stat st{M, S2.x + S2.y, U2.x + U2.y, above};
-      const float d = max_nan(ref - M, FAR), e = ex2(d * k);
-      st.U = (st.U + st.S * d) * e;
-      st.S *= e;
-      st = warp_join(st, k);
+      // (the sums are around ref; a warp's largest ref stands for its M)
+      const Stat st = warp_join(Stat{ref, S2.x + S2.y, U2.x + U2.y, (int)above}, k);
       if (lane == 0) rs.stat[warp] = st;
     }
     // a NaN target ranks below every number: count those
@@ -546,7 +485,45 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
       if (lane == 0) rs.stat[warp].above = c;  // zero so far: no entry is above a NaN
     }
     if (K > 0) {
+      {  // this warp's bound: its nth largest thread maximum
+        const int nth = (K + busy - 1) / busy;
+        unsigned o = M > LOWEST ? ordered(M) : 0u, m = __reduce_max_sync(0xffffffffu, o);
+        for (int i = 1; i < nth; ++i) {
+          const unsigned at = __ballot_sync(0xffffffffu, o == m);
+          if (lane == __ffs(at) - 1) o = 0u;
+          m = __reduce_max_sync(0xffffffffu, o);
+        }
+        if (lane == 0) rs.bound[warp] = m;
+      }
       if (tid < 32) rs.best[tid] = 0;
+      __syncthreads();
+      const unsigned bound = __reduce_min_sync(0xffffffffu, lane < busy ? rs.bound[lane] : 0xFFFFFFFFu);
+      u64 thr = (u64)bound << 32;  // keys below it are not among the top k; 0: no bound, NaN may be among them
+      float tf = bound ? from_ordered(bound) : -pos_inf();
+      if (M >= tf || !bound) rs.hot[atomicAdd(&rs.nhot, 1)] = (uint16_t)tid;
+      __syncthreads();
+      {  // the hot threads' units: (hot thread, unit of its own) over all threads
+        const int upt = (sl.np + WARPS - 1) / WARPS * B, lg = 32 - __clz(upt - 1 > 0 ? upt - 1 : 0);
+        const int items = rs.nhot << (upt > 1 ? lg : 0);
+        for (int q = tid; q < items; q += THREADS) {
+          const int h = rs.hot[upt > 1 ? q >> lg : q], j = upt > 1 ? q & ((1 << lg) - 1) : 0;
+          const int u = u0 + ((h >> 5) + WARPS * (j / B)) * PU + (j % B) * 32 + (h & 31);
+          if (j >= upt || u >= u1) continue;
+          const Unit<T> c = row.load(u, reinterpret_cast<const uint8_t*>(row.row + (8ll * u - row.off)));
+          float x[8];
+          c.to_f32(x);
+          uint32_t left = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) left |= (x[e] < tf ? 0u : 1u) << e;
+          for (left &= c.ok; left; left &= left - 1) {
+            const int e = __ffs(left) - 1, id = 8 * u - row.off + e;
+            const u64 key = rank_key(Elem<T>::get(row.row[id]), id);
+            if (key < thr) continue;
+            const int at = atomicAdd(&rs.n, 1);
+            if (at < CAP) rs.buf[at] = key;
+          }
+        }
+      }
       __syncthreads();
       int n = rs.n;
       while (n > CAP) {
@@ -589,7 +566,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
     if (warp == 0) {
       st = warp_join(lane < WARPS ? rs.stat[lane] : Stat{LOWEST, 0.f, 0.f, 0}, k);
       if (sh.failed) st.S = __uint_as_float(0x7FC00000u);
-      if (lane == 0) rs.n = 0;  // for the row after the next
+      if (lane == 0) rs.n = rs.nhot = 0;  // for the row after the next
     }
     if (a.cl > 1) {
       if (tid == 0) rs.total = st;
@@ -700,7 +677,7 @@ int launch_token_logprobs(const LogprobParams& p, cudaStream_t s) {
   // has a piece for each of its warps
   const int piece = (int)PIECE_BYTES / type_bytes(p.c.logit_type);
   a.cl = 1;
-  while (a.cl < MAX_CLUSTER && (long long)p.m * a.cl < BLOCKS_PER_SM * sms && p.c.vocab / (2 * a.cl) >= WARPS * piece / 2) a.cl *= 2;
+  while (a.cl < MAX_CLUSTER && 2ll * p.m * a.cl <= BLOCKS_PER_SM * sms && p.c.vocab / (2 * a.cl) >= WARPS * piece / 2) a.cl *= 2;
   while ((1 << a.cl_log2) < a.cl) ++a.cl_log2;
   if (p.c.logit_type == MOE_T_F32) return launch_m<MOE_T_F32>(a, sms, s);
   if (p.c.logit_type == MOE_T_BF16) return launch_m<MOE_T_BF16>(a, sms, s);
