@@ -18,14 +18,15 @@
 //    so that a warp hardly ever diverges to rescale them; they are packed pairs
 //    of f32 (two sums an instruction).  Rank and reference cost one comparison
 //    of the unit's maximum with min(reference + 8 bits, the target's logit).
-//  - Top entries take nothing from the stream but each thread's maximum.  The
-//    maxima are distinct entries, so with w warps the least of the warps'
-//    ceil(k / w)-th largest ones bounds the k-th largest key (value, then lower
-//    id: a 64-bit number) from below, and the top entries belong to the few
-//    threads whose maximum reaches the bound: their units are read again, from
-//    L2, what reaches the bound goes to a buffer, and the places in order are
-//    counted.  Where the buffer overflows (many equal entries), the k-th largest
-//    key of what it holds is a better bound, and the slice is gone through again.
+//  - Top entries take nothing from the stream but maxima: each thread's (short
+//    slices), or each piece's (from 64 pieces on).  They are distinct entries,
+//    so with w warps holding a value a lane the least of the warps' ceil(k / w)-th
+//    largest ones bounds the k-th largest key (value, then lower id: a 64-bit
+//    number) from below, and the top entries belong to the few threads or pieces
+//    whose maximum reaches the bound: those are read again, what reaches the
+//    bound goes to a buffer, and the places in order are counted.  Where the
+//    buffer overflows (many equal entries), the k-th largest key of what it holds
+//    is a better bound, and the slice is gone through again.
 // Sums follow the fixed order of threads, warps and blocks; the buffer's order
 // varies, its sorted content does not.
 #include "ops.h"
@@ -42,6 +43,7 @@ constexpr int BLOCKS_PER_SM = 4;
 constexpr int WARPS = THREADS / 32;
 constexpr int CAP = 768;              // keys of the candidate buffer
 constexpr int MAX_CLUSTER = 16;
+constexpr int SEGS = 2 * THREADS;     // piece maxima of a row
 constexpr int STAGES = 2;             // pieces of a warp's ring
 constexpr uint32_t PIECE_BYTES = 2048;
 constexpr uint32_t RING_BYTES = WARPS * STAGES * PIECE_BYTES;
@@ -160,10 +162,21 @@ struct RowState {
   unsigned bound[WARPS];     // ordered bits of each warp's bound
   int n;                     // keys pushed (counted past CAP)
   int nhot;
-  uint16_t hot[THREADS];     // threads whose maximum reaches the bound
+  unsigned seg[SEGS];        // ordered bits of the pieces' maxima, 2^sh pieces each; zero between rows
+  uint16_t hot[SEGS];        // threads or segments whose maximum reaches the bound
+};
+
+// Where a warp's copies stand: pieces of the rows its block walks through, as
+// byte offsets from the 16-byte aligned address at or below a row's start.
+struct Cursor {
+  const uint8_t* base;
+  uint32_t at, lo, hi, end;  // the next piece; the inner units; the slice's end
+  int row;                   // the row of `base`
+  uint32_t fetched;          // pieces so far
 };
 
 struct Shared {
+  Cursor cursor[WARPS];
   u64 full[WARPS][STAGES];   // a piece has landed
   u64 lists[WARPS][32];
   RowState row[2];
@@ -186,6 +199,10 @@ __device__ __forceinline__ void block_top(Shared& sh, const u64* keys, int n) {
   }
   __syncthreads();
 }
+
+// log2 of the pieces of a segment: at most SEGS segments.
+__device__ __forceinline__ int seg_shift(int np) { return max(0, 32 - __clz((np - 1) >> 9)); }
+static_assert(SEGS == 512, "seg_shift");
 
 // Eight entries of the row.
 template <int T>
@@ -315,14 +332,7 @@ struct Slice {
   }
 };
 
-// Where a warp's copies stand: pieces of the rows its block walks through, as
-// byte offsets from the 16-byte aligned address at or below a row's start.
-struct Cursor {
-  const uint8_t* base;
-  uint32_t at, lo, hi, end;  // the next piece; the inner units; the slice's end
-};
-
-template <int T, bool MASK>
+template <int T, bool MASK, bool by_piece>
 __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const LogprobArgs a) {
   extern __shared__ __align__(128) uint8_t rings[];
   __shared__ Shared sh;
@@ -344,39 +354,40 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
     sh.failed = 0u;
     sh.row[0].n = sh.row[1].n = sh.row[0].nhot = sh.row[1].nhot = 0;
   }
+  for (int i = tid; i < SEGS; i += THREADS) sh.row[0].seg[i] = sh.row[1].seg[i] = 0u;
   __syncthreads();
   grid_wait();
-  // lane 0 copies STAGES pieces ahead, of row fr next
-  int fr = r0 - step;
-  Cursor cu{nullptr, 0u, 0u, 0u, 0u};
-  uint32_t fetched = 0;
+  // lane 0 copies STAGES pieces ahead
   auto fetch_next = [&]() {
-    while (cu.at >= cu.end) {  // this row has no more for the warp
-      fr += step;
-      if (fr >= p.m) {
-        fr -= step;
-        return;
-      }
+    Cursor& cu = sh.cursor[warp];
+    uint32_t at = cu.at;
+    while (at >= cu.end) {  // this row has no more for the warp
+      const int fr = cu.row + step;
+      if (fr >= p.m) return;
       const Slice<T, MASK> s(a, fr, rank);
+      cu.row = fr;
       cu.base = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(s.row.row) & ~uintptr_t(15));
-      cu.at = (uint32_t)s.u0 * UB + (uint32_t)warp * PIECE_BYTES;
       cu.end = (uint32_t)s.u1 * UB;
       cu.lo = (uint32_t)s.row.inner_begin() * UB;
       cu.hi = min(cu.end, (uint32_t)s.row.inner_end() * UB);
+      at = (uint32_t)s.u0 * UB + (uint32_t)warp * PIECE_BYTES;
+      cu.at = at;
     }
-    const uint32_t st = fetched % STAGES;
-    const uint32_t lo = max(cu.at, cu.lo), hi = min(cu.at + PIECE_BYTES, cu.hi);
+    const uint32_t st = cu.fetched % STAGES;
+    const uint32_t lo = max(at, cu.lo), hi = min(at + PIECE_BYTES, cu.hi);
     if (lo < hi) {
       mbar_arrive_expect_tx(full + st, hi - lo);
-      bulk_g2s(ring + st * PIECE_BYTES + (lo - cu.at), cu.base + lo, hi - lo, full + st);
+      bulk_g2s(ring + st * PIECE_BYTES + (lo - at), cu.base + lo, hi - lo, full + st);
     } else {
       mbar_arrive(full + st);  // nothing but units the row begins or ends inside
     }
-    ++fetched;
-    cu.at += WARPS * PIECE_BYTES;
+    ++cu.fetched;
+    cu.at = at + WARPS * PIECE_BYTES;
   };
-  if (lane == 0)
+  if (lane == 0) {
+    sh.cursor[warp] = Cursor{nullptr, 0u, 0u, 0u, 0u, r0 - step, 0u};
     for (int i = 0; i < STAGES; ++i) fetch_next();
+  }
   const float rt = 1.0f / p.c.temperature;
   const float k = 1.4426950408889634f * rt;
   const float slack = 8.0f / k;
@@ -404,7 +415,6 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
     t_next = target_of(r + 2 * step);
     // +inf (nothing is above it) where no rank is asked for
     const float xr = scored && p.rank ? xt : pos_inf();
-    const int busy = max(1, min(WARPS, sl.np));  // warps with pieces of this row
 
     float M = LOWEST;       // the largest entry so far
     float ref = LOWEST;     // S and U are sums around it,
@@ -419,11 +429,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
         mbar_wait_for(full + st, (used / STAGES) & 1u, TIMEOUT_NS, &sh.failed);
       // where every lane's maximum stays below `lim`, the units add to the
       // sums alone (the warp decides as one: both ways would cost their sum)
-      float lim = fminf(ref_hi, xr);
+      float lim = fminf(ref_hi, xr), Mp = LOWEST;
       auto work = [&](const float (&x)[8], unsigned lanes) {
         const float mv = fmaxf(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]));
         const float lo = fminf(min3(min3(x[0], x[1], x[2]), x[3], x[4]), min3(x[5], x[6], x[7]));
-        M = fmaxf(M, mv);
+        Mp = fmaxf(Mp, mv);
         if (__any_sync(lanes, mv >= lim)) {
           if (mv > ref_hi) {
             const float d = fmaxf(ref - mv, FAR), e = ex2(d * k);
@@ -462,6 +472,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
           __syncwarp();
         }
       }
+      M = fmaxf(M, Mp);
+      if (by_piece && K > 0) {
+        const int sh_seg = seg_shift(sl.np);
+        const unsigned m = __reduce_max_sync(0xffffffffu, Mp > LOWEST ? ordered(Mp) : 0u);
+        if (lane == 0) atomicMax(&rs.seg[i0 >> sh_seg], m);
+      }
       __syncwarp();  // the warp is done with this piece
       if (lane == 0) fetch_next();
       ++used;
@@ -485,9 +501,17 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
       if (lane == 0) rs.stat[warp].above = c;  // zero so far: no entry is above a NaN
     }
     if (K > 0) {
-      {  // this warp's bound: its nth largest thread maximum
+      const int sh_seg = seg_shift(sl.np);
+      if (by_piece) __syncthreads();  // the segments' maxima are complete
+      // values of distinct entries, one or two a thread; the warp's bound is its
+      // nth largest lane
+      const int nseg = ((sl.np - 1) >> sh_seg) + 1;
+      const unsigned v0 = by_piece ? rs.seg[tid] : (M > LOWEST ? ordered(M) : 0u);
+      const unsigned v1 = by_piece ? rs.seg[tid + THREADS] : 0u;
+      const int busy = by_piece ? min(WARPS, (nseg + 31) >> 5) : max(1, min(WARPS, sl.np));  // warps with values
+      {
         const int nth = (K + busy - 1) / busy;
-        unsigned o = M > LOWEST ? ordered(M) : 0u, m = __reduce_max_sync(0xffffffffu, o);
+        unsigned o = max(v0, v1), m = __reduce_max_sync(0xffffffffu, o);
         for (int i = 1; i < nth; ++i) {
           const unsigned at = __ballot_sync(0xffffffffu, o == m);
           if (lane == __ffs(at) - 1) o = 0u;
@@ -500,28 +524,52 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
       const unsigned bound = __reduce_min_sync(0xffffffffu, lane < busy ? rs.bound[lane] : 0xFFFFFFFFu);
       u64 thr = (u64)bound << 32;  // keys below it are not among the top k; 0: no bound, NaN may be among them
       float tf = bound ? from_ordered(bound) : -pos_inf();
-      if (M >= tf || !bound) rs.hot[atomicAdd(&rs.nhot, 1)] = (uint16_t)tid;
+      const bool live = !by_piece || tid < nseg;
+      if (live && v0 >= bound) rs.hot[atomicAdd(&rs.nhot, 1)] = (uint16_t)tid;
+      if (by_piece) {
+        if (tid + THREADS < nseg && v1 >= bound) rs.hot[atomicAdd(&rs.nhot, 1)] = (uint16_t)(tid + THREADS);
+        rs.seg[tid] = rs.seg[tid + THREADS] = 0u;  // for the row after the next
+      }
       __syncthreads();
-      {  // the hot threads' units: (hot thread, unit of its own) over all threads
-        const int upt = (sl.np + WARPS - 1) / WARPS * B, lg = 32 - __clz(upt - 1 > 0 ? upt - 1 : 0);
-        const int items = rs.nhot << (upt > 1 ? lg : 0);
-        for (int q = tid; q < items; q += THREADS) {
-          const int h = rs.hot[upt > 1 ? q >> lg : q], j = upt > 1 ? q & ((1 << lg) - 1) : 0;
-          const int u = u0 + ((h >> 5) + WARPS * (j / B)) * PU + (j % B) * 32 + (h & 31);
-          if (j >= upt || u >= u1) continue;
-          const Unit<T> c = row.load(u, reinterpret_cast<const uint8_t*>(row.row + (8ll * u - row.off)));
-          float x[8];
-          c.to_f32(x);
-          uint32_t left = 0;
+      auto unit_at = [&](int u) {  // unit u, from global memory
+        return row.load(u, reinterpret_cast<const uint8_t*>(row.row + (8ll * u - row.off)));
+      };
+      auto push = [&](const Unit<T>& c, int u) {
+        float x[8];
+        c.to_f32(x);
+        uint32_t left = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) left |= (x[e] < tf ? 0u : 1u) << e;
-          for (left &= c.ok; left; left &= left - 1) {
-            const int e = __ffs(left) - 1, id = 8 * u - row.off + e;
-            const u64 key = rank_key(Elem<T>::get(row.row[id]), id);
-            if (key < thr) continue;
-            const int at = atomicAdd(&rs.n, 1);
-            if (at < CAP) rs.buf[at] = key;
+        for (int e = 0; e < 8; ++e) left |= (x[e] < tf ? 0u : 1u) << e;
+        for (left &= c.ok; left; left &= left - 1) {
+          const int e = __ffs(left) - 1, id = 8 * u - row.off + e;
+          const u64 key = rank_key(Elem<T>::get(row.row[id]), id);
+          if (key < thr) continue;
+          const int at = atomicAdd(&rs.n, 1);
+          if (at < CAP) rs.buf[at] = key;
+        }
+      };
+      if (by_piece) {  // (hot segment, piece of it) over the warps, the loads of a piece together
+        const int items = rs.nhot << sh_seg;
+        for (int q = warp; q < items; q += WARPS) {
+          const int i0 = (rs.hot[q >> sh_seg] << sh_seg) + (q & ((1 << sh_seg) - 1));
+          const int base = u0 + i0 * PU + lane;
+          Unit<T> c[B];
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            c[i].ok = 0u;
+            if (base + i * 32 < u1) c[i] = unit_at(base + i * 32);
           }
+#pragma unroll
+          for (int i = 0; i < B; ++i)
+            if (c[i].ok) push(c[i], base + i * 32);
+        }
+      } else {  // (hot thread, unit of its own) over all threads
+        const int upt = (sl.np + WARPS - 1) / WARPS * B, lg = upt > 1 ? 32 - __clz(upt - 1) : 0;
+        const int items = rs.nhot << lg;
+        for (int q = tid; q < items; q += THREADS) {
+          const int h = rs.hot[q >> lg], j = q & ((1 << lg) - 1);
+          const int u = u0 + ((h >> 5) + WARPS * (j / B)) * PU + (j % B) * 32 + (h & 31);
+          if (j < upt && u < u1) push(unit_at(u), u);
         }
       }
       __syncthreads();
@@ -612,19 +660,19 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
   }
   if (sh.failed && lane == 0) {  // the copies in flight land before the block leaves
     const uint64_t d2 = globaltimer_ns() + TIMEOUT_NS;
-    for (uint32_t v = used; v < fetched; ++v)
+    for (uint32_t v = used; v < sh.cursor[warp].fetched; ++v)
       mbar_wait_bounded(full + v % STAGES, (v / STAGES) & 1u, d2, &sh.failed);
   }
 }
 
-template <int T, bool MASK>
+template <int T, bool MASK, bool BY_PIECE>
 int launch(const LogprobArgs& a, int sms, cudaStream_t s) {
   static int attr_dev = -1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (attr_dev != dev) {
-    if (cudaFuncSetAttribute(k_token_logprobs<T, MASK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaFuncSetAttribute(k_token_logprobs<T, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(k_token_logprobs<T, MASK, BY_PIECE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(k_token_logprobs<T, MASK, BY_PIECE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)RING_BYTES) != cudaSuccess)
       return MOE_ERR_CUDA;
     attr_dev = dev;
@@ -649,19 +697,25 @@ int launch(const LogprobArgs& a, int sms, cudaStream_t s) {
       lc.dynamicSmemBytes = RING_BYTES;
       lc.attrs = at;
       lc.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&fit[a.cl], k_token_logprobs<T, MASK>, &lc) != cudaSuccess || fit[a.cl] < 1)
+      if (cudaOccupancyMaxActiveClusters(&fit[a.cl], k_token_logprobs<T, MASK, BY_PIECE>, &lc) != cudaSuccess || fit[a.cl] < 1)
         return MOE_ERR_CUDA;
     }
     clusters = fit[a.cl];
   }
   const int grid = (a.p.m < clusters ? a.p.m : clusters) * a.cl;
-  return launch_overlapped(k_token_logprobs<T, MASK>, dim3((unsigned)grid), dim3(THREADS),
+  return launch_overlapped(k_token_logprobs<T, MASK, BY_PIECE>, dim3((unsigned)grid), dim3(THREADS),
                            RING_BYTES, s, a, a.cl);
 }
 
 template <int T>
 int launch_m(const LogprobArgs& a, int sms, cudaStream_t s) {
-  return a.p.allowed ? launch<T, true>(a, sms, s) : launch<T, false>(a, sms, s);
+  // the maxima of pieces rather than threads from 64 pieces a slice on: with
+  // 256 pieces (512 rows of 131072 f32) the threads' units are spread over so
+  // much memory that reading them again costs 37 us against 20, with 49 pieces
+  // (1000 rows of 50001 bf16) the maxima cost 9 us more than they save
+  const bool by_piece = a.p.c.vocab / a.cl >= 64 * (int)PIECE_BYTES / type_bytes(T);
+  if (by_piece) return a.p.allowed ? launch<T, true, true>(a, sms, s) : launch<T, false, true>(a, sms, s);
+  return a.p.allowed ? launch<T, true, false>(a, sms, s) : launch<T, false, false>(a, sms, s);
 }
 
 }  // namespace
