@@ -39,7 +39,7 @@ namespace {
 constexpr int BOX_ROWS = 32;
 constexpr int BOX_K = 256;
 constexpr uint32_t BOX_BYTES = BOX_ROWS * BOX_K / 2;
-constexpr int MAX_WARPS = 16;
+constexpr int MAX_WARPS = 20;
 constexpr int MAX_CTAS = 152;
 constexpr int MAX_STAGES = 4;
 constexpr int PART = BOX_ROWS * DECODE_MAX_M;  // floats of one partial tile
@@ -80,7 +80,7 @@ struct Q4Args {
   CUtensorMap map;           // w as bytes [n][k / 2], box {128 bytes, 32 rows}
   Q4Params p;                // m <= 8 tokens of this pass
   int nb;                    // boxes per row tile
-  FastDiv dnb, dwarps;       // division by nb and by the warps of a block
+  FastDiv dnb, dwarps, dng;  // division by nb, by the warps of a block, by the groups of a row
   Deal deal;                 // boxes (or whole row tiles) to blocks
   bool by_tile;              // blocks are dealt whole row tiles
   int stages;                // ring depth of a warp
@@ -95,7 +95,7 @@ struct Q4Args {
 struct Q4Ctl {
   unsigned long long bar[MAX_WARPS][MAX_STAGES];
   unsigned count[MAX_WARPS];             // boxes stored of the row tile that runs over the warp's end
-  unsigned amax[DECODE_MAX_M];           // bits of the largest finite |x|
+  unsigned amax[DECODE_MAX_M];           // f32 bits of the largest |x|
   unsigned bad;                          // bit t: token t holds an infinity or a NaN
 };
 constexpr uint32_t CTL_BYTES = (sizeof(Q4Ctl) + 15) & ~15u;
@@ -126,6 +126,10 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const void* map, int x, in
           dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_box(const void* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
 }
 
 // The power of two that scales a token: its largest value's exponent e, held
@@ -305,68 +309,80 @@ __device__ __forceinline__ void copy_x(const Q4Params& p, uint32_t xs) {
                    : "memory");
 }
 
-template <int G>
-__device__ __forceinline__ void stage_x(const Q4Params& p, Q4Ctl& C, uint8_t* xp, float4* xs, int xs_ld) {
+// Eight x of type XT as f32.
+template <int XT>
+__device__ __forceinline__ void x_f32(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (XT == MOE_T_BF16) {
+      f[2 * i] = bf16lo(w[i]);
+      f[2 * i + 1] = bf16hi(w[i]);
+    } else {
+      const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = q.x;
+      f[2 * i + 1] = q.y;
+    }
+  }
+}
+
+template <int G, int XT>
+__device__ __forceinline__ void stage_x_t(const Q4Params& p, const FastDiv& dng, Q4Ctl& C, uint8_t* xp, float4* xs,
+                                          int xs_ld) {
   const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int pieces = p.k / 8;
-  const float inf = __uint_as_float(0x7F800000u);
-  {  // the largest finite magnitude of each token: warps share the tokens out
+  {  // each token's largest magnitude (the patterns order like the magnitudes); warps share the tokens out
     const int tok = warp % p.m, part = warp / p.m, parts = ((nthr >> 5) - tok + p.m - 1) / p.m;
-    float mx = 0.f;
-    bool bad = false;
+    uint32_t mx = 0u;
+#pragma unroll 4
     for (int q = part * 32 + lane; q < pieces; q += parts * 32) {
       const uint4 v = *reinterpret_cast<const uint4*>(xp + x_piece(p.m, tok, q));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float f = fabsf(bits_f32((i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu, p.x_type));
-        bad |= !(f < inf);
-        mx = fmaxf(mx, f < inf ? f : 0.f);
-      }
+      mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                 __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
     }
-    const unsigned b = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-    bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) {
-      atomicMax(&C.amax[tok], b);
-      if (bad) atomicOr(&C.bad, 1u << tok);
-    }
+    const unsigned b = __reduce_max_sync(0xffffffffu, max(mx >> 16, mx & 0xFFFFu));
+    if (lane == 0) atomicMax(&C.amax[tok], __float_as_uint(bits_f32(b, XT)));
   }
   __syncthreads();
+  // an infinity or a NaN anywhere: those tokens are computed by terms
+  if (tid < p.m && C.amax[tid] >= 0x7F800000u) atomicOr(&C.bad, 1u << tid);
   constexpr int LPG = G / 8;  // lanes per group, one piece each
   const float unit = p.zeros ? -CODE_UNIT : -8.0f * CODE_UNIT;
-  for (int tok = 0; tok < p.m; ++tok) {
-    const float e = __uint_as_float((uint32_t)(14 - token_exp(C.amax[tok]) + 127) << 23);
-    for (int g0 = 0; g0 < p.ng; g0 += nthr / LPG) {
-      const int grp = g0 + tid / LPG, q = grp * LPG + (tid & (LPG - 1));
-      float sum = 0.f;
-      if (q < pieces) {
-        uint4* at = reinterpret_cast<uint4*>(xp + x_piece(p.m, tok, q));
-        const uint4 v = *at;
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        float f[8];
+  const int work = p.m * p.ng * LPG, rounds = (work + nthr - 1) / nthr;
+#pragma unroll 2
+  for (int i = 0; i < rounds; ++i) {
+    const int at = i * nthr + tid, gg = at / LPG, tok = dng(gg), grp = gg - tok * p.ng;
+    const int q = grp * LPG + (tid & (LPG - 1));
+    const bool live = at < work;
+    float sum = 0.f;
+    if (live && q < pieces) {
+      const float e = __uint_as_float((uint32_t)(14 - token_exp(C.amax[tok]) + 127) << 23), e16 = e * 0.0625f;
+      uint4* ptr = reinterpret_cast<uint4*>(xp + x_piece(p.m, tok, q));
+      float f[8];
+      x_f32<XT>(*ptr, f);
+      sum = e * (((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7])));
+      uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float raw = bits_f32((i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu, p.x_type);
-          f[i] = fabsf(raw) < inf ? raw * e : 0.f;
-          sum += f[i];
-        }
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // odd pairs meet 16 q
-          const float r = (i & 1) ? 0.0625f : 1.0f;
-          const __half2 h = __floats2half2_rn(f[i] * r, f[i + 4] * r);
-          o[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *at = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int j = 0; j < 4; ++j) {  // odd pairs meet 16 q
+        const __half2 h = __floats2half2_rn(f[j] * ((j & 1) ? e16 : e), f[j + 4] * ((j & 1) ? e16 : e));
+        o[j] = *reinterpret_cast<const uint32_t*>(&h);
       }
+      *ptr = make_uint4(o[0], o[1], o[2], o[3]);
+    }
 #pragma unroll
-      for (int o = LPG / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (grp < p.ng && (tid & (LPG - 1)) == 0) {
-        float* at = reinterpret_cast<float*>(xs + grp * xs_ld + (tok >> 1)) + (tok & 1);
-        at[0] = at[2] = sum * unit;
-      }
+    for (int o = LPG / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (live && (tid & (LPG - 1)) == 0) {
+      float* to = reinterpret_cast<float*>(xs + grp * xs_ld + (tok >> 1)) + (tok & 1);
+      to[0] = to[2] = sum * unit;
     }
   }
+}
+
+template <int G>
+__device__ __forceinline__ void stage_x(const Q4Params& p, const FastDiv& dng, Q4Ctl& C, uint8_t* xp, float4* xs,
+                                        int xs_ld) {
+  if (p.x_type == MOE_T_BF16) stage_x_t<G, MOE_T_BF16>(p, dng, C, xp, xs, xs_ld);
+  else stage_x_t<G, MOE_T_F16>(p, dng, C, xp, xs, xs_ld);
 }
 
 template <int G, bool ZEROS>
@@ -408,10 +424,23 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   if (threadIdx.x < MAX_WARPS) C.count[threadIdx.x] = 0u;
   if (threadIdx.x < DECODE_MAX_M) C.amax[threadIdx.x] = 0u;
   if (threadIdx.x == 0) C.bad = 0u;
+  // the first boxes start towards L2 (which every earlier write goes through)
+  if (lane == 0) {
+    int pt = it, pb = ib;
+    for (int i = 0; i < a.stages && i < left; ++i) {
+      prefetch_box(&a.map, pb * (BOX_K / 2), pt * BOX_ROWS);
+      if (++pb == a.nb) {
+        pb = 0;
+        ++pt;
+      }
+    }
+  }
   __syncthreads();
   grid_wait();
-  // x first: its few bytes would otherwise queue behind the weights
+  // x first, all of it: its few bytes would otherwise queue behind the weights
   copy_x(p, smem_u32(xp));
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
   auto issue = [&]() {
     mbar_arrive_expect_tx(barp + ist, BOX_BYTES);
     tma_box(ring + (uint32_t)ist * BOX_BYTES, &a.map, ib * (BOX_K / 2), it * BOX_ROWS, smem_u32(barp + ist));
@@ -428,9 +457,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   BoxScales<G, ZEROS> sc, sc_next;
   size_t sat = (size_t)(tile * BOX_ROWS + g) * p.ng + b * NGB;  // of the box whose scales are loaded next
   if (f0 < f1) sc.load(p, a.vec, sat, tile * BOX_ROWS + g, b * NGB);
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
-  stage_x<G>(p, C, xp, xs, pairs);
+  stage_x<G>(p, a.dng, C, xp, xs, pairs);
   __syncthreads();
   if (f0 >= f1) return;
 
@@ -481,8 +508,11 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
           // the warps that hold them: from the one whose run reaches over the
           // tile's first box here
           int w0 = warp, w1 = warp;
-          while (w0 > 0 && wbegin(w0) > tf0) --w0;
+          if (tf0 <= cf0) w0 = 0;
+          while (wbegin(w0) > max(tf0, cf0)) --w0;
+          if (tf1 >= cf1) w1 = min(W, cf1 - cf0) - 1;
           while (w1 + 1 < W && wbegin(w1 + 1) < min(tf1, cf1)) ++w1;
+          const bool cut = wbegin(w0) < tf0;  // only the first run can have begun in an earlier tile
           float* dst = (first_tile == tile ? parts + warp * part_ld : reinterpret_cast<float*>(ringp)) + (t * 8 + g) * 8;
           if (t < pairs) {
             *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -499,10 +529,10 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] = 0.f;
             if (t < pairs) {
+#pragma unroll 4
               for (int v = w0; v <= w1; ++v) {
-                const bool first = wbegin(v) >= tf0;  // the run began in this tile
-                const float* src = (first ? parts + v * part_ld
-                                          : reinterpret_cast<const float*>(ringp + (v - warp) * a.stages * (int)BOX_BYTES)) +
+                const float* src = (cut && v == w0 ? reinterpret_cast<const float*>(ringp + (v - warp) * a.stages * (int)BOX_BYTES)
+                                                   : parts + v * part_ld) +
                                    (t * 8 + g) * 8;
                 const float4 q0 = *reinterpret_cast<const float4*>(src);
                 const float4 q1 = *reinterpret_cast<const float4*>(src + 4);
@@ -647,6 +677,7 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
           reinterpret_cast<uintptr_t>(p0.zeros) % ngb == 0;
   a.nb = (p0.k + BOX_K - 1) / BOX_K;
   a.dnb = FastDiv::of((unsigned)a.nb);
+  a.dng = FastDiv::of((unsigned)p0.ng);
   const int tiles = (p0.n + BOX_ROWS - 1) / BOX_ROWS, total = tiles * a.nb;
   sms = min(sms, MAX_CTAS);
   for (int t0 = 0; t0 < p0.m;) {
