@@ -42,6 +42,7 @@ constexpr uint32_t BOX_BYTES = BOX_ROWS * BOX_K / 2;
 constexpr int MAX_WARPS = 20;
 constexpr int MAX_CTAS = 152;
 constexpr int MAX_STAGES = 4;
+constexpr int PREFETCH = 1;                    // boxes a warp sends for before the stream's previous kernel has ended
 constexpr int PART = BOX_ROWS * DECODE_MAX_M;  // floats of one partial tile
 constexpr uint32_t SMEM_MAX = 232448;
 constexpr float CODE_UNIT = 0x1.0p-24f;        // value of the fp16 bit pattern 1
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   // the first boxes start towards L2 (which every earlier write goes through)
   if (lane == 0) {
     int pt = it, pb = ib;
-    for (int i = 0; i < a.stages && i < left; ++i) {
+    for (int i = 0; i < PREFETCH && i < left; ++i) {
       prefetch_box(&a.map, pb * (BOX_K / 2), pt * BOX_ROWS);
       if (++pb == a.nb) {
         pb = 0;
@@ -451,13 +452,15 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
     if (++ist == a.stages) ist = 0;
     --left;
   };
-  if (lane == 0)
-    for (int i = 0; i < a.stages && left > 0; ++i) issue();
+  // one box a warp keeps the memory busy while x is laid out, and is issued sooner than all
+  if (lane == 0 && left > 0) issue();
   constexpr int NGB = BOX_K / G;
   BoxScales<G, ZEROS> sc, sc_next;
   size_t sat = (size_t)(tile * BOX_ROWS + g) * p.ng + b * NGB;  // of the box whose scales are loaded next
   if (f0 < f1) sc.load(p, a.vec, sat, tile * BOX_ROWS + g, b * NGB);
   stage_x<G>(p, a.dng, C, xp, xs, pairs);
+  if (lane == 0)
+    for (int i = 1; i < a.stages && left > 0; ++i) issue();
   __syncthreads();
   if (f0 >= f1) return;
 
