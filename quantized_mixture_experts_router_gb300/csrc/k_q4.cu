@@ -187,47 +187,63 @@ struct BoxScales {
   static constexpr int NS = NG / 2, NZ = (NG + 3) / 4;
   uint32_t s[4][NS];  // two 16-bit scales a word
   uint32_t z[4][NZ];
-  // at: index of the lane's first row's first group of the box; row0 that
-  // row, g0 its first group
-  __device__ __forceinline__ void load(const Q4Params& p, bool vec, size_t at0, int row0, int g0) {
+  // sp, zp: the lane's first row's first group of the box; stride: elements from
+  // row to row g + 8; rows, groups: how many of the lane's four rows, and of the
+  // box's groups, there are (a scale past them is 0).
+  __device__ __forceinline__ void load(bool vec, const uint16_t* sp, const uint8_t* zp, int stride, int rows,
+                                       int groups) {
+    if (rows == 4 && groups >= NG) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int j = 0; j < NS; ++j) s[i][j] = 0u;
-#pragma unroll
-      for (int j = 0; j < NZ; ++j) z[i][j] = 0u;
-      if (row0 + 8 * i >= p.n) continue;  // scale 0
-      const size_t at = at0 + (unsigned)(8 * i * p.ng);
-      if (vec) {
-        const uint16_t* q = p.scales + at;
-        const uint8_t* zq = p.zeros + at;
-        if (NG == 2) {
-          s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(q));
-          if (ZEROS) z[i][0] = __ldg(reinterpret_cast<const uint16_t*>(zq));
-        } else if (NG == 4) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
-          s[i][0] = v.x;
-          s[i][NS - 1] = v.y;
-          if (ZEROS) z[i][0] = __ldg(reinterpret_cast<const uint32_t*>(zq));
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t* q = sp + i * stride;
+        const uint8_t* zq = zp + i * stride;
+        if (vec) {
+          if (NG == 2) {
+            s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+            if (ZEROS) z[i][0] = __ldg(reinterpret_cast<const uint16_t*>(zq));
+          } else if (NG == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
+            s[i][0] = v.x;
+            s[i][NS - 1] = v.y;
+            if (ZEROS) z[i][0] = __ldg(reinterpret_cast<const uint32_t*>(zq));
+          } else {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(q));
+            s[i][0] = v.x;
+            s[i][1 % NS] = v.y;
+            s[i][2 % NS] = v.z;
+            s[i][NS - 1] = v.w;
+            if (ZEROS) {
+              const uint2 u = __ldg(reinterpret_cast<const uint2*>(zq));
+              z[i][0] = u.x;
+              z[i][NZ - 1] = u.y;
+            }
+          }
         } else {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(q));
-          s[i][0] = v.x;
-          s[i][1 % NS] = v.y;
-          s[i][2 % NS] = v.z;
-          s[i][NS - 1] = v.w;
+#pragma unroll
+          for (int j = 0; j < NS; ++j)
+            s[i][j] = (uint32_t)__ldg(q + 2 * j) | ((uint32_t)__ldg(q + 2 * j + 1) << 16);
           if (ZEROS) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(zq));
-            z[i][0] = u.x;
-            z[i][NZ - 1] = u.y;
+#pragma unroll
+            for (int j = 0; j < NZ; ++j) {
+              z[i][j] = (uint32_t)__ldg(zq + 4 * j) | ((uint32_t)__ldg(zq + 4 * j + 1) << 8);
+              if (NG >= 4)
+                z[i][j] |= ((uint32_t)__ldg(zq + 4 * j + 2) << 16) | ((uint32_t)__ldg(zq + 4 * j + 3) << 24);
+            }
           }
         }
-      } else {
-        const int left = p.ng - g0;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) s[i][j] = 0u;
+#pragma unroll
+        for (int j = 0; j < NZ; ++j) z[i][j] = 0u;
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-          if (j < left) {
-            s[i][j / 2] |= (uint32_t)__ldg(p.scales + at + j) << (16 * (j & 1));
-            if (ZEROS) z[i][j / 4] |= (uint32_t)__ldg(p.zeros + at + j) << (8 * (j & 3));
+          if (i < rows && j < groups) {
+            s[i][j / 2] |= (uint32_t)__ldg(sp + i * stride + j) << (16 * (j & 1));
+            if (ZEROS) z[i][j / 4] |= (uint32_t)__ldg(zp + i * stride + j) << (8 * (j & 3));
           }
         }
       }
@@ -456,8 +472,14 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   if (lane == 0 && left > 0) issue();
   constexpr int NGB = BOX_K / G;
   BoxScales<G, ZEROS> sc, sc_next;
-  size_t sat = (size_t)(tile * BOX_ROWS + g) * p.ng + b * NGB;  // of the box whose scales are loaded next
-  if (f0 < f1) sc.load(p, a.vec, sat, tile * BOX_ROWS + g, b * NGB);
+  // scales (and zeros) of the box that is loaded next
+  const uint16_t* sp = p.scales + (size_t)(tile * BOX_ROWS + g) * p.ng + b * NGB;
+  const uint8_t* zp = p.zeros + (ZEROS ? (size_t)(tile * BOX_ROWS + g) * p.ng + b * NGB : 0);
+  auto load_scales = [&](BoxScales<G, ZEROS>& to, int tl, int bx) {
+    const int rows = p.n - tl * BOX_ROWS >= BOX_ROWS ? 4 : max(0, (p.n - tl * BOX_ROWS - g + 7) >> 3);
+    to.load(a.vec, sp, zp, 8 * p.ng, rows, p.ng - bx * NGB);
+  };
+  if (f0 < f1) load_scales(sc, tile, b);
   stage_x<G>(p, a.dng, C, xp, xs, pairs);
   if (lane == 0)
     for (int i = 1; i < a.stages && left > 0; ++i) issue();
@@ -481,8 +503,10 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   for (; f < f1; ++f) {
     const bool wrap = b + 1 == a.nb;
     const int tile1 = wrap ? tile + 1 : tile, b1 = wrap ? 0 : b + 1;
-    sat += wrap ? (size_t)(BOX_ROWS * p.ng - b * NGB) : (size_t)NGB;
-    if (f + 1 < f1) sc_next.load(p, a.vec, sat, tile1 * BOX_ROWS + g, b1 * NGB);
+    const int hop = wrap ? BOX_ROWS * p.ng - b * NGB : NGB;
+    sp += hop;
+    if (ZEROS) zp += hop;
+    if (f + 1 < f1) load_scales(sc_next, tile1, b1);
     if (!mbar_try_wait(barp + st, phase) && !mbar_wait_for(barp + st, phase, a.timeout_ns, a.status)) ok = false;
     if (!__all_sync(0xffffffffu, ok)) break;
     const uint32_t buf = ring + (uint32_t)st * BOX_BYTES + alane;
