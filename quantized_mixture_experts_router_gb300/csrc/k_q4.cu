@@ -108,13 +108,12 @@ __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-// d = A B + c, A 16 rows x 16 k, B 16 k x 8 tokens, fp16 with f32 sums.
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                         const float (&c)[4]) {
+// c += A B, A 16 rows x 16 k, B 16 k x 8 tokens, fp16 with f32 sums.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float bits_f32(uint32_t v16, int t) {
@@ -190,14 +189,14 @@ struct BoxScales {
   // sp, zp: the lane's first row's first group of the box; stride: elements from
   // row to row g + 8; rows, groups: how many of the lane's four rows, and of the
   // box's groups, there are (a scale past them is 0).
-  __device__ __forceinline__ void load(bool vec, const uint16_t* sp, const uint8_t* zp, int stride, int rows,
-                                       int groups) {
+  template <bool VEC>
+  __device__ __forceinline__ void load(const uint16_t* sp, const uint8_t* zp, int stride, int rows, int groups) {
     if (rows == 4 && groups >= NG) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint16_t* q = sp + i * stride;
         const uint8_t* zq = zp + i * stride;
-        if (vec) {
+        if (VEC) {
           if (NG == 2) {
             s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(q));
             if (ZEROS) z[i][0] = __ldg(reinterpret_cast<const uint16_t*>(zq));
@@ -293,7 +292,7 @@ __device__ __forceinline__ void do_box(int scale_type, const BoxScales<G, ZEROS>
           for (int i = 0; i < 2; ++i) {
             const uint32_t wa = h ? w[2 * i] >> 8 : w[2 * i], wb = h ? w[2 * i + 1] >> 8 : w[2 * i + 1];
             const uint32_t a[4] = {wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u};
-            mma16816(c[i], a, xv[2 * h], xv[2 * h + 1], c[i]);
+            mma16816(c[i], a, xv[2 * h], xv[2 * h + 1]);
           }
       }
     }
@@ -402,7 +401,7 @@ __device__ __forceinline__ void stage_x(const Q4Params& p, const FastDiv& dng, Q
   else stage_x_t<G, MOE_T_F16>(p, dng, C, xp, xs, xs_ld);
 }
 
-template <int G, bool ZEROS>
+template <int G, bool ZEROS, bool VEC>
 __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_constant__ Q4Args a) {
   extern __shared__ __align__(1024) uint8_t raw_smem[];
   const uint32_t base0 = smem_u32(raw_smem);
@@ -477,7 +476,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   const uint8_t* zp = p.zeros + (ZEROS ? (size_t)(tile * BOX_ROWS + g) * p.ng + b * NGB : 0);
   auto load_scales = [&](BoxScales<G, ZEROS>& to, int tl, int bx) {
     const int rows = p.n - tl * BOX_ROWS >= BOX_ROWS ? 4 : max(0, (p.n - tl * BOX_ROWS - g + 7) >> 3);
-    to.load(a.vec, sp, zp, 8 * p.ng, rows, p.ng - bx * NGB);
+    to.template load<VEC>(sp, zp, 8 * p.ng, rows, p.ng - bx * NGB);
   };
   if (f0 < f1) load_scales(sc, tile, b);
   stage_x<G>(p, a.dng, C, xp, xs, pairs);
@@ -645,23 +644,26 @@ uint32_t fixed_bytes(int tokens, int k, int ng, int warps) {
   return 1024 + CTL_BYTES + (uint32_t)warps * pairs * 256 + (uint32_t)tokens * k * 2 + (uint32_t)ng * pairs * 16;
 }
 
-template <int G, bool ZEROS>
+template <int G, bool ZEROS, bool VEC>
 int launch_rows(const Q4Args& a, unsigned grid, int warps, uint32_t smem, cudaStream_t s) {
   static int attr_dev = -1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (attr_dev != dev) {
-    if (cudaFuncSetAttribute(k_q4_rows<G, ZEROS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) !=
+    if (cudaFuncSetAttribute(k_q4_rows<G, ZEROS, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) !=
         cudaSuccess)
       return MOE_ERR_CUDA;
     attr_dev = dev;
   }
-  return launch_overlapped(k_q4_rows<G, ZEROS>, dim3(grid), dim3((unsigned)warps * 32), smem, s, a);
+  return launch_overlapped(k_q4_rows<G, ZEROS, VEC>, dim3(grid), dim3((unsigned)warps * 32), smem, s, a);
 }
 
 template <int G>
 int launch_rows_z(const Q4Args& a, unsigned grid, int warps, uint32_t smem, cudaStream_t s) {
-  return a.p.zeros ? launch_rows<G, true>(a, grid, warps, smem, s) : launch_rows<G, false>(a, grid, warps, smem, s);
+  if (a.vec) return a.p.zeros ? launch_rows<G, true, true>(a, grid, warps, smem, s)
+                              : launch_rows<G, false, true>(a, grid, warps, smem, s);
+  return a.p.zeros ? launch_rows<G, true, false>(a, grid, warps, smem, s)
+                   : launch_rows<G, false, false>(a, grid, warps, smem, s);
 }
 
 }  // namespace
