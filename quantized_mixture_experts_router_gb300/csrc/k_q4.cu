@@ -693,8 +693,9 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
   a.status = &reinterpret_cast<Ctrl*>(base + w.ctrl)->status;
   // Up to sixteen tokens two passes over the weights cost less than the tiles'
   // dequantisation (131072 x 5120: 2 x 64 us against 165 us; 5120 x 2304: 13 us
-  // against 16 us), from there on more.
-  if (p0.m > 2 * DECODE_MAX_M) return launch_q4_gemm(p0, a.status, sms, s);
+  // against 16 us), from there on more.  (The tiles address out by 32-bit
+  // offsets within a tile: not for pitches above 2^24.)
+  if (p0.m > 2 * DECODE_MAX_M && p0.ldo <= (1 << 24)) return launch_q4_gemm(p0, a.status, sms, s);
   if (!make_map_2d(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p0.w, (uint64_t)p0.k / 2, (uint64_t)p0.n, (uint64_t)p0.k / 2,
                    BOX_K / 2, BOX_ROWS, 128))
     return MOE_ERR_CUDA;

@@ -380,10 +380,33 @@ __device__ __forceinline__ void drain(uint32_t col, int np, float s, float (&R)[
   }
 }
 
-__device__ __forceinline__ void store_cols(const Q4Params& p, int row, int tok0, int np, const float (&R)[64]) {
+// Tokens tok0 .. tok0 + 63 of one row (those that exist): a warp's stores of a
+// token are contiguous.  One comparison, one addition and one store an output:
+// the code is unrolled over the registers and its length is what it costs.
+template <int T>
+__device__ __forceinline__ void store_cols_t(char* out, uint32_t off, uint32_t step, int count, const float (&R)[64]) {
 #pragma unroll
-  for (int j = 0; j < 64; ++j)
-    if (j < np && tok0 + j < p.m && row < p.n) store_elem(p.out, (tok0 + j) * p.ldo + row, p.out_type, R[j]);
+  for (int j = 0; j < 64; ++j) {
+    if (j < count) *reinterpret_cast<typename Elem<T>::type*>(out + off) = Elem<T>::put(R[j]);
+    off += step;
+  }
+}
+__device__ __forceinline__ void store_cols(const Q4Params& p, int row0, int r, int tok0, int np, const float (&R)[64]) {
+  const int count = row0 + r < p.n ? min(np, p.m - tok0) : 0;
+  const int sz = type_bytes(p.out_type);
+  char* out = static_cast<char*>(p.out) + ((long long)tok0 * p.ldo + row0) * sz;
+  const uint32_t off = (uint32_t)(r * sz), step = (uint32_t)p.ldo * (uint32_t)sz;  // 64 rows of out span less than 4 GB
+  if (p.out_type == MOE_T_F32) store_cols_t<MOE_T_F32>(out, off, step, count, R);
+  else if (p.out_type == MOE_T_BF16) store_cols_t<MOE_T_BF16>(out, off, step, count, R);
+  else store_cols_t<MOE_T_F16>(out, off, step, count, R);
+}
+
+// A 16-bit load that stays where it is written (the compiler would move it next
+// to its use, behind the wait that is to hide it).
+__device__ __forceinline__ uint32_t load_u16_here(const uint16_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
 }
 
 __device__ void run_epilogue(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, const Waiter& wt) {
@@ -400,10 +423,10 @@ __device__ void run_epilogue(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, con
     float R0[64], R1[64];
 #pragma unroll
     for (int j = 0; j < 64; ++j) R0[j] = R1[j] = 0.f;
-    uint32_t next = __ldg(srow);
+    uint32_t next = load_u16_here(srow);
     for (int g = 0; g < p.ng; ++g) {
       const float s = p.scale_type == MOE_T_BF16 ? __uint_as_float(next << 16) : half_bits_to_float(next);
-      if (g + 1 < p.ng) next = __ldg(srow + g + 1);
+      if (g + 1 < p.ng) next = load_u16_here(srow + g + 1);
       const uint32_t r0 = T.n > HALF ? 0u : (uint32_t)g & 1u;  // as the MMA issuer picks them
       if (!wt.warp(C.acc_full[r0], (par >> r0) & 1u)) return;
       par ^= 1u << r0;
@@ -416,8 +439,8 @@ __device__ void run_epilogue(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, con
         drain(col + HALF, np1, s, R1, C.acc_empty[1]);
       }
     }
-    store_cols(p, row, T.tok0 + 64 * set, np0, R0);
-    if (T.n > HALF) store_cols(p, row, T.tok0 + HALF + 64 * set, np1, R1);
+    store_cols(p, T.row0, quarter * 32 + lane, T.tok0 + 64 * set, np0, R0);
+    if (T.n > HALF) store_cols(p, T.row0, quarter * 32 + lane, T.tok0 + HALF + 64 * set, np1, R1);
   }
 }
 
