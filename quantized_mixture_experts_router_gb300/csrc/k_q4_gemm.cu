@@ -4,13 +4,13 @@
 //
 //   A  q - z, exact in bf16 and fp16, written by the dequantising warps into
 //      tensor memory (lane = row), so that shared memory carries B alone.
-//   B  x as it is, by TMA (128-byte swizzle), 128 k a stage.
+//   B  x as it is, by TMA (128-byte swizzle), 64 or 128 k a stage.
 // A group's products accumulate into a fresh tensor-memory accumulator; the
 // epilogue warps drain it, multiply by the row's f32 scale and add it to
 // running sums in registers.  So no weight is rounded and the scale costs one
-// FMA per group and output.  Two accumulators of 128 tokens alternate: a tile
-// of more than 128 tokens is two halves that share each A stage, one drained
-// while the tensor cores fill the other.
+// FMA per group and output.  Two or three accumulators of 128 tokens take
+// turns (a tile of more than 128 tokens is two halves that share each A stage),
+// so that one is drained while the tensor cores fill the others.
 //
 // x, at 256 tokens a tile, is the larger operand by far (a weight has four
 // bits): a cluster of two blocks takes consecutive row tiles of the same
@@ -31,17 +31,33 @@ namespace {
 constexpr int TM = 128;            // weight rows per tile
 constexpr int TN = 256;            // tokens per tile, at most
 constexpr int HALF = 128;          // tokens per accumulator
-constexpr int KC = 128;            // k per stage
-constexpr int KS = 64;             // k per swizzled 128-byte row: a stage of B is two such tiles
+constexpr int KS = 64;             // k per swizzled 128-byte row of x
+constexpr int RAW_K = 128;         // k per raw stage
 constexpr int BBOX = 64;           // tokens per B copy
-constexpr uint32_t B_HALF = TN * KS * 2;
-constexpr uint32_t B_STAGE = 2 * B_HALF;
-constexpr uint32_t RAW_STAGE = TM * KC / 2;
-constexpr int NS = 3;              // stages of the A and B rings, which move together
+constexpr uint32_t B_SUB = TN * KS * 2;       // 64 k of all tokens
+constexpr uint32_t RAW_STAGE = TM * RAW_K / 2;
 constexpr int NSR = 4;             // raw stages
-constexpr uint32_t A_COL0 = 2 * HALF;      // tensor-memory columns of the A ring, 64 a stage
+
+// Groups of 128: stages of 128 k and two accumulators; a drain and its two
+// hand-overs fit behind the other half's MMAs, and fewer hand-overs of stages
+// count more (512 tokens, 131072 x 5120: 513 us against 579 with the other
+// choice).  Shorter groups: stages of 64 k leave tensor memory for a third
+// accumulator, which doubles the time for a drain (groups of 64: 777 us
+// against 1095; of 32: 1410 against 1360).
+template <int G>
+struct Cfg {
+  static constexpr int KC = G == 128 ? 128 : 64;   // k per stage of A and B
+  static constexpr int SUBS = KC / KS;
+  static constexpr int NS = G == 128 ? 3 : 4;      // stages of the A and B rings, which move together
+  static constexpr int NACC = G == 128 ? 2 : 3;    // accumulators
+  static constexpr uint32_t B_STAGE = SUBS * B_SUB;
+  static constexpr uint32_t A_COLS = KC / 2;       // tensor-memory columns of an A stage
+  static constexpr uint32_t A_COL0 = NACC * HALF;
+  static_assert(A_COL0 + NS * A_COLS <= 512, "tensor memory");
+};
+constexpr int MAX_NS = 4, MAX_NACC = 3;
 constexpr int NEW = 8;             // epilogue warps 0-7: tokens 0-63 (0-3) and 64-127 (4-7) of each half
-constexpr int NDW = 8;             // dequantising warps 8-15: the first (8-11) and second 64 k (12-15) of a stage
+constexpr int NDW = 8;             // dequantising warps 8-15: the even (8-11) and odd (12-15) 64 k
 constexpr int W_TMA = 16, W_MMA = 17, W_RAW = 18;
 constexpr int NTHR = 640;
 // Registers per thread: 96 at launch; the shares add up to the launch's total.
@@ -60,17 +76,18 @@ struct Q4GemmArgs {
 };
 
 struct GemmCtl {
-  unsigned long long full[NS];    // a stage's A and B are there
-  unsigned long long empty[NS];   // every block of the cluster is done with them
+  unsigned long long full[MAX_NS];    // a stage's A and B are there
+  unsigned long long empty[MAX_NS];   // every block of the cluster is done with them
   unsigned long long r_full[NSR], r_empty[NSR];
-  unsigned long long acc_full[2], acc_empty[2];
+  unsigned long long acc_full[MAX_NACC], acc_empty[MAX_NACC];
   unsigned long long done;
   uint32_t tmem;
   uint32_t abort;
 };
 
-constexpr uint32_t SMEM_BYTES = 1024 + NS * B_STAGE + NSR * RAW_STAGE + ((sizeof(GemmCtl) + 15) & ~15u);
-static_assert(SMEM_BYTES <= 232448, "stages exceed the shared memory of a block");
+template <int G>
+constexpr uint32_t SMEM_BYTES = 1024 + Cfg<G>::NS * Cfg<G>::B_STAGE + NSR * RAW_STAGE + ((sizeof(GemmCtl) + 15) & ~15u);
+static_assert(SMEM_BYTES<128> <= 232448 && SMEM_BYTES<64> <= 232448, "stages exceed the shared memory of a block");
 
 __device__ __forceinline__ uint64_t* bp(unsigned long long& b) { return reinterpret_cast<uint64_t*>(&b); }
 
@@ -132,6 +149,17 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// A place in a ring: the index, and the phase of each entry in a bit.
+template <int N>
+struct Place {
+  uint32_t i, phases;
+  __device__ __forceinline__ uint32_t parity() const { return (phases >> i) & 1u; }
+  __device__ __forceinline__ void next() {
+    phases ^= 1u << i;
+    i = i + 1 == N ? 0u : i + 1;
+  }
+};
+
 struct Tile {
   int row0, tok0, n;  // n: tokens, rounded up to 16; rows past the end compute zeros
 };
@@ -146,7 +174,7 @@ __device__ __forceinline__ Tile tile_of(const Q4GemmArgs& a, int t) {
 
 // ------------------------------------------------------------ TMA issuers
 __device__ void run_raw(const Q4GemmArgs& a, GemmCtl& C, uint32_t raw_smem, const Waiter& wt) {
-  const int chunks = (a.p.k + KC - 1) / KC;
+  const int chunks = (a.p.k + RAW_K - 1) / RAW_K;
   uint32_t u = 0;
   for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
     const Tile T = tile_of(a, t);
@@ -154,7 +182,7 @@ __device__ void run_raw(const Q4GemmArgs& a, GemmCtl& C, uint32_t raw_smem, cons
       const uint32_t st = u % NSR;
       if (u >= NSR && !wt.one(C.r_empty[st], (u / NSR - 1) & 1u)) goto out;
       mbar_arrive_expect_tx(bp(C.r_full[st]), RAW_STAGE);
-      tma_load_2d(raw_smem + st * RAW_STAGE, &a.map_w, c * (KC / 2), T.row0, bp(C.r_full[st]));
+      tma_load_2d(raw_smem + st * RAW_STAGE, &a.map_w, c * (RAW_K / 2), T.row0, bp(C.r_full[st]));
     }
   }
 out:
@@ -166,7 +194,9 @@ out:
 
 // A and B stage j of the ring holds chunks j, j + NS, ... of every tile, so that
 // the roles' loops unroll to fixed stages; `par` holds a stage's phase in bit j.
+template <int G>
 __device__ void run_x(const Q4GemmArgs& a, GemmCtl& C, uint32_t b_smem, const Waiter& wt) {
+  constexpr int KC = Cfg<G>::KC, NS = Cfg<G>::NS, SUBS = Cfg<G>::SUBS;
   const int chunks = (a.p.k + KC - 1) / KC, rank = (int)cluster_rank();
   const uint16_t mask = (uint16_t)((1u << a.cl) - 1u);
   uint32_t par = 0, used = 0;
@@ -177,9 +207,10 @@ __device__ void run_x(const Q4GemmArgs& a, GemmCtl& C, uint32_t b_smem, const Wa
     for (int c = 0; c < chunks; ++c) {
       if (!wt.one(C.empty[st], ((par >> st) & 1u) ^ 1u)) goto out;  // passes at once the first time
       mbar_arrive_expect_tx(bp(C.full[st]), (uint32_t)nbox * BBOX * KC * 2);
-      for (int r = rank; r < 2 * nbox; r += a.cl) {  // (tokens 64 (r / 2) .., k 64 (r % 2) ..)
-        const uint32_t dst = b_smem + st * B_STAGE + (uint32_t)(r & 1) * B_HALF + (uint32_t)(r >> 1) * (BBOX * 128);
-        const int x = c * KC + (r & 1) * KS, y = T.tok0 + (r >> 1) * BBOX;
+      for (int r = rank; r < SUBS * nbox; r += a.cl) {  // (64 tokens, 64 k)
+        const int sub = r % SUBS, box = r / SUBS;
+        const uint32_t dst = b_smem + st * Cfg<G>::B_STAGE + (uint32_t)sub * B_SUB + (uint32_t)box * (BBOX * 128);
+        const int x = c * KC + sub * KS, y = T.tok0 + box * BBOX;
         if (a.cl > 1) tma_load_2d_multi(dst, &a.map_x, x, y, bp(C.full[st]), mask);
         else tma_load_2d(dst, &a.map_x, x, y, bp(C.full[st]));
       }
@@ -202,51 +233,50 @@ out:
 // ------------------------------------------------------------ MMA issuer
 // The whole warp walks the loop, so that addresses and descriptors are uniform
 // values, and one elected thread issues.  The instructions of this warp per
-// MMA bound the kernel: a round of NS chunks is unrolled, with fixed stages
-// and offsets.  Accumulator of a use: its half (two halves), or the use's
-// lowest bit (one).
+// MMA count: a round of NS chunks is unrolled, with fixed stages and offsets.
+// Every use of an accumulator takes the next one of the ring.
 template <bool BF, int G, int NH>
 __device__ __forceinline__ bool mma_tile(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, uint64_t bdesc0,
                                          const Waiter& wt, int n, int chunks, uint16_t mask, uint32_t& full_par,
-                                         uint32_t& acc_par) {
+                                         Place<Cfg<G>::NACC>& pc) {
+  constexpr int KC = Cfg<G>::KC, NS = Cfg<G>::NS;
   constexpr int GPC = KC / G;        // groups per chunk
   constexpr int STEPS = G / 16;      // MMA steps of a group
   const uint32_t id0 = umma_idesc(min(n, HALF), BF), id1 = umma_idesc(NH == 2 ? n - HALF : 16, BF);
-  const int last_groups = (a.p.k - (chunks - 1) * KC + G - 1) / G;  // groups of the last chunk
+  const int last_groups = GPC == 1 ? 1 : (a.p.k - (chunks - 1) * KC + G - 1) / G;  // groups of the last chunk
 #pragma unroll 1
   for (int c0 = 0; c0 < chunks; c0 += NS) {
     asm volatile("" : "+l"(bdesc0), "+r"(tmem));  // offsets are added in place, not kept in registers over the loop
 #pragma unroll
     for (int st = 0; st < NS; ++st) {
       if (c0 + st >= chunks) break;
-      const int groups = c0 + st == chunks - 1 ? last_groups : GPC;
 #pragma unroll
       for (int gi = 0; gi < GPC; ++gi) {
-        if (GPC > 1 && gi >= groups) break;
+        if (gi > 0 && c0 + st == chunks - 1 && gi >= last_groups) break;
+        const bool frees = gi == GPC - 1 || (c0 + st == chunks - 1 && gi + 1 >= last_groups);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          const int reg = NH == 2 ? h : (GPC == 1 ? (c0 + st) & 1 : gi & 1);
           if (h == 0 && gi == 0 && !wt.warp(C.full[st], (full_par >> st) & 1u)) return false;
-          if (!wt.warp(C.acc_empty[reg], ((acc_par >> reg) & 1u) ^ 1u)) return false;
-          acc_par ^= 1u << reg;
+          if (!wt.warp(C.acc_empty[pc.i], pc.parity() ^ 1u)) return false;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t d = tmem + reg * HALF, id = h ? id1 : id0;
+            const uint32_t d = tmem + pc.i * HALF, id = h ? id1 : id0;
             // k past the end of the row meets zeros of x (the copies fill them in)
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
               const int step = gi * STEPS + i;
-              umma_f16_ta(d, tmem + A_COL0 + st * 64 + step * 8,
-                          bdesc0 + (uint64_t)((st * B_STAGE + (step / 4) * B_HALF + h * HALF * 128) >> 4) +
+              umma_f16_ta(d, tmem + Cfg<G>::A_COL0 + st * Cfg<G>::A_COLS + step * 8,
+                          bdesc0 + (uint64_t)((st * Cfg<G>::B_STAGE + (step / 4) * B_SUB + h * HALF * 128) >> 4) +
                               2u * (step % 4),
                           id, i > 0);
             }
-            umma_commit(bp(C.acc_full[reg]));
-            if (h == NH - 1 && (GPC == 1 || gi + 1 == groups)) {  // the stage is free once these are done
+            umma_commit(bp(C.acc_full[pc.i]));
+            if (h == NH - 1 && frees) {  // the stage is free once these are done
               if (a.cl > 1) umma_commit_multi(bp(C.empty[st]), mask);
               else umma_commit(bp(C.empty[st]));
             }
           }
+          pc.next();
         }
       }
       full_par ^= 1u << st;
@@ -257,14 +287,15 @@ __device__ __forceinline__ bool mma_tile(const Q4GemmArgs& a, GemmCtl& C, uint32
 
 template <bool BF, int G>
 __device__ void run_mma(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, uint32_t b_smem, const Waiter& wt) {
-  const int chunks = (a.p.k + KC - 1) / KC;
+  const int chunks = (a.p.k + Cfg<G>::KC - 1) / Cfg<G>::KC;
   const uint64_t bdesc0 = umma_desc(b_smem);
   const uint16_t mask = (uint16_t)((1u << a.cl) - 1u);
-  uint32_t full_par = 0, acc_par = 0;
+  uint32_t full_par = 0;
+  Place<Cfg<G>::NACC> pc{0u, 0u};
   for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
     const Tile T = tile_of(a, t);
-    const bool ok = T.n > HALF ? mma_tile<BF, G, 2>(a, C, tmem, bdesc0, wt, T.n, chunks, mask, full_par, acc_par)
-                               : mma_tile<BF, G, 1>(a, C, tmem, bdesc0, wt, T.n, chunks, mask, full_par, acc_par);
+    const bool ok = T.n > HALF ? mma_tile<BF, G, 2>(a, C, tmem, bdesc0, wt, T.n, chunks, mask, full_par, pc)
+                               : mma_tile<BF, G, 1>(a, C, tmem, bdesc0, wt, T.n, chunks, mask, full_par, pc);
     if (!ok) break;
   }
   __syncwarp();
@@ -295,27 +326,28 @@ __device__ __forceinline__ void expand8(uint32_t w, uint32_t zz, uint32_t* o) {
   o[3] = h2_sub(__byte_perm(b, BASE, 0x4342u), zz, BF);
 }
 
-// Warps 8-11 write the first 64 k of every stage, warps 12-15 the second;
-// thread = weight row.
-template <bool BF>
+// Warps 8-11 write the even 64 k, warps 12-15 the odd ones; thread = weight row.
+template <bool BF, int G>
 __device__ void run_dequant(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, const uint8_t* raw, const Waiter& wt) {
   const Q4Params& p = a.p;
   const int w = (threadIdx.x >> 5) - NEW, lane = threadIdx.x & 31;
   const int hi = w >> 2, quarter = w & 3, r = quarter * 32 + lane;
-  const int chunks = (p.k + KC - 1) / KC;
+  constexpr int KC = Cfg<G>::KC, NS = Cfg<G>::NS;
+  const int raws = (p.k + RAW_K - 1) / RAW_K;
   const uint32_t base = BF ? 0x43004300u : 0x64006400u;
-  const uint32_t acol = tmem + ((uint32_t)(quarter * 32) << 16) + A_COL0 + (uint32_t)hi * 32u;
+  const uint32_t acol = tmem + ((uint32_t)(quarter * 32) << 16) + Cfg<G>::A_COL0 + (KC == 128 ? (uint32_t)hi * 32u : 0u);
   uint32_t ru = 0, par = 0;  // raw stages walked; phases of the A stages
   for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
     const Tile T = tile_of(a, t);
     const uint8_t* zrow = p.zeros && T.row0 + r < p.n ? p.zeros + (size_t)(T.row0 + r) * p.ng : nullptr;
-    uint32_t as = 0;
-    for (int c = 0; c < chunks; ++c, ++ru) {
+    uint32_t as = KC == 128 ? 0u : (uint32_t)hi;
+    for (int rc = 0; rc < raws; ++rc, ++ru) {
+      const int k0 = rc * RAW_K + hi * KS;
       const uint32_t rs = ru % NSR;
       uint32_t zz[2];  // 32 k each: one group at most
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int k = c * KC + hi * KS + 32 * j;
+        const int k = k0 + 32 * j;
         zz[j] = base + (p.zeros ? (zrow && k < p.k ? (uint32_t)__ldg(zrow + k / p.group) : 0u) : 8u) * 0x00010001u;
       }
       if (!wt.warp(C.r_full[rs], (ru / NSR) & 1u)) return;
@@ -326,6 +358,7 @@ __device__ void run_dequant(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, cons
       for (int j = 0; j < 2; ++j) v[j] = *reinterpret_cast<const uint4*>(row + (((2 * hi + j) ^ ((r >> 1) & 3)) << 4));
       __syncwarp();
       if (lane == 0) mbar_arrive(bp(C.r_empty[rs]));
+      if (KC == 64 && k0 >= p.k) continue;  // the row ends in the first half
       if (!wt.warp(C.empty[as], ((par >> as) & 1u) ^ 1u)) return;
       par ^= 1u << as;
       tc_fence_after();
@@ -336,12 +369,12 @@ __device__ void run_dequant(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, cons
         expand8<BF>(v[j].y, zz[j], o + 4);
         expand8<BF>(v[j].z, zz[j], o + 8);
         expand8<BF>(v[j].w, zz[j], o + 12);
-        tmem_st8(acol + as * 64 + j * 16, o);
-        tmem_st8(acol + as * 64 + j * 16 + 8, o + 8);
+        tmem_st8(acol + as * Cfg<G>::A_COLS + j * 16, o);
+        tmem_st8(acol + as * Cfg<G>::A_COLS + j * 16 + 8, o + 8);
       }
       tmem_wait_st();
       warp_arrive(C.full[as]);
-      as = as + 1 == NS ? 0 : as + 1;
+      as = KC == 128 ? (as + 1 == NS ? 0u : as + 1) : (as + 2) % NS;
     }
   }
 }
@@ -409,12 +442,13 @@ __device__ __forceinline__ uint32_t load_u16_here(const uint16_t* p) {
   return v;
 }
 
+template <int G>
 __device__ void run_epilogue(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, const Waiter& wt) {
   const Q4Params& p = a.p;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int set = w >> 2, quarter = w & 3;
   const uint32_t col = tmem + ((uint32_t)(quarter * 32) << 16) + 64u * set;
-  uint32_t par = 0;  // phases of the two accumulators
+  Place<Cfg<G>::NACC> pc{0u, 0u};
   for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
     const Tile T = tile_of(a, t);
     const int row = T.row0 + quarter * 32 + lane;
@@ -427,16 +461,15 @@ __device__ void run_epilogue(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, con
     for (int g = 0; g < p.ng; ++g) {
       const float s = p.scale_type == MOE_T_BF16 ? __uint_as_float(next << 16) : half_bits_to_float(next);
       if (g + 1 < p.ng) next = load_u16_here(srow + g + 1);
-      const uint32_t r0 = T.n > HALF ? 0u : (uint32_t)g & 1u;  // as the MMA issuer picks them
-      if (!wt.warp(C.acc_full[r0], (par >> r0) & 1u)) return;
-      par ^= 1u << r0;
+      if (!wt.warp(C.acc_full[pc.i], pc.parity())) return;
       tc_fence_after();
-      drain(col + r0 * HALF, np0, s, R0, C.acc_empty[r0]);
+      drain(col + pc.i * HALF, np0, s, R0, C.acc_empty[pc.i]);
+      pc.next();
       if (T.n > HALF) {
-        if (!wt.warp(C.acc_full[1], (par >> 1) & 1u)) return;
-        par ^= 2u;
+        if (!wt.warp(C.acc_full[pc.i], pc.parity())) return;
         tc_fence_after();
-        drain(col + HALF, np1, s, R1, C.acc_empty[1]);
+        drain(col + pc.i * HALF, np1, s, R1, C.acc_empty[pc.i]);
+        pc.next();
       }
     }
     store_cols(p, T.row0, quarter * 32 + lane, T.tok0 + 64 * set, np0, R0);
@@ -449,20 +482,20 @@ template <bool BF, int G>
 __global__ void __launch_bounds__(NTHR, 1) k_q4_gemm(const __grid_constant__ Q4GemmArgs a) {
   extern __shared__ __align__(1024) uint8_t raw_smem[];
   uint8_t* sm = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
-  uint8_t* raw = sm + NS * B_STAGE;
+  uint8_t* raw = sm + Cfg<G>::NS * Cfg<G>::B_STAGE;
   GemmCtl& C = *reinterpret_cast<GemmCtl*>(raw + NSR * RAW_STAGE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_launch_dependents();
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(bp(C.full[i]), 1 + NDW);  // the copy of x and the warps that write A
+    for (int i = 0; i < Cfg<G>::NS; ++i) {
+      mbar_init(bp(C.full[i]), 1 + NDW / 2 * Cfg<G>::SUBS);  // the copy of x and the warps that write A
       mbar_init(bp(C.empty[i]), (uint32_t)a.cl);
     }
     for (int i = 0; i < NSR; ++i) {
       mbar_init(bp(C.r_full[i]), 1);
       mbar_init(bp(C.r_empty[i]), NDW);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < Cfg<G>::NACC; ++i) {
       mbar_init(bp(C.acc_full[i]), 1);
       mbar_init(bp(C.acc_empty[i]), NEW);
     }
@@ -482,14 +515,14 @@ __global__ void __launch_bounds__(NTHR, 1) k_q4_gemm(const __grid_constant__ Q4G
 
   if (warp < NEW) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_EPI));
-    run_epilogue(a, C, tmem, wt);
+    run_epilogue<G>(a, C, tmem, wt);
   } else if (warp < NEW + NDW) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_DEQ));
-    run_dequant<BF>(a, C, tmem, raw, wt);
+    run_dequant<BF, G>(a, C, tmem, raw, wt);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_REST));
     if (warp == W_MMA) run_mma<BF, G>(a, C, tmem, b_smem, wt);
-    else if (warp == W_TMA && lane == 0) run_x(a, C, b_smem, wt);
+    else if (warp == W_TMA && lane == 0) run_x<G>(a, C, b_smem, wt);
     else if (warp == W_RAW && lane == 0) run_raw(a, C, r_smem, wt);
   }
   __syncwarp();
@@ -514,7 +547,7 @@ int launch_gemm(Q4GemmArgs& a, int mt, int sms, cudaStream_t s) {
     // the register trade needs the launch to hold what the shares add up to
     cudaFuncAttributes fa{};
     if (cudaFuncGetAttributes(&fa, k_q4_gemm<BF, G>) != cudaSuccess || fa.numRegs != REG_LAUNCH) return MOE_ERR_CUDA;
-    if (cudaFuncSetAttribute(k_q4_gemm<BF, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES) !=
+    if (cudaFuncSetAttribute(k_q4_gemm<BF, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES<G>) !=
         cudaSuccess)
       return MOE_ERR_CUDA;
     // clusters of two that the GPU holds at once
@@ -525,7 +558,7 @@ int launch_gemm(Q4GemmArgs& a, int mt, int sms, cudaStream_t s) {
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3((unsigned)(sms / 2 * 2));
     lc.blockDim = dim3(NTHR);
-    lc.dynamicSmemBytes = SMEM_BYTES;
+    lc.dynamicSmemBytes = SMEM_BYTES<G>;
     lc.attrs = at;
     lc.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&pairs, k_q4_gemm<BF, G>, &lc) != cudaSuccess) return MOE_ERR_CUDA;
@@ -535,7 +568,7 @@ int launch_gemm(Q4GemmArgs& a, int mt, int sms, cudaStream_t s) {
   a.tiles = (mt + a.cl - 1) / a.cl * a.nt;
   const int grid = (a.tiles < fit ? a.tiles : fit) * a.cl;
   if (grid < 1) return MOE_ERR_CUDA;
-  return launch_overlapped(k_q4_gemm<BF, G>, dim3((unsigned)grid), dim3(NTHR), SMEM_BYTES, s, a, a.cl);
+  return launch_overlapped(k_q4_gemm<BF, G>, dim3((unsigned)grid), dim3(NTHR), SMEM_BYTES<G>, s, a, a.cl);
 }
 
 }  // namespace
@@ -543,7 +576,7 @@ int launch_gemm(Q4GemmArgs& a, int mt, int sms, cudaStream_t s) {
 int launch_q4_gemm(const Q4Params& p, unsigned* status, int sms, cudaStream_t s) {
   Q4GemmArgs a{};
   if (!make_map_2d(&a.map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, (uint64_t)p.k / 2, (uint64_t)p.n, (uint64_t)p.k / 2,
-                   KC / 2, TM, 64) ||
+                   RAW_K / 2, TM, 64) ||
       !make_map_2d(&a.map_x, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.x, (uint64_t)p.k, (uint64_t)p.m, (uint64_t)p.ldx * 2, KS,
                    BBOX, 128))
     return MOE_ERR_CUDA;
