@@ -691,11 +691,18 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
   const Ws w = q4_ws();
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.status = &reinterpret_cast<Ctrl*>(base + w.ctrl)->status;
-  // Up to sixteen tokens two passes over the weights cost less than the tiles'
-  // dequantisation (131072 x 5120: 2 x 64 us against 165 us; 5120 x 2304: 13 us
-  // against 16 us), from there on more.  (The tiles address out by 32-bit
-  // offsets within a tile: not for pitches above 2^24.)
-  if (p0.m > 2 * DECODE_MAX_M && p0.ldo <= (1 << 24)) return launch_q4_gemm(p0, a.status, sms, s);
+  // More than eight tokens: passes of eight over the weights (6.5 us each and
+  // the weights at 5.6 TB/s) against tiles of 128 rows (3 us, and 0.5 us for each
+  // 128 k of the tiles an SM takes).  Measured at 16 tokens: 131072 x 5120, 125
+  // us in passes, 143 us in tiles; 5120 x 2304, 16.5 us against 12.4 us.  (The
+  // tiles address out by 32-bit offsets within a tile: not for pitches above
+  // 2^24.)
+  if (p0.m > DECODE_MAX_M && p0.ldo <= (1 << 24)) {
+    const long long passes = (p0.m + DECODE_MAX_M - 1) / DECODE_MAX_M;
+    const long long ns_passes = passes * (6500 + (long long)p0.n * p0.k / 2 / 5600);
+    const long long ns_tiles = 3000 + 500ll * (((p0.n + 127) / 128 + sms - 1) / sms) * ((p0.k + 127) / 128);
+    if (ns_tiles < ns_passes) return launch_q4_gemm(p0, a.status, sms, s);
+  }
   if (!make_map_2d(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p0.w, (uint64_t)p0.k / 2, (uint64_t)p0.n, (uint64_t)p0.k / 2,
                    BOX_K / 2, BOX_ROWS, 128))
     return MOE_ERR_CUDA;

@@ -257,10 +257,12 @@ __device__ __forceinline__ bool mma_tile(const Q4GemmArgs& a, GemmCtl& C, uint32
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           if (h == 0 && gi == 0 && !wt.warp(C.full[st], (full_par >> st) & 1u)) return false;
-          if (!wt.warp(C.acc_empty[pc.i], pc.parity() ^ 1u)) return false;
+          // two halves and two accumulators: the half names its own
+          const uint32_t reg = NH == 2 && Cfg<G>::NACC == 2 ? (uint32_t)h : pc.i;
+          if (!wt.warp(C.acc_empty[reg], ((pc.phases >> reg) & 1u) ^ 1u)) return false;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t d = tmem + pc.i * HALF, id = h ? id1 : id0;
+            const uint32_t d = tmem + reg * HALF, id = h ? id1 : id0;
             // k past the end of the row meets zeros of x (the copies fill them in)
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
@@ -270,7 +272,7 @@ __device__ __forceinline__ bool mma_tile(const Q4GemmArgs& a, GemmCtl& C, uint32
                               2u * (step % 4),
                           id, i > 0);
             }
-            umma_commit(bp(C.acc_full[pc.i]));
+            umma_commit(bp(C.acc_full[reg]));
             if (h == NH - 1 && frees) {  // the stage is free once these are done
               if (a.cl > 1) umma_commit_multi(bp(C.empty[st]), mask);
               else umma_commit(bp(C.empty[st]));
@@ -294,6 +296,7 @@ __device__ void run_mma(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, uint32_t
   Place<Cfg<G>::NACC> pc{0u, 0u};
   for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
     const Tile T = tile_of(a, t);
+    pc.i = 0u;  // every tile begins with the first accumulator
     const bool ok = T.n > HALF ? mma_tile<BF, G, 2>(a, C, tmem, bdesc0, wt, T.n, chunks, mask, full_par, pc)
                                : mma_tile<BF, G, 1>(a, C, tmem, bdesc0, wt, T.n, chunks, mask, full_par, pc);
     if (!ok) break;
@@ -457,6 +460,7 @@ __device__ void run_epilogue(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, con
     float R0[64], R1[64];
 #pragma unroll
     for (int j = 0; j < 64; ++j) R0[j] = R1[j] = 0.f;
+    pc.i = 0u;
     uint32_t next = load_u16_here(srow);
     for (int g = 0; g < p.ng; ++g) {
       const float s = p.scale_type == MOE_T_BF16 ? __uint_as_float(next << 16) : half_bits_to_float(next);
