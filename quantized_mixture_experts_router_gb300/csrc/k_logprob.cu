@@ -9,7 +9,7 @@
 //  - A row belongs to a cluster of 1..16 blocks (the fewer rows the more), a
 //    contiguous slice each, whose results meet in distributed shared memory; a
 //    cluster walks through several rows when there are many.
-//  - Each warp streams its own 2 KB pieces of the slice with bulk copies into a
+//  - Each warp streams its own pieces (4 KB of f32, 2 KB of 16 bits) of the slice with bulk copies into a
 //    ring of its own, across the ends of rows, so that the loads in flight cost
 //    no registers and warps meet twice a row only.  (Units of eight entries that
 //    the row begins or ends inside are read entry by entry.)
@@ -39,14 +39,21 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int THREADS = 256;
-constexpr int BLOCKS_PER_SM = 4;
 constexpr int WARPS = THREADS / 32;
 constexpr int CAP = 768;              // keys of the candidate buffer
 constexpr int MAX_CLUSTER = 16;
 constexpr int SEGS = 2 * THREADS;     // piece maxima of a row
 constexpr int STAGES = 2;             // pieces of a warp's ring
-constexpr uint32_t PIECE_BYTES = 2048;
-constexpr uint32_t RING_BYTES = WARPS * STAGES * PIECE_BYTES;
+// Bytes of a piece and blocks an SM holds: f32 rows are long and take few
+// instructions a byte, 16-bit rows need the warps (512 f32 rows of 131072: 60 us
+// with 4 KB pieces and two blocks, 66 us with 2 KB and four, when this was chosen; 1000 bf16 rows of
+// 50001: 55 and 43 us).
+template <int T>
+constexpr uint32_t PIECE_BYTES = T == MOE_T_F32 ? 4096 : 2048;
+template <int T>
+constexpr int BLOCKS_PER_SM = T == MOE_T_F32 ? 2 : 4;
+template <int T>
+constexpr uint32_t RING_BYTES = WARPS * STAGES * PIECE_BYTES<T>;
 constexpr uint64_t TIMEOUT_NS = 2000000000ull;  // of one wait for a copy
 constexpr float LOWEST = -3.4028234663852886e38f;
 constexpr float FAR = -1.0e30f;       // a difference whose exponential is zero, but whose product with it is not NaN
@@ -73,7 +80,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-__device__ __forceinline__ float min3(float a, float b, float c) { return fminf(fminf(a, b), c); }
 
 // S += e, U += e d with e = exp2(d k), d = x - M, for eight entries; CLAMP: an
 // infinite d counts as FAR (the product with its e = 0 is 0 then, not NaN).
@@ -141,7 +147,7 @@ __device__ __forceinline__ u64 warp_merge(u64 a, u64 b) {
 }
 
 template <int T>
-constexpr int PIECE_UNITS = PIECE_BYTES / (8 * (T == MOE_T_F32 ? 4 : 2));
+constexpr int PIECE_UNITS = PIECE_BYTES<T> / (8 * (T == MOE_T_F32 ? 4 : 2));
 
 // f32 as an unsigned number of the same order (0 for "none").
 __device__ __forceinline__ unsigned ordered(float x) {
@@ -333,18 +339,18 @@ struct Slice {
 };
 
 template <int T, bool MASK, bool by_piece>
-__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const LogprobArgs a) {
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(const LogprobArgs a) {
   extern __shared__ __align__(128) uint8_t rings[];
   __shared__ Shared sh;
   const LogprobParams& p = a.p;
   constexpr int PU = PIECE_UNITS<T>, B = PU / 32;
-  constexpr uint32_t UB = PIECE_BYTES / PU;  // bytes of a unit
+  constexpr uint32_t UB = PIECE_BYTES<T> / PU;  // bytes of a unit
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int K = p.c.top_k;
   const uint32_t rank = a.cl > 1 ? cluster_rank() : 0u;
   const int step = (int)gridDim.x / a.cl, r0 = (int)blockIdx.x / a.cl;
   uint64_t* full = reinterpret_cast<uint64_t*>(sh.full[warp]);
-  uint8_t* ring = rings + warp * STAGES * PIECE_BYTES;
+  uint8_t* ring = rings + warp * STAGES * PIECE_BYTES<T>;
   grid_launch_dependents();
   if (lane == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(full + i, 1);
@@ -370,19 +376,19 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
       cu.end = (uint32_t)s.u1 * UB;
       cu.lo = (uint32_t)s.row.inner_begin() * UB;
       cu.hi = min(cu.end, (uint32_t)s.row.inner_end() * UB);
-      at = (uint32_t)s.u0 * UB + (uint32_t)warp * PIECE_BYTES;
+      at = (uint32_t)s.u0 * UB + (uint32_t)warp * PIECE_BYTES<T>;
       cu.at = at;
     }
     const uint32_t st = cu.fetched % STAGES;
-    const uint32_t lo = max(at, cu.lo), hi = min(at + PIECE_BYTES, cu.hi);
+    const uint32_t lo = max(at, cu.lo), hi = min(at + PIECE_BYTES<T>, cu.hi);
     if (lo < hi) {
       mbar_arrive_expect_tx(full + st, hi - lo);
-      bulk_g2s(ring + st * PIECE_BYTES + (lo - at), cu.base + lo, hi - lo, full + st);
+      bulk_g2s(ring + st * PIECE_BYTES<T> + (lo - at), cu.base + lo, hi - lo, full + st);
     } else {
       mbar_arrive(full + st);  // nothing but units the row begins or ends inside
     }
     ++cu.fetched;
-    cu.at = at + WARPS * PIECE_BYTES;
+    cu.at = at + WARPS * PIECE_BYTES<T>;
   };
   if (lane == 0) {
     sh.cursor[warp] = Cursor{nullptr, 0u, 0u, 0u, 0u, r0 - step, 0u};
@@ -424,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
     for (int i0 = warp; i0 < sl.np; i0 += WARPS) {
       const int b0 = u0 + i0 * PU;
       const uint32_t st = used % STAGES;
-      const uint8_t* mem = ring + st * PIECE_BYTES + lane * UB;
+      const uint8_t* mem = ring + st * PIECE_BYTES<T> + lane * UB;
       if (!mbar_try_wait(full + st, (used / STAGES) & 1u))
         mbar_wait_for(full + st, (used / STAGES) & 1u, TIMEOUT_NS, &sh.failed);
       // where every lane's maximum stays below `lim`, the units add to the
@@ -432,7 +438,6 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
       float lim = fminf(ref_hi, xr), Mp = LOWEST;
       auto work = [&](const float (&x)[8], unsigned lanes) {
         const float mv = fmaxf(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]));
-        const float lo = fminf(min3(min3(x[0], x[1], x[2]), x[3], x[4]), min3(x[5], x[6], x[7]));
         Mp = fmaxf(Mp, mv);
         if (__any_sync(lanes, mv >= lim)) {
           if (mv > ref_hi) {
@@ -445,16 +450,31 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
           }
           above += count_above(x, xr);
         }
-        if (__any_sync(lanes, lo <= FAR || ref >= -FAR)) add_unit<true>(x, ref, k, S2, U2);
-        else add_unit<false>(x, ref, k, S2, U2);
       };
       const bool plain = !MASK && b0 >= row.inner_begin() && b0 + PU <= min(u1, row.inner_end());  // whole units alone
       if (plain) {
+        const float2 S0 = S2, U0 = U2;
+        const float ref0 = ref;
 #pragma unroll 2
         for (int i = 0; i < B; ++i) {
           float x[8];
           row.inner(mem + (uint32_t)i * (32 * UB)).to_f32(x);
           work(x, 0xffffffffu);
+          add_unit<false>(x, ref, k, S2, U2);
+        }
+        // an entry too far below the reference (-inf) has made 0 * inf of its
+        // product: take the piece's sums again, with a bound on the difference
+        const float u = U2.x + U2.y, u0 = U0.x + U0.y;
+        if (__any_sync(0xffffffffu, u != u && u0 == u0)) {
+          const float d = fmaxf(ref0 - ref, FAR), e = ex2(d * k);
+          U2 = make_float2((U0.x + S0.x * d) * e, (U0.y + S0.y * d) * e);
+          S2 = make_float2(S0.x * e, S0.y * e);
+#pragma unroll 1
+          for (int i = 0; i < B; ++i) {
+            float x[8];
+            row.inner(mem + (uint32_t)i * (32 * UB)).to_f32(x);
+            add_unit<true>(x, ref, k, S2, U2);
+          }
         }
       } else {
 #pragma unroll 1
@@ -468,6 +488,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) k_token_logprobs(const
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = (c.ok >> e) & 1u ? x[e] : -pos_inf();
             work(x, lanes);
+            add_unit<true>(x, ref, k, S2, U2);
           }
           __syncwarp();
         }
@@ -673,13 +694,13 @@ int launch(const LogprobArgs& a, int sms, cudaStream_t s) {
   if (attr_dev != dev) {
     if (cudaFuncSetAttribute(k_token_logprobs<T, MASK, BY_PIECE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaFuncSetAttribute(k_token_logprobs<T, MASK, BY_PIECE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)RING_BYTES) != cudaSuccess)
+                             (int)RING_BYTES<T>) != cudaSuccess)
       return MOE_ERR_CUDA;
     attr_dev = dev;
   }
-  // four blocks per SM; clusters of more than two blocks leave some SMs out, so
+  // as many blocks as the SMs hold; clusters of more than two blocks leave some SMs out, so
   // that their number comes from the runtime
-  int clusters = BLOCKS_PER_SM * sms / a.cl;
+  int clusters = BLOCKS_PER_SM<T> * sms / a.cl;
   if (a.cl > 2) {
     static int fit[MAX_CLUSTER + 1] = {}, fit_dev = -1;
     if (fit_dev != dev) {
@@ -692,9 +713,9 @@ int launch(const LogprobArgs& a, int sms, cudaStream_t s) {
       at[0].val.clusterDim.x = (unsigned)a.cl;
       at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
       cudaLaunchConfig_t lc{};
-      lc.gridDim = dim3((unsigned)(BLOCKS_PER_SM * sms / a.cl * a.cl));
+      lc.gridDim = dim3((unsigned)(BLOCKS_PER_SM<T> * sms / a.cl * a.cl));
       lc.blockDim = dim3(THREADS);
-      lc.dynamicSmemBytes = RING_BYTES;
+      lc.dynamicSmemBytes = RING_BYTES<T>;
       lc.attrs = at;
       lc.numAttrs = 1;
       if (cudaOccupancyMaxActiveClusters(&fit[a.cl], k_token_logprobs<T, MASK, BY_PIECE>, &lc) != cudaSuccess || fit[a.cl] < 1)
@@ -704,16 +725,16 @@ int launch(const LogprobArgs& a, int sms, cudaStream_t s) {
   }
   const int grid = (a.p.m < clusters ? a.p.m : clusters) * a.cl;
   return launch_overlapped(k_token_logprobs<T, MASK, BY_PIECE>, dim3((unsigned)grid), dim3(THREADS),
-                           RING_BYTES, s, a, a.cl);
+                           RING_BYTES<T>, s, a, a.cl);
 }
 
 template <int T>
 int launch_m(const LogprobArgs& a, int sms, cudaStream_t s) {
   // the maxima of pieces rather than threads from 64 pieces a slice on: with
-  // 256 pieces (512 rows of 131072 f32) the threads' units are spread over so
-  // much memory that reading them again costs 37 us against 20, with 49 pieces
-  // (1000 rows of 50001 bf16) the maxima cost 9 us more than they save
-  const bool by_piece = a.p.c.vocab / a.cl >= 64 * (int)PIECE_BYTES / type_bytes(T);
+  // 128 pieces (512 rows of 131072 f32) a thread's units are spread over so much
+  // memory that reading them again makes 75 us of 58; with 49 pieces (1000 rows of
+  // 50001 bf16) the pieces' maxima make 50 us of 42
+  const bool by_piece = a.p.c.vocab / a.cl >= 64 * (int)PIECE_BYTES<T> / type_bytes(T);
   if (by_piece) return a.p.allowed ? launch<T, true, true>(a, sms, s) : launch<T, false, true>(a, sms, s);
   return a.p.allowed ? launch<T, true, false>(a, sms, s) : launch<T, false, false>(a, sms, s);
 }
@@ -727,11 +748,11 @@ int launch_token_logprobs(const LogprobParams& p, cudaStream_t s) {
     return MOE_ERR_CUDA;
   LogprobArgs a{};
   a.p = p;
-  // blocks per row: enough to fill the GPU, while a block's slice
-  // has a piece for each of its warps
-  const int piece = (int)PIECE_BYTES / type_bytes(p.c.logit_type);
+  // blocks per row: enough to fill the GPU (four blocks an SM), while a block's
+  // slice has 2 KB for each of its warps
+  const int piece = 2048 / type_bytes(p.c.logit_type);
   a.cl = 1;
-  while (a.cl < MAX_CLUSTER && 2ll * p.m * a.cl <= BLOCKS_PER_SM * sms && p.c.vocab / (2 * a.cl) >= WARPS * piece / 2) a.cl *= 2;
+  while (a.cl < MAX_CLUSTER && 2ll * p.m * a.cl <= 4 * sms && p.c.vocab / (2 * a.cl) >= WARPS * piece / 2) a.cl *= 2;
   while ((1 << a.cl_log2) < a.cl) ++a.cl_log2;
   if (p.c.logit_type == MOE_T_F32) return launch_m<MOE_T_F32>(a, sms, s);
   if (p.c.logit_type == MOE_T_BF16) return launch_m<MOE_T_BF16>(a, sms, s);
