@@ -83,11 +83,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(
 
 // S += e, U += e d with e = exp2(d k), d = x - M, for eight entries; CLAMP: an
 // infinite d counts as FAR (the product with its e = 0 is 0 then, not NaN).
-template <bool CLAMP>
-__device__ __forceinline__ void add_unit(const float (&x)[8], float M, float k, float2& S, float2& U) {
+template <bool CLAMP, int N>
+__device__ __forceinline__ void add_unit(const float (&x)[N], float M, float k, float2& S, float2& U) {
   const float2 nm = make_float2(-M, -M), kk = make_float2(k, k);
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
+  for (int e = 0; e < N; e += 2) {
     float2 d = __fadd2_rn(make_float2(x[e], x[e + 1]), nm);
     if (CLAMP) d = make_float2(max_nan(d.x, FAR), max_nan(d.y, FAR));
     const float2 h = __fmul2_rn(d, kk);
@@ -98,10 +98,11 @@ __device__ __forceinline__ void add_unit(const float (&x)[8], float M, float k, 
 }
 
 // How many of eight entries are above r (as 1.0 each: set and packed add).
-__device__ __forceinline__ float count_above(const float (&x)[8], float r) {
+template <int N>
+__device__ __forceinline__ float count_above(const float (&x)[N], float r) {
   float2 c = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
+  for (int e = 0; e < N; e += 2) {
     float2 s;
     asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(s.x) : "f"(x[e]), "f"(r));
     asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(s.y) : "f"(x[e + 1]), "f"(r));
@@ -216,7 +217,7 @@ struct Unit {
   static constexpr int NV = T == MOE_T_F32 ? 2 : 1;
   uint4 v[NV];
   uint32_t ok;  // bit e: entry e is in the row and allowed
-  __device__ __forceinline__ void to_f32(float (&x)[8]) const {
+  __device__ __forceinline__ void to_f32(float* x) const {
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[NV - 1].x, v[NV - 1].y, v[NV - 1].z, v[NV - 1].w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -436,8 +437,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
       // where every lane's maximum stays below `lim`, the units add to the
       // sums alone (the warp decides as one: both ways would cost their sum)
       float lim = fminf(ref_hi, xr), Mp = LOWEST;
-      auto work = [&](const float (&x)[8], unsigned lanes) {
-        const float mv = fmaxf(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]));
+      auto work = [&](const auto& x, unsigned lanes) {
+        constexpr int N = (int)(sizeof(x) / sizeof(float));
+        float mv = max3(x[5], x[6], x[7]), mw = max3(x[0], x[1], x[2]);
+#pragma unroll
+        for (int e = 8; e < N; e += 2) mv = max3(mv, x[e], x[e + 1]);
+        mv = fmaxf(max3(mw, x[3], x[4]), mv);
         Mp = fmaxf(Mp, mv);
         if (__any_sync(lanes, mv >= lim)) {
           if (mv > ref_hi) {
@@ -455,10 +460,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
       if (plain) {
         const float2 S0 = S2, U0 = U2;
         const float ref0 = ref;
-#pragma unroll 2
-        for (int i = 0; i < B; ++i) {
-          float x[8];
+#pragma unroll 1
+        for (int i = 0; i < B; i += 2) {
+          float x[16];
           row.inner(mem + (uint32_t)i * (32 * UB)).to_f32(x);
+          row.inner(mem + (uint32_t)(i + 1) * (32 * UB)).to_f32(x + 8);
           work(x, 0xffffffffu);
           add_unit<false>(x, ref, k, S2, U2);
         }
