@@ -28,6 +28,10 @@
 //    one shared by several blocks through the workspace; the last to arrive
 //    adds all the parts in the order of the runs, so that the result does not
 //    depend on which one that was.
+// Measured: 131072 x 5120, one token: 59 us, 5.9 TB/s (copies reach 6.8): the
+// masks keep the integer pipe 53% busy while warps wait for boxes.  50001 x 2336,
+// five tokens, zeros: 18.7 us, 3.3 TB/s.  512 x 5120, one token: 5.3 us, of which
+// about 3 are the launch, x and the first box's latency one after the other.
 #include <cudaTypedefs.h>
 
 #include "ops.h"
@@ -719,7 +723,7 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
   sms = min(sms, MAX_CTAS);
   for (int t0 = 0; t0 < p0.m;) {
     // x of the pass's tokens stays in shared memory beside two boxes per warp:
-    // 16 warps while it leaves them room, else 12 or 8, else fewer tokens
+    // 20 warps while it leaves them room, else 16, 12 or 8, else fewer tokens
     int warps = MAX_WARPS, tokens = min(p0.m - t0, DECODE_MAX_M);
     auto fits = [&](int wps, int toks) {
       return fixed_bytes(toks, p0.k, p0.ng, wps) + (uint32_t)wps * 2 * BOX_BYTES <= SMEM_MAX;
@@ -729,7 +733,9 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
     const uint32_t fixed = fixed_bytes(tokens, p0.k, p0.ng, warps);
     a.stages = min(MAX_STAGES, (int)((SMEM_MAX - fixed) / ((uint32_t)warps * BOX_BYTES)));
     // Whole row tiles per block save the join between blocks, about as long as
-    // four boxes of a warp; blocks that share row tiles are more even.
+    // four boxes of a warp; blocks that share row tiles are more even (4608 x 5120,
+    // eight tokens: 11.4 us by tile, 14.0 us shared; 512 x 32768, one token: 17.6
+    // and 10.2 us).
     const int even = (total + sms * warps - 1) / (sms * warps);
     const int by_tile = ((tiles + sms - 1) / sms * a.nb + warps - 1) / warps;
     a.by_tile = by_tile <= even + 4;

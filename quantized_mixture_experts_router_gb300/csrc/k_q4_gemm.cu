@@ -18,6 +18,11 @@
 //
 // The running sums of 128 outputs per thread need more registers than an even
 // split of the register file: the warpgroups trade them (setmaxnreg).
+//
+// Measured: 512 tokens, 131072 x 5120, groups of 128: 520 us, 1.32 PFLOP/s (a
+// library bf16 product reaches 1.92).  The hand-overs between the warps that
+// dequantise, issue and drain bound it: the tensor pipe is 55% busy over a
+// shorter call of 32768 rows, memory 9%.
 #include <cudaTypedefs.h>
 
 #include "internal.h"
