@@ -13,16 +13,17 @@
 // so that one is drained while the tensor cores fill the others.
 //
 // x, at 256 tokens a tile, is the larger operand by far (a weight has four
-// bits): a cluster of two blocks takes consecutive row tiles of the same
-// tokens, each block loads its half of the tile's x and multicasts it to both.
+// bits).  Every block loads its own copy; blocks that run at the same time walk
+// through the same k of the same few token tiles, so that x comes from L2
+// (pairs of blocks that each loaded half and copied it to both: 515 us where
+// this takes 497).
 //
 // The running sums of 128 outputs per thread need more registers than an even
 // split of the register file: the warpgroups trade them (setmaxnreg).
 //
-// Measured: 512 tokens, 131072 x 5120, groups of 128: 520 us, 1.32 PFLOP/s (a
-// library bf16 product reaches 1.92).  The hand-overs between the warps that
-// dequantise, issue and drain bound it: the tensor pipe is 55% busy over a
-// shorter call of 32768 rows, memory 9%.
+// Measured: 512 tokens, 131072 x 5120, groups of 128: 497 us in a graph, 1.38
+// PFLOP/s (a library bf16 product reaches 1.92); groups of 64: 773 us.  The
+// hand-overs between the warps that dequantise, issue and drain bound it.
 #include <cudaTypedefs.h>
 
 #include "internal.h"
@@ -74,15 +75,14 @@ struct Q4GemmArgs {
   CUtensorMap map_x;               // x [m][k], box {64 values, 64 rows}
   Q4Params p;
   int tn;                          // tokens per tile: 64, 128 or 256
-  int cl;                          // blocks per cluster: consecutive row tiles, the same tokens
-  int nt, tiles;                   // token tiles; tiles of cl row tiles x one token tile
+  int nt, tiles;                   // token tiles; all tiles
   unsigned* status;
   unsigned long long timeout_ns;
 };
 
 struct GemmCtl {
   unsigned long long full[MAX_NS];    // a stage's A and B are there
-  unsigned long long empty[MAX_NS];   // every block of the cluster is done with them
+  unsigned long long empty[MAX_NS];   // the MMAs are done with them
   unsigned long long r_full[NSR], r_empty[NSR];
   unsigned long long acc_full[MAX_NACC], acc_empty[MAX_NACC];
   unsigned long long done;
@@ -120,34 +120,6 @@ __device__ __forceinline__ void warp_arrive(unsigned long long& b) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bp(b));
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// tma_load_2d into the same place of every block in `mask`, completing on each one's barrier.
-__device__ __forceinline__ void tma_load_2d_multi(uint32_t dst, const void* map, int x, int y, uint64_t* bar,
-                                                  uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
-      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(mask)
-      : "memory");
-}
-
-// umma_commit on the same barrier of every block in `mask`.
-__device__ __forceinline__ void umma_commit_multi(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(mask)
-      : "memory");
-}
-
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
@@ -170,8 +142,8 @@ struct Tile {
 };
 __device__ __forceinline__ Tile tile_of(const Q4GemmArgs& a, int t) {
   Tile T;
-  const int mt = t / a.nt, nt = t - mt * a.nt;  // neighbouring clusters share weight rows
-  T.row0 = (mt * a.cl + (int)cluster_rank()) * TM;
+  const int mt = t / a.nt, nt = t - mt * a.nt;  // neighbouring blocks share weight rows
+  T.row0 = mt * TM;
   T.tok0 = nt * a.tn;
   T.n = (min(a.tn, a.p.m - T.tok0) + 15) & ~15;
   return T;
@@ -181,7 +153,7 @@ __device__ __forceinline__ Tile tile_of(const Q4GemmArgs& a, int t) {
 __device__ void run_raw(const Q4GemmArgs& a, GemmCtl& C, uint32_t raw_smem, const Waiter& wt) {
   const int chunks = (a.p.k + RAW_K - 1) / RAW_K;
   uint32_t u = 0;
-  for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
+  for (int t = (int)blockIdx.x; t < a.tiles; t += (int)gridDim.x) {
     const Tile T = tile_of(a, t);
     for (int c = 0; c < chunks; ++c, ++u) {
       const uint32_t st = u % NSR;
@@ -202,22 +174,19 @@ out:
 template <int G>
 __device__ void run_x(const Q4GemmArgs& a, GemmCtl& C, uint32_t b_smem, const Waiter& wt) {
   constexpr int KC = Cfg<G>::KC, NS = Cfg<G>::NS, SUBS = Cfg<G>::SUBS;
-  const int chunks = (a.p.k + KC - 1) / KC, rank = (int)cluster_rank();
-  const uint16_t mask = (uint16_t)((1u << a.cl) - 1u);
+  const int chunks = (a.p.k + KC - 1) / KC;
   uint32_t par = 0, used = 0;
-  for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
+  for (int t = (int)blockIdx.x; t < a.tiles; t += (int)gridDim.x) {
     const Tile T = tile_of(a, t);
     const int nbox = (T.n + BBOX - 1) / BBOX;
     uint32_t st = 0;
     for (int c = 0; c < chunks; ++c) {
       if (!wt.one(C.empty[st], ((par >> st) & 1u) ^ 1u)) goto out;  // passes at once the first time
       mbar_arrive_expect_tx(bp(C.full[st]), (uint32_t)nbox * BBOX * KC * 2);
-      for (int r = rank; r < SUBS * nbox; r += a.cl) {  // (64 tokens, 64 k)
+      for (int r = 0; r < SUBS * nbox; ++r) {  // (64 tokens, 64 k)
         const int sub = r % SUBS, box = r / SUBS;
         const uint32_t dst = b_smem + st * Cfg<G>::B_STAGE + (uint32_t)sub * B_SUB + (uint32_t)box * (BBOX * 128);
-        const int x = c * KC + sub * KS, y = T.tok0 + box * BBOX;
-        if (a.cl > 1) tma_load_2d_multi(dst, &a.map_x, x, y, bp(C.full[st]), mask);
-        else tma_load_2d(dst, &a.map_x, x, y, bp(C.full[st]));
+        tma_load_2d(dst, &a.map_x, c * KC + sub * KS, T.tok0 + box * BBOX, bp(C.full[st]));
       }
       par ^= 1u << st;
       used |= 1u << st;
@@ -226,13 +195,8 @@ __device__ void run_x(const Q4GemmArgs& a, GemmCtl& C, uint32_t b_smem, const Wa
   }
 out:
   const uint64_t d2 = globaltimer_ns() + a.timeout_ns;
-  for (uint32_t st = 0; st < NS; ++st) {
-    if (!((used >> st) & 1u)) continue;
-    mbar_wait_bounded(bp(C.full[st]), ((par >> st) & 1u) ^ 1u, d2, a.status);
-    // and so do the other blocks' commits to this one's barriers
-    if (!*reinterpret_cast<volatile uint32_t*>(&C.abort))
-      mbar_wait_bounded(bp(C.empty[st]), ((par >> st) & 1u) ^ 1u, d2, a.status);
-  }
+  for (uint32_t st = 0; st < NS; ++st)
+    if ((used >> st) & 1u) mbar_wait_bounded(bp(C.full[st]), ((par >> st) & 1u) ^ 1u, d2, a.status);
 }
 
 // ------------------------------------------------------------ MMA issuer
@@ -242,7 +206,7 @@ out:
 // Every use of an accumulator takes the next one of the ring.
 template <bool BF, int G, int NH>
 __device__ __forceinline__ bool mma_tile(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, uint64_t bdesc0,
-                                         const Waiter& wt, int n, int chunks, uint16_t mask, uint32_t& full_par,
+                                         const Waiter& wt, int n, int chunks, uint32_t& full_par,
                                          Place<Cfg<G>::NACC>& pc) {
   constexpr int KC = Cfg<G>::KC, NS = Cfg<G>::NS;
   constexpr int GPC = KC / G;        // groups per chunk
@@ -278,10 +242,7 @@ __device__ __forceinline__ bool mma_tile(const Q4GemmArgs& a, GemmCtl& C, uint32
                           id, i > 0);
             }
             umma_commit(bp(C.acc_full[reg]));
-            if (h == NH - 1 && frees) {  // the stage is free once these are done
-              if (a.cl > 1) umma_commit_multi(bp(C.empty[st]), mask);
-              else umma_commit(bp(C.empty[st]));
-            }
+            if (h == NH - 1 && frees) umma_commit(bp(C.empty[st]));  // the stage is free once these are done
           }
           pc.next();
         }
@@ -296,14 +257,13 @@ template <bool BF, int G>
 __device__ void run_mma(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, uint32_t b_smem, const Waiter& wt) {
   const int chunks = (a.p.k + Cfg<G>::KC - 1) / Cfg<G>::KC;
   const uint64_t bdesc0 = umma_desc(b_smem);
-  const uint16_t mask = (uint16_t)((1u << a.cl) - 1u);
   uint32_t full_par = 0;
   Place<Cfg<G>::NACC> pc{0u, 0u};
-  for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
+  for (int t = (int)blockIdx.x; t < a.tiles; t += (int)gridDim.x) {
     const Tile T = tile_of(a, t);
     pc.i = 0u;  // every tile begins with the first accumulator
-    const bool ok = T.n > HALF ? mma_tile<BF, G, 2>(a, C, tmem, bdesc0, wt, T.n, chunks, mask, full_par, pc)
-                               : mma_tile<BF, G, 1>(a, C, tmem, bdesc0, wt, T.n, chunks, mask, full_par, pc);
+    const bool ok = T.n > HALF ? mma_tile<BF, G, 2>(a, C, tmem, bdesc0, wt, T.n, chunks, full_par, pc)
+                               : mma_tile<BF, G, 1>(a, C, tmem, bdesc0, wt, T.n, chunks, full_par, pc);
     if (!ok) break;
   }
   __syncwarp();
@@ -345,7 +305,7 @@ __device__ void run_dequant(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, cons
   const uint32_t base = BF ? 0x43004300u : 0x64006400u;
   const uint32_t acol = tmem + ((uint32_t)(quarter * 32) << 16) + Cfg<G>::A_COL0 + (KC == 128 ? (uint32_t)hi * 32u : 0u);
   uint32_t ru = 0, par = 0;  // raw stages walked; phases of the A stages
-  for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
+  for (int t = (int)blockIdx.x; t < a.tiles; t += (int)gridDim.x) {
     const Tile T = tile_of(a, t);
     const uint8_t* zrow = p.zeros && T.row0 + r < p.n ? p.zeros + (size_t)(T.row0 + r) * p.ng : nullptr;
     uint32_t as = KC == 128 ? 0u : (uint32_t)hi;
@@ -457,7 +417,7 @@ __device__ void run_epilogue(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, con
   const int set = w >> 2, quarter = w & 3;
   const uint32_t col = tmem + ((uint32_t)(quarter * 32) << 16) + 64u * set;
   Place<Cfg<G>::NACC> pc{0u, 0u};
-  for (int t = (int)blockIdx.x / a.cl; t < a.tiles; t += (int)gridDim.x / a.cl) {
+  for (int t = (int)blockIdx.x; t < a.tiles; t += (int)gridDim.x) {
     const Tile T = tile_of(a, t);
     const int row = T.row0 + quarter * 32 + lane;
     const uint16_t* srow = p.scales + (size_t)min(row, p.n - 1) * p.ng;
@@ -498,7 +458,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_q4_gemm(const __grid_constant__ Q4G
   if (tid == 0) {
     for (int i = 0; i < Cfg<G>::NS; ++i) {
       mbar_init(bp(C.full[i]), 1 + NDW / 2 * Cfg<G>::SUBS);  // the copy of x and the warps that write A
-      mbar_init(bp(C.empty[i]), (uint32_t)a.cl);
+      mbar_init(bp(C.empty[i]), 1);
     }
     for (int i = 0; i < NSR; ++i) {
       mbar_init(bp(C.r_full[i]), 1);
@@ -515,7 +475,6 @@ __global__ void __launch_bounds__(NTHR, 1) k_q4_gemm(const __grid_constant__ Q4G
   if (warp == 0) tmem_alloc(&C.tmem, 512);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // every block's barriers are ready for the others' copies and commits
   tc_fence_after();
   const uint32_t tmem = C.tmem;
   const uint32_t b_smem = smem_u32(sm), r_smem = smem_u32(raw);
@@ -540,7 +499,6 @@ __global__ void __launch_bounds__(NTHR, 1) k_q4_gemm(const __grid_constant__ Q4G
   if (warp == 0 && lane == 0) mbar_wait_bounded(bp(C.done), 0u, globaltimer_ns() + a.timeout_ns, a.status);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // no other block still copies into this one's memory or commits to its barriers
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -548,8 +506,8 @@ __global__ void __launch_bounds__(NTHR, 1) k_q4_gemm(const __grid_constant__ Q4G
 }
 
 template <bool BF, int G>
-int launch_gemm(Q4GemmArgs& a, int mt, int sms, cudaStream_t s) {
-  static int attr_dev = -1, pairs = 0;
+int launch_gemm(const Q4GemmArgs& a, int sms, cudaStream_t s) {
+  static int attr_dev = -1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (attr_dev != dev) {
@@ -559,25 +517,10 @@ int launch_gemm(Q4GemmArgs& a, int mt, int sms, cudaStream_t s) {
     if (cudaFuncSetAttribute(k_q4_gemm<BF, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES<G>) !=
         cudaSuccess)
       return MOE_ERR_CUDA;
-    // clusters of two that the GPU holds at once
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3((unsigned)(sms / 2 * 2));
-    lc.blockDim = dim3(NTHR);
-    lc.dynamicSmemBytes = SMEM_BYTES<G>;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&pairs, k_q4_gemm<BF, G>, &lc) != cudaSuccess) return MOE_ERR_CUDA;
     attr_dev = dev;
   }
-  const int fit = a.cl == 2 ? pairs : sms;
-  a.tiles = (mt + a.cl - 1) / a.cl * a.nt;
-  const int grid = (a.tiles < fit ? a.tiles : fit) * a.cl;
-  if (grid < 1) return MOE_ERR_CUDA;
-  return launch_overlapped(k_q4_gemm<BF, G>, dim3((unsigned)grid), dim3(NTHR), SMEM_BYTES<G>, s, a, a.cl);
+  const int grid = a.tiles < sms ? a.tiles : sms;
+  return launch_overlapped(k_q4_gemm<BF, G>, dim3((unsigned)grid), dim3(NTHR), SMEM_BYTES<G>, s, a);
 }
 
 }  // namespace
@@ -606,11 +549,11 @@ int launch_q4_gemm(const Q4Params& p, unsigned* status, int sms, cudaStream_t s)
       a.nt = nt;
     }
   }
-  a.cl = mt * a.nt <= sms ? 1 : 2;
+  a.tiles = mt * a.nt;
   const bool bf = p.x_type == MOE_T_BF16;
-  if (p.group == 128) return bf ? launch_gemm<true, 128>(a, mt, sms, s) : launch_gemm<false, 128>(a, mt, sms, s);
-  if (p.group == 64) return bf ? launch_gemm<true, 64>(a, mt, sms, s) : launch_gemm<false, 64>(a, mt, sms, s);
-  return bf ? launch_gemm<true, 32>(a, mt, sms, s) : launch_gemm<false, 32>(a, mt, sms, s);
+  if (p.group == 128) return bf ? launch_gemm<true, 128>(a, sms, s) : launch_gemm<false, 128>(a, sms, s);
+  if (p.group == 64) return bf ? launch_gemm<true, 64>(a, sms, s) : launch_gemm<false, 64>(a, sms, s);
+  return bf ? launch_gemm<true, 32>(a, sms, s) : launch_gemm<false, 32>(a, sms, s);
 }
 
 }  // namespace moe
