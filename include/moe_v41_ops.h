@@ -109,7 +109,7 @@ typedef struct {
   int32_t vocab;       /* 1..2^28 */
   int32_t logit_type;  /* MOE_T_* */
   int32_t top_k;       /* 0..32 */
-  float temperature;   /* > 0, finite */
+  float temperature;   /* 1e-36..1e36 */
 } moe_v41_logprob_cfg;
 
 /* logits [m, vocab] (pitch ld, aligned to the element), allowed u32

@@ -1,7 +1,7 @@
 // Log probabilities of given tokens, entropy and the top alternatives of each
 // row of logits.  With z = logit / T over the allowed entries, M = max z,
-// S = sum exp(z - M), U = sum exp(z - M) (z - M):
-//   lse = M + log S,  logprob = (z_t - M) - log S,  entropy = log S - U / S
+// S = sum exp(z - M), U = sum exp(z - M) (z - M) / log 2:
+//   lse = M + log S,  logprob = (z_t - M) - log S,  entropy = log S - U / S log 2
 // (differences are taken around M before anything is rounded away, so that
 // large common offsets cost no digits).
 //
@@ -60,7 +60,7 @@ template <int T>
 constexpr uint32_t RING_BYTES = WARPS * STAGES * PIECE_BYTES<T>;
 constexpr uint64_t TIMEOUT_NS = 2000000000ull;  // of one wait for a copy
 constexpr float LOWEST = -3.4028234663852886e38f;
-constexpr float FAR = -1.0e30f;       // a difference whose exponential is zero, but whose product with it is not NaN
+constexpr float FAR = -256.0f;        // an exponent of two whose power is zero, but whose product with it is not NaN
 
 __device__ __forceinline__ float pos_inf() { return __uint_as_float(0x7F800000u); }
 
@@ -85,19 +85,20 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
-// S += e, U += e d with e = exp2(d k), d = x - M, for eight entries; CLAMP: an
-// infinite d counts as FAR (the product with its e = 0 is 0 then, not NaN).
+// S += e, U += e h with e = exp2(h), h = (x - M) k, for eight entries; CLAMP: an
+// infinite h counts as FAR (the product with its e = 0 is 0 then, not NaN).  U is
+// kept in h, not in x - M, so that neither FAR nor U's size depends on the
+// temperature.
 template <bool CLAMP, int N>
 __device__ __forceinline__ void add_unit(const float (&x)[N], float M, float k, float2& S, float2& U) {
   const float2 nm = make_float2(-M, -M), kk = make_float2(k, k);
 #pragma unroll
   for (int e = 0; e < N; e += 2) {
-    float2 d = __fadd2_rn(make_float2(x[e], x[e + 1]), nm);
-    if (CLAMP) d = make_float2(max_nan(d.x, FAR), max_nan(d.y, FAR));
-    const float2 h = __fmul2_rn(d, kk);
+    float2 h = __fmul2_rn(__fadd2_rn(make_float2(x[e], x[e + 1]), nm), kk);
+    if (CLAMP) h = make_float2(max_nan(h.x, FAR), max_nan(h.y, FAR));
     const float2 w = make_float2(ex2(h.x), ex2(h.y));
     S = __fadd2_rn(S, w);
-    U = __ffma2_rn(w, d, U);
+    U = __ffma2_rn(w, h, U);
   }
 }
 
@@ -316,8 +317,8 @@ struct LogprobArgs {
 // whose order is fixed.
 __device__ __forceinline__ Stat warp_join(Stat st, float k) {
   const float M = from_ordered(__reduce_max_sync(0xffffffffu, ordered(st.M)));
-  const float d = max_nan(st.M - M, FAR), e = ex2(d * k);
-  st.U = (st.U + st.S * d) * e;
+  const float h = max_nan((st.M - M) * k, FAR), e = ex2(h);
+  st.U = (st.U + st.S * h) * e;
   st.S *= e;
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
   }
   const float rt = 1.0f / p.c.temperature;
   const float k = 1.4426950408889634f * rt;
-  const float slack = 8.0f / k;
+  const float slack = 8.0f / k;  // at most 6e36: an entry's difference from the reference stays finite upwards
 
   auto target_of = [&](int r) { return p.target && r < p.m ? __ldg(p.target + r) : -1; };
   auto target_logit = [&](int r, int t) {  // a masked one counts as -inf
@@ -450,8 +451,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
         Mp = fmaxf(Mp, mv);
         if (__any_sync(lanes, mv >= lim)) {
           if (mv > ref_hi) {
-            const float d = fmaxf(ref - mv, FAR), e = ex2(d * k);
-            U2 = make_float2((U2.x + S2.x * d) * e, (U2.y + S2.y * d) * e);
+            const float h = fmaxf((ref - mv) * k, FAR), e = ex2(h);
+            U2 = make_float2((U2.x + S2.x * h) * e, (U2.y + S2.y * h) * e);
             S2 = make_float2(S2.x * e, S2.y * e);
             ref = mv;
             ref_hi = mv + slack;
@@ -473,11 +474,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
           add_unit<false>(x, ref, k, S2, U2);
         }
         // an entry too far below the reference (-inf) has made 0 * inf of its
-        // product: take the piece's sums again, with a bound on the difference
+        // product: take the piece's sums again, with a bound on the exponent
         const float u = U2.x + U2.y, u0 = U0.x + U0.y;
         if (__any_sync(0xffffffffu, u != u && u0 == u0)) {
-          const float d = fmaxf(ref0 - ref, FAR), e = ex2(d * k);
-          U2 = make_float2((U0.x + S0.x * d) * e, (U0.y + S0.y * d) * e);
+          const float h = fmaxf((ref0 - ref) * k, FAR), e = ex2(h);
+          U2 = make_float2((U0.x + S0.x * h) * e, (U0.y + S0.y * h) * e);
           S2 = make_float2(S0.x * e, S0.y * e);
 #pragma unroll 1
           for (int i = 0; i < B; ++i) {
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
       const float ls = logf(st.S);
       if (lane == 0) {
         if (p.lse) p.lse[r] = empty ? -inf : st.M * rt + ls;
-        if (p.entropy) p.entropy[r] = empty ? 0.f : ls - st.U / st.S * rt;
+        if (p.entropy) p.entropy[r] = empty ? 0.f : ls - st.U / st.S * 0.69314718055994531f;
         if (p.logprob) p.logprob[r] = scored ? (empty ? -inf : (xt - st.M) * rt - ls) : (t == -1 ? 0.f : nan);
         if (p.rank) p.rank[r] = scored ? st.above + 1 : (t == -1 ? 0 : -1);
       }

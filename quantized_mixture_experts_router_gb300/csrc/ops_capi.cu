@@ -36,7 +36,8 @@ int check_logprob(const moe_v41_logprob_cfg* c) {
   if (!c) return MOE_ERR_ARG;
   if (c->vocab < 1 || c->vocab > (1 << 28) || !is_type(c->logit_type)) return MOE_ERR_ARG;
   if (c->top_k < 0 || c->top_k > 32) return MOE_ERR_ARG;
-  if (!(c->temperature > 0.0f) || c->temperature > 3.0e38f) return MOE_ERR_ARG;
+  // 1 / T and log2(e) / T are finite normal numbers, and a difference of logits that overflows f32 has no weight
+  if (!(c->temperature >= 1.0e-36f) || !(c->temperature <= 1.0e36f)) return MOE_ERR_ARG;
   return MOE_OK;
 }
 

@@ -3,7 +3,7 @@ through in parts: several tiles a block, ranges and places at the ends of what
 the calls take.  Tolerances as in test_gpu_ops.py."""
 import pytest
 import torch
-from test_gpu_ops import Q, Q4  # noqa: F401
+from test_gpu_ops import INF, Lp, Q, Q4, gen  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +21,33 @@ def test_q4_many_tiles_a_block(Q, m, k, group):  # noqa: F811
         t.out.zero_()
         t.call()
         assert torch.equal(t.out, first)
+
+
+@pytest.mark.parametrize("m,v", [(3, 3001), (2, 70000), (400, 3000)])
+@pytest.mark.parametrize("temp", [1e-36, 1e-20, 1e20, 5e28, 1e30, 1e36])
+def test_logprob_far_temperatures(Q, temp, m, v):  # noqa: F811
+    """logits of the temperature's own size; what is masked or -inf has no weight at any temperature"""
+    rnd = torch.randn((m, v), device="cuda", generator=gen(v))
+    for mask in (False, True):
+        c = Lp(Q, m, v, "f32", 5, temp=temp, mask=mask, seed=m + v, logits=rnd * temp)
+        c.x[0, 1::3] = -INF
+        c.target[1] = 0
+        c.x[1, 7] = -3e38                                          # far below at every temperature, and finite
+        if mask:
+            c.x[~c.allowed()] = torch.finfo(torch.float32).min
+        c.call()
+        c.check()
+
+
+def test_logprob_entropy_of_a_far_largest_entry(Q):  # noqa: F811
+    """sums of 10^9 around a reference 10^30 below the largest entry: their weight is zero"""
+    v = 1 << 26
+    c = Lp(Q, 1, 8, "f32", 1)
+    c.v, c.cfg = v, Q.make_logprob_cfg(v, Q.MOE_T_F32, 1)
+    c.x = torch.full((1, v), 5.0, device="cuda")
+    c.x.view(-1, 1 << 16)[:, :1 << 14] = 0.0                       # lower references than most entries
+    c.x[0, v - 5] = 2e30
+    c.target[0] = v - 5
+    c.call()
+    assert int(c.ids[0, 0]) == v - 5 and int(c.rank[0]) == 1
+    assert float(c.entropy[0]) == 0.0 and float(c.logprob[0]) == 0.0 and float(c.lse[0]) == float(c.x[0, v - 5])
