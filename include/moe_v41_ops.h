@@ -23,7 +23,9 @@ enum { MOE_T_F32 = 0, MOE_T_BF16 = 1, MOE_T_F16 = 2 };
 
 /* ------------------------------------------------ 4-bit weights, group scales
  *   out[t, r] = sum_k x[t, k] * s[r, k / group] * (q[r, k] - z[r, k / group])
- * q in 0..15.  Sums are f32; each out is rounded once to its type. */
+ * q and z in 0..15.  Sums are f32, with more than eight tokens from a group's
+ * sum of (q - z) x on (which then has to stay in the range of f32); each out is
+ * rounded once to its type. */
 typedef struct {
   int32_t n;           /* rows of the weight (outputs per token): 1..2^24 */
   int32_t k;           /* inputs per token: a multiple of 32, 32..32768 */

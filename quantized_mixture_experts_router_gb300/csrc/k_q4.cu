@@ -1,6 +1,5 @@
 // Products with 4-bit weights and group scales, up to eight tokens a pass:
-//   out[t, r] = sum_k x[t, k] s[r, k/G] (q[r, k] - z[r, k/G])
-//             = sum_groups s (sum_k q x - z sum_k x)
+//   out[t, r] = sum_groups s[r, j] sum_{k in j} (q[r, k] - z[r, j]) x[t, k]
 //
 // Bound by the weights' bytes as long as a code costs few instructions, so
 // both are kept small.
@@ -14,23 +13,25 @@
 //    Masked in pairs, codes are fp16 numbers as they stand: 0x000q is
 //    q 2^-24 and 0x00q0 is 16 q 2^-24, both subnormal and exact, which the
 //    tensor cores (m16n8k16, rows x tokens, f32 sums) take at full rate.  One
-//    shift and four masks per eight codes, no conversion.
+//    shift and four masks per eight codes, no conversion; and one packed
+//    subtraction a pair takes z off, exactly.  (Taking z sum x off the group's
+//    sum instead would be cheaper by it, but a large x that meets a code equal
+//    to its zero would leave the rounding of two large sums where its product
+//    is 0.)  No weight is ever rounded: the scale multiplies the group's sum.
 //  - x is laid out in shared memory once per block as fp16, scaled by a power
-//    of two per token that brings its largest value to 2^14..2^15: fp16 then
-//    holds values down to 2^-32 of the largest exactly (the rest is off by
-//    less than 2^-39 of it, far below the f32 sums' own rounding).  The
-//    entries that meet 16 q are scaled by 1/16.  A token with an infinity or
-//    a NaN is computed term by term instead.
-//  - The sum of x over each group is taken once per block, in f32, and z times
-//    it leaves the group's sum before the scale multiplies it: no weight is
-//    ever rounded.
+//    of two per token that brings its largest value to 2^14..2^15.  The entries
+//    that meet 16 q are scaled by 1/16 more: of those, fp16 holds bf16 values
+//    down to 2^-28 of the largest exactly, fp16 values down to 2^-25, and the
+//    rest is off by at most 2^-35 of the largest; of the others all three are
+//    2^-4 of that.  A token with an infinity or a NaN is computed term by term
+//    instead.
 //  - A row tile shared by several warps of a block is joined in shared memory,
 //    one shared by several blocks through the workspace; the last to arrive
 //    adds all the parts in the order of the runs, so that the result does not
 //    depend on which one that was.
-// Measured: 131072 x 5120, one token: 59 us, 5.9 TB/s (copies reach 6.8): the
-// masks keep the integer pipe 53% busy while warps wait for boxes.  50001 x 2336,
-// five tokens, zeros: 18.7 us, 3.3 TB/s.  512 x 5120, one token: 5.3 us, of which
+// Measured: 131072 x 5120, one token: 54 us, 6.4 TB/s (copies reach 6.8).  8 x
+// 131072 x 5120, groups of 32: 83 us, where instructions bound it.  50001 x 2336,
+// five tokens, zeros: 19.2 us, 3.2 TB/s.  512 x 5120, one token: 5.4 us, of which
 // about 3 are the launch, x and the first box's latency one after the other.
 #include <cudaTypedefs.h>
 
@@ -49,7 +50,6 @@ constexpr int MAX_STAGES = 4;
 constexpr int PREFETCH = 1;                    // boxes a warp sends for before the stream's previous kernel has ended
 constexpr int PART = BOX_ROWS * DECODE_MAX_M;  // floats of one partial tile
 constexpr uint32_t SMEM_MAX = 232448;
-constexpr float CODE_UNIT = 0x1.0p-24f;        // value of the fp16 bit pattern 1
 
 // n / d for 0 <= n < 2^31 by one multiplication: with s = ceil(log2 d) and
 // mul = floor(2^(31+s) / d) + 1 the error n (mul d - 2^(31+s)) / (d 2^(31+s)) < 1 / d.
@@ -85,7 +85,7 @@ struct Q4Args {
   CUtensorMap map;           // w as bytes [n][k / 2], box {128 bytes, 32 rows}
   Q4Params p;                // m <= 8 tokens of this pass
   int nb;                    // boxes per row tile
-  FastDiv dnb, dwarps, dng;  // division by nb, by the warps of a block, by the groups of a row
+  FastDiv dnb, dwarps;       // division by nb, by the warps of a block
   Deal deal;                 // boxes (or whole row tiles) to blocks
   bool by_tile;              // blocks are dealt whole row tiles
   int stages;                // ring depth of a warp
@@ -254,33 +254,27 @@ struct BoxScales {
   }
 };
 
-// One box: acc += s (q x - z sum x) over its chunks of 32 k (all eight, or the
-// first `chunks`).  buf: the lane's row in the ring slot, its swizzle folded
-// in; xb: the lane's x of the box's first chunk; xs: the group sums of the
-// lane's token pair, xs_ld float4 from group to group.  The sums of a group
-// start from -z sum x.
+// a - b in both halves, as fp16 numbers
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// One box: acc += s (q - z) x over its chunks of 32 k (all eight, or the first
+// `chunks`).  buf: the lane's row in the ring slot, its swizzle folded in; xb:
+// the lane's x of the box's first chunk.
 template <int G, bool ZEROS, bool WHOLE>
 __device__ __forceinline__ void do_box(int scale_type, const BoxScales<G, ZEROS>& sc, uint32_t buf, uint32_t xb,
-                                       uint32_t xchunk, const float4* xs, int xs_ld, int chunks, float (&acc)[8]) {
+                                       uint32_t xchunk, int chunks, float (&acc)[8]) {
   constexpr int CPG = G / 32;  // chunks per group
 #pragma unroll
   for (int gi = 0; gi < BOX_K / G; ++gi) {
     if (!WHOLE && gi * CPG >= chunks) break;
-    const float4 xq = xs[gi * xs_ld];  // (-8 S0, -8 S1) twice, or (-S0, -S1) twice when zeros are given
-    float c[2][4];
+    uint32_t z[4];  // of the lane's rows, in both halves
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      c[i][0] = xq.x; c[i][1] = xq.y; c[i][2] = xq.z; c[i][3] = xq.w;
-      if (ZEROS) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {  // z as f32: its byte in the mantissa of 2^23
-          const uint32_t zb = __byte_perm(sc.z[2 * i + r][gi / 4], 0x4B000000u, 0x7440u + (gi & 3));
-          const float z = __uint_as_float(zb) - 8388608.0f;
-          c[i][2 * r] *= z;
-          c[i][2 * r + 1] *= z;
-        }
-      }
-    }
+    for (int i = 0; i < 4; ++i)
+      z[i] = ZEROS ? __byte_perm(sc.z[i][gi / 4], 0u, 0x4040u + 0x0101u * (gi & 3)) : 0x00080008u;
+    float c[2][4] = {};
 #pragma unroll
     for (int cj = 0; cj < CPG; ++cj) {
       const int ch = gi * CPG + cj;
@@ -295,7 +289,9 @@ __device__ __forceinline__ void do_box(int scale_type, const BoxScales<G, ZEROS>
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t wa = h ? w[2 * i] >> 8 : w[2 * i], wb = h ? w[2 * i + 1] >> 8 : w[2 * i + 1];
-            const uint32_t a[4] = {wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u};
+            const uint32_t za = z[2 * i], zb = z[2 * i + 1];
+            const uint32_t a[4] = {sub2(wa & 0x000F000Fu, za), sub2(wb & 0x000F000Fu, zb),
+                                   sub2(wa & 0x00F000F0u, za << 4), sub2(wb & 0x00F000F0u, zb << 4)};
             mma16816(c[i], a, xv[2 * h], xv[2 * h + 1]);
           }
       }
@@ -313,9 +309,7 @@ __device__ __forceinline__ void do_box(int scale_type, const BoxScales<G, ZEROS>
 // x of the pass, which copy_x brings into shared memory as it is, in place to
 // the form the tensor cores read (see the head of the file): 16-byte pieces
 // (chunk of 32 k, token, quarter), the eight values as pairs (0,4) (1,5) (2,6)
-// (3,7), the order the masked codes come in; behind them, per group and token
-// pair, the group sums times -8 (or -1 when zeros are given), twice over: the
-// starting values of a fragment.
+// (3,7), the order the masked codes come in.
 __device__ __forceinline__ uint32_t x_piece(int m, int tok, int q) {
   return (uint32_t)((((q >> 2) * m + tok) << 2) + (q & 3)) * 16u;
 }
@@ -346,16 +340,16 @@ __device__ __forceinline__ void x_f32(const uint4& v, float (&f)[8]) {
   }
 }
 
-template <int G, int XT>
-__device__ __forceinline__ void stage_x_t(const Q4Params& p, const FastDiv& dng, Q4Ctl& C, uint8_t* xp, float4* xs,
-                                          int xs_ld) {
+template <int XT>
+__device__ __forceinline__ void stage_x_t(const Q4Params& p, Q4Ctl& C, uint8_t* xp) {
   const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int pieces = p.k / 8;
-  {  // each token's largest magnitude (the patterns order like the magnitudes); warps share the tokens out
-    const int tok = warp % p.m, part = warp / p.m, parts = ((nthr >> 5) - tok + p.m - 1) / p.m;
+  // warps share the tokens out
+  const int tok = warp % p.m, first = warp / p.m * 32 + lane, step = ((nthr >> 5) - tok + p.m - 1) / p.m * 32;
+  {  // each token's largest magnitude (the patterns order like the magnitudes)
     uint32_t mx = 0u;
 #pragma unroll 4
-    for (int q = part * 32 + lane; q < pieces; q += parts * 32) {
+    for (int q = first; q < pieces; q += step) {
       const uint4 v = *reinterpret_cast<const uint4*>(xp + x_piece(p.m, tok, q));
       mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                                  __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
@@ -366,43 +360,25 @@ __device__ __forceinline__ void stage_x_t(const Q4Params& p, const FastDiv& dng,
   __syncthreads();
   // an infinity or a NaN anywhere: those tokens are computed by terms
   if (tid < p.m && C.amax[tid] >= 0x7F800000u) atomicOr(&C.bad, 1u << tid);
-  constexpr int LPG = G / 8;  // lanes per group, one piece each
-  const float unit = p.zeros ? -CODE_UNIT : -8.0f * CODE_UNIT;
-  const int work = p.m * p.ng * LPG, rounds = (work + nthr - 1) / nthr;
+  const float e = __uint_as_float((uint32_t)(14 - token_exp(C.amax[tok]) + 127) << 23), e16 = e * 0.0625f;
 #pragma unroll 2
-  for (int i = 0; i < rounds; ++i) {
-    const int at = i * nthr + tid, gg = at / LPG, tok = dng(gg), grp = gg - tok * p.ng;
-    const int q = grp * LPG + (tid & (LPG - 1));
-    const bool live = at < work;
-    float sum = 0.f;
-    if (live && q < pieces) {
-      const float e = __uint_as_float((uint32_t)(14 - token_exp(C.amax[tok]) + 127) << 23), e16 = e * 0.0625f;
-      uint4* ptr = reinterpret_cast<uint4*>(xp + x_piece(p.m, tok, q));
-      float f[8];
-      x_f32<XT>(*ptr, f);
-      sum = e * (((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7])));
-      uint32_t o[4];
+  for (int q = first; q < pieces; q += step) {
+    uint4* ptr = reinterpret_cast<uint4*>(xp + x_piece(p.m, tok, q));
+    float f[8];
+    x_f32<XT>(*ptr, f);
+    uint32_t o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // odd pairs meet 16 q
-        const __half2 h = __floats2half2_rn(f[j] * ((j & 1) ? e16 : e), f[j + 4] * ((j & 1) ? e16 : e));
-        o[j] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      *ptr = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int j = 0; j < 4; ++j) {  // odd pairs meet 16 q
+      const __half2 h = __floats2half2_rn(f[j] * ((j & 1) ? e16 : e), f[j + 4] * ((j & 1) ? e16 : e));
+      o[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
-#pragma unroll
-    for (int o = LPG / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (live && (tid & (LPG - 1)) == 0) {
-      float* to = reinterpret_cast<float*>(xs + grp * xs_ld + (tok >> 1)) + (tok & 1);
-      to[0] = to[2] = sum * unit;
-    }
+    *ptr = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
-template <int G>
-__device__ __forceinline__ void stage_x(const Q4Params& p, const FastDiv& dng, Q4Ctl& C, uint8_t* xp, float4* xs,
-                                        int xs_ld) {
-  if (p.x_type == MOE_T_BF16) stage_x_t<G, MOE_T_BF16>(p, dng, C, xp, xs, xs_ld);
-  else stage_x_t<G, MOE_T_F16>(p, dng, C, xp, xs, xs_ld);
+__device__ __forceinline__ void stage_x(const Q4Params& p, Q4Ctl& C, uint8_t* xp) {
+  if (p.x_type == MOE_T_BF16) stage_x_t<MOE_T_BF16>(p, C, xp);
+  else stage_x_t<MOE_T_F16>(p, C, xp);
 }
 
 template <int G, bool ZEROS, bool VEC>
@@ -414,7 +390,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   // shared memory: the warps' rings, the control block, a partial tile per
-  // warp, x, the group sums
+  // warp, x
   uint8_t* ringp = raw_smem + pad + (uint32_t)(warp * a.stages) * BOX_BYTES;
   const uint32_t ring = smem_u32(ringp);
   uint8_t* q = raw_smem + pad + (uint32_t)(W * a.stages) * BOX_BYTES;
@@ -423,7 +399,6 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   const int part_ld = pairs * 64;  // floats of a partial tile
   float* parts = reinterpret_cast<float*>(q + CTL_BYTES);
   uint8_t* xp = q + CTL_BYTES + (uint32_t)(W * part_ld) * 4;
-  float4* xs = reinterpret_cast<float4*>(xp + (uint32_t)p.m * p.k * 2);
   uint64_t* barp = reinterpret_cast<uint64_t*>(C.bar[warp]);
 
   // everything up to here and the barriers needs no memory of the stream: it
@@ -483,7 +458,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
     to.template load<VEC>(sp, zp, 8 * p.ng, rows, p.ng - bx * NGB);
   };
   if (f0 < f1) load_scales(sc, tile, b);
-  stage_x<G>(p, a.dng, C, xp, xs, pairs);
+  stage_x(p, C, xp);
   if (lane == 0)
     for (int i = 1; i < a.stages && left > 0; ++i) issue();
   __syncthreads();
@@ -492,7 +467,6 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   // a lane past the tokens reads token 0's values: its columns are never stored
   const uint32_t xlane = smem_u32(xp) + (uint32_t)((g < p.m ? g : 0) * 64 + t * 16);
   const uint32_t xchunk = (uint32_t)p.m * 64u;
-  const float4* xsl = xs + (t < pairs ? t : 0);
   const uint32_t alane = (uint32_t)lane * 128u + (uint32_t)((lane & 7) << 4);
   float acc[8];
 #pragma unroll
@@ -514,9 +488,8 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
     if (!__all_sync(0xffffffffu, ok)) break;
     const uint32_t buf = ring + (uint32_t)st * BOX_BYTES + alane;
     const uint32_t xb = xlane + (uint32_t)(b * (BOX_K / 32)) * xchunk;
-    const float4* xsb = xsl + b * NGB * pairs;
-    if (b < whole) do_box<G, ZEROS, true>(p.scale_type, sc, buf, xb, xchunk, xsb, pairs, BOX_K / 32, acc);
-    else do_box<G, ZEROS, false>(p.scale_type, sc, buf, xb, xchunk, xsb, pairs, (p.k - b * BOX_K) / 32, acc);
+    if (b < whole) do_box<G, ZEROS, true>(p.scale_type, sc, buf, xb, xchunk, BOX_K / 32, acc);
+    else do_box<G, ZEROS, false>(p.scale_type, sc, buf, xb, xchunk, (p.k - b * BOX_K) / 32, acc);
     __syncwarp();  // every lane has read the box before the ring slot is refilled
     if (lane == 0 && left > 0) issue();
     sc = sc_next;
@@ -643,9 +616,9 @@ Ws q4_ws() {
 }
 
 // Shared memory beside the rings.
-uint32_t fixed_bytes(int tokens, int k, int ng, int warps) {
+uint32_t fixed_bytes(int tokens, int k, int warps) {
   const uint32_t pairs = (uint32_t)(tokens + 1) / 2;
-  return 1024 + CTL_BYTES + (uint32_t)warps * pairs * 256 + (uint32_t)tokens * k * 2 + (uint32_t)ng * pairs * 16;
+  return 1024 + CTL_BYTES + (uint32_t)warps * pairs * 256 + (uint32_t)tokens * k * 2;
 }
 
 template <int G, bool ZEROS, bool VEC>
@@ -718,7 +691,6 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
           reinterpret_cast<uintptr_t>(p0.zeros) % ngb == 0;
   a.nb = (p0.k + BOX_K - 1) / BOX_K;
   a.dnb = FastDiv::of((unsigned)a.nb);
-  a.dng = FastDiv::of((unsigned)p0.ng);
   const int tiles = (p0.n + BOX_ROWS - 1) / BOX_ROWS, total = tiles * a.nb;
   sms = min(sms, MAX_CTAS);
   for (int t0 = 0; t0 < p0.m;) {
@@ -726,11 +698,11 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
     // 20 warps while it leaves them room, else 16, 12 or 8, else fewer tokens
     int warps = MAX_WARPS, tokens = min(p0.m - t0, DECODE_MAX_M);
     auto fits = [&](int wps, int toks) {
-      return fixed_bytes(toks, p0.k, p0.ng, wps) + (uint32_t)wps * 2 * BOX_BYTES <= SMEM_MAX;
+      return fixed_bytes(toks, p0.k, wps) + (uint32_t)wps * 2 * BOX_BYTES <= SMEM_MAX;
     };
     while (warps > 8 && !fits(warps, tokens)) warps -= 4;
     while (tokens > 1 && !fits(warps, tokens)) --tokens;
-    const uint32_t fixed = fixed_bytes(tokens, p0.k, p0.ng, warps);
+    const uint32_t fixed = fixed_bytes(tokens, p0.k, warps);
     a.stages = min(MAX_STAGES, (int)((SMEM_MAX - fixed) / ((uint32_t)warps * BOX_BYTES)));
     // Whole row tiles per block save the join between blocks, about as long as
     // four boxes of a warp; blocks that share row tiles are more even (4608 x 5120,

@@ -51,3 +51,33 @@ def test_logprob_entropy_of_a_far_largest_entry(Q):  # noqa: F811
     c.call()
     assert int(c.ids[0, 0]) == v - 5 and int(c.rank[0]) == 1
     assert float(c.entropy[0]) == 0.0 and float(c.logprob[0]) == 0.0 and float(c.lse[0]) == float(c.x[0, v - 5])
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("m,n,k,group", [(1, 300, 5120, 128), (3, 64, 512, 32), (8, 1000, 2336, 64), (1, 40, 32768, 32),
+                                         (40, 300, 512, 128)])
+def test_q4_large_x_at_codes_equal_to_their_zero(Q, m, n, k, group, zeros):  # noqa: F811
+    """x of 2^30 whose codes are the zeros, among small whole numbers: every sum is a whole number below 2^24, exact"""
+    t = Q4(Q, m, n, k, group, zeros=zeros, seed=k + m)
+    t.scales.fill_(1.0)
+    t.x.copy_(torch.randint(-3, 4, (m, k), device="cuda", generator=gen(2)))
+    for at in (5, k // 2, k - 1):                                  # even and odd codes
+        t.x[:, at] = 2.0 ** 30
+        z = t.zeros[:, at // group] if zeros else torch.full((n,), 8, dtype=torch.uint8, device="cuda")
+        b = t.w[:, at // 2]
+        t.w[:, at // 2] = (b & 0x0F) | (z << 4) if at & 1 else (b & 0xF0) | z
+    t.call()
+    assert torch.equal(t.out.double(), t.x.double() @ t.weights().t())
+
+
+@pytest.mark.parametrize("m", [1, 8])
+def test_q4_x_near_the_end_of_bf16(Q, m):  # noqa: F811
+    """neighbours of one sign whose plain sum overflows f32, under small scales"""
+    t = Q4(Q, m, 70, 512, 64, zeros=True, seed=4)
+    t.scales.fill_(2.0 ** -12)
+    t.x.fill_(2.0 ** 126)
+    t.w[:] = 0x33
+    t.zeros[:] = (torch.arange(70, device="cuda") % 3 + 1).to(torch.uint8)[:, None]
+    t.call()
+    want = t.x.double() @ t.weights().t()                          # 512 2^126 2^-12 times 2, 1 or 0: powers of two
+    assert torch.equal(t.out.double(), want) and (want < 2.0 ** 125).all()
