@@ -86,7 +86,8 @@ typedef struct {
  * next block; then h_out is needed).  gate as its kind says, ldg the pitch of
  * its rows.  post_w .. pre_b [dim], each may be NULL.  Pointers are aligned to
  * their element; outputs overlap no input except h_out == h (with
- * ldh_out == ldh). */
+ * ldh_out == ldh).  Rows that a block could not read within two seconds (a copy
+ * that never lands) are NaN in h_out and x_out. */
 MOE_API int moe_v41_block_norm(const moe_v41_norm_cfg* cfg, int m, const void* y, int64_t ldy, const void* post_w,
                                const void* post_b, const void* gate, int64_t ldg, const void* h, int64_t ldh,
                                void* h_out, int64_t ldh_out, const void* pre_w, const void* pre_b, void* x_out,

@@ -266,6 +266,21 @@ __global__ void __launch_bounds__(1024, 1) k_norm_row(const NormParams p) {
                       sum);
 }
 
+// This row and the block's later ones become NaN.
+template <int NG>
+__device__ __noinline__ void store_nan(const NormParams& p, long long r, int step) {
+  using R = Row<NG, true>;
+  float v[NG][4];
+#pragma unroll
+  for (int i = 0; i < NG; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[i][e] = __uint_as_float(0x7FC00000u);
+  for (; r < p.m; r += step) {
+    if (p.h_out) R::store(p.h_out, r * p.ldh_out, p.c.h_type, p.c.dim, v);
+    if (p.x_out) R::store(p.x_out, r * p.ldx, p.c.x_type, p.c.dim, v);
+  }
+}
+
 struct NormRowsArgs {
   NormParams p;
   uint32_t y_bytes, h_bytes;  // of a row; a stage holds y, then h
@@ -277,7 +292,7 @@ __global__ void __launch_bounds__(MAX_THREADS, BLOCKS) k_norm_rows(const NormRow
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ alignas(16) float red[2 * MAX_WARPS];
   __shared__ alignas(8) uint64_t full[STAGES];
-  __shared__ unsigned failed;
+  __shared__ unsigned timed_out;  // where a wait that runs out leaves its bit; each thread also learns it from the wait
   const NormParams& p = a.p;
   const int d = p.c.dim;
   const uint32_t stage_bytes = a.y_bytes + a.h_bytes;
@@ -285,7 +300,7 @@ __global__ void __launch_bounds__(MAX_THREADS, BLOCKS) k_norm_rows(const NormRow
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(full + i, 1);
     fence_mbar_init();
-    failed = 0u;
+    timed_out = 0u;
   }
   clear_sums(red);
   BlockSum sum{red, (int)blockDim.x >> 5, 0};
@@ -304,13 +319,22 @@ __global__ void __launch_bounds__(MAX_THREADS, BLOCKS) k_norm_rows(const NormRow
   int st = 0;
   uint32_t phase = 0;
   for (long long r = blockIdx.x; r < p.m; r += step) {
-    if (!mbar_try_wait(full + st, phase)) mbar_wait_for(full + st, phase, TIMEOUT_NS, &failed);
+    const bool here = mbar_try_wait(full + st, phase) || mbar_wait_for(full + st, phase, TIMEOUT_NS, &timed_out);
     const uint8_t* s = stages + (uint32_t)st * stage_bytes;
     float v[NG][4], h[NG][4];
     if (p.y) R::load(s, 0, p.c.y_type, d, v);
     R::load(s + a.y_bytes, 0, p.c.h_type, d, h);
     const float tg = p.y && p.c.gate_kind == MOE_GATE_TOKEN ? load_elem(p.gate, r / p.c.gate_group, p.c.gate_type) : 1.0f;
-    __syncthreads();  // the stage has been read
+    // the stage has been read; where it had not arrived for some thread, the block
+    // gives up, once its copies in flight have landed (or two seconds later)
+    if (__syncthreads_or(!here)) {
+      store_nan<NG>(p, r, step);
+      const uint64_t deadline = globaltimer_ns() + TIMEOUT_NS;
+      if (threadIdx.x == 0)
+        for (int j = 0; j < STAGES && r + (long long)j * step < p.m; ++j)
+          mbar_wait_bounded(full + (st + j) % STAGES, phase ^ (st + j >= STAGES ? 1u : 0u), deadline, &timed_out);
+      return;
+    }
     if (threadIdx.x == 0 && r + (long long)STAGES * step < p.m) fetch(r + (long long)STAGES * step, st);
     finish_row<NG, true>(p, r, v, h, w1, w2, tg,
                          [&](float (&u)[NG][4]) {

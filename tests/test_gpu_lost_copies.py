@@ -1,0 +1,62 @@
+"""A copy that never lands: the kernel's bounded wait runs out, the rows that
+depended on it are marked, the others are right, and the GPU stays usable.
+The kernels are built here with a copy that the test drops (lost_copies.cu)."""
+import ctypes
+import os
+import subprocess
+import time
+
+import pytest
+import torch
+from test_gpu_ops import Norm, Q  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(os.path.dirname(HERE), "quantized_mixture_experts_router_gb300", "csrc")
+
+
+def build(tmp, kernel, define):
+    import quantized_mixture_experts_router_gb300.build as qb
+    so = os.path.join(str(tmp), define.lower() + ".so")
+    subprocess.run([qb.NVCC, *qb.ARCH, *qb.FLAGS, "-I", CSRC, f"-DKERNEL=\"{kernel}\"", f"-D{define}", "-shared",
+                    os.path.join(HERE, "lost_copies.cu"), "-o", so, "-lcudart"], check=True)
+    lib = ctypes.CDLL(so)
+    lib.lose.argtypes = [ctypes.c_uint64]
+    return lib
+
+
+def vp(*tensors):
+    return [ctypes.c_void_p(t.data_ptr()) for t in tensors]
+
+
+def spaced(rows, first, m):
+    """rows are first, first + step, ... up to m"""
+    step = rows[1] - rows[0] if len(rows) > 1 else m
+    return rows == list(range(first, m, step)) and step > 1
+
+
+@pytest.mark.parametrize("lose", ["y", "h"])
+def test_norm_marks_the_rows_of_a_lost_copy(Q, tmp_path_factory, lose):  # noqa: F811
+    lib = build(tmp_path_factory.getbasetemp(), "k_norm.cu", "NORM")
+    m, dim, at = 900, 5120, 200
+    t = Norm(Q, m, dim, y="f32", h="f32", seed=1)
+    t.post_w = t.pre_w = None
+    t.call(post_w=None, pre_w=None)
+    want = t.h_out.clone(), t.x_out.clone()
+    t.h_out.fill_(7.0)
+    t.x_out.fill_(7.0)
+    torch.cuda.synchronize()
+    assert lib.lose(getattr(t, lose)[at].data_ptr()) == 0
+    begin = time.monotonic()
+    assert lib.block_norm(ctypes.byref(t.cfg), m, *vp(t.y, t.h, t.h_out, t.x_out)) == 0
+    torch.cuda.synchronize()
+    assert time.monotonic() - begin < 20
+    bad = torch.isnan(t.h_out).any(1)
+    assert spaced(bad.nonzero()[:, 0].tolist(), at, m)
+    assert torch.isnan(t.h_out[bad]).all() and torch.isnan(t.x_out[bad]).all()
+    assert torch.equal(t.h_out[~bad], want[0][~bad]) and torch.equal(t.x_out[~bad], want[1][~bad])
+    assert lib.lose(0) == 0                                     # the same kernel with every copy
+    assert lib.block_norm(ctypes.byref(t.cfg), m, *vp(t.y, t.h, t.h_out, t.x_out)) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(t.h_out, want[0]) and torch.equal(t.x_out, want[1])
