@@ -107,7 +107,9 @@ MOE_API int moe_v41_block_norm(const moe_v41_norm_cfg* cfg, int m, const void* y
  *  - NaN or +inf in an allowed place: the row's lse, entropy and logprobs are
  *    NaN.  Ids and rank stay defined: a NaN ranks below every number (so the
  *    rank of a NaN target is 1 + the number of allowed entries that are
- *    numbers). */
+ *    numbers).
+ *  - Rows that a block could not read within two seconds (a copy that never
+ *    lands): lse, entropy and logprobs NaN, ids and the rank of a target -1. */
 typedef struct {
   int32_t vocab;       /* 1..2^28 */
   int32_t logit_type;  /* MOE_T_* */

@@ -59,6 +59,7 @@ constexpr int BLOCKS_PER_SM = T == MOE_T_F32 ? 2 : 4;
 template <int T>
 constexpr uint32_t RING_BYTES = WARPS * STAGES * PIECE_BYTES<T>;
 constexpr uint64_t TIMEOUT_NS = 2000000000ull;  // of one wait for a copy
+constexpr uint32_t LOST = 1u << 31;   // above any number of pieces: they are 2 KB at least
 constexpr float LOWEST = -3.4028234663852886e38f;
 constexpr float FAR = -256.0f;        // an exponent of two whose power is zero, but whose product with it is not NaN
 
@@ -119,7 +120,7 @@ __device__ __forceinline__ float count_above(const float (&x)[N], float r) {
 // The running statistics of a set of entries.
 struct Stat {
   float M, S, U;
-  int above;
+  int above;  // entries above the target's; -1: the set could not be read
 };
 
 __device__ __forceinline__ u64 shfl_xor_u64(u64 v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
@@ -325,7 +326,8 @@ __device__ __forceinline__ Stat warp_join(Stat st, float k) {
     st.S += __shfl_xor_sync(0xffffffffu, st.S, o);
     st.U += __shfl_xor_sync(0xffffffffu, st.U, o);
   }
-  st.above = (int)__reduce_add_sync(0xffffffffu, (unsigned)st.above);
+  const bool failed = __any_sync(0xffffffffu, st.above < 0);
+  st.above = failed ? -1 : (int)__reduce_add_sync(0xffffffffu, (unsigned)st.above);
   st.M = M;
   return st;
 }
@@ -412,7 +414,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
   int t_now = target_of(r0), t_next = target_of(r0 + step);
   float xt_now = target_logit(r0, t_now);
 
-  uint32_t used = 0;  // pieces so far
+  // pieces so far; with LOST, one did not land in time: the warp waits and copies
+  // no more, and the block's rows are NaN
+  uint32_t used = 0;
   int parity = 0;
   for (int r = r0; r < p.m; r += step, parity ^= 1) {
     RowState& rs = sh.row[parity];
@@ -433,12 +437,15 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
     float ref_hi = LOWEST;  // and it moves when an entry lies above this
     float2 S2 = make_float2(0.f, 0.f), U2 = S2;
     float above = 0.f;      // entries above the target's (at most 2^20 a thread: exact)
-    for (int i0 = warp; i0 < sl.np; i0 += WARPS) {
+    for (int i0 = used < LOST ? warp : sl.np; i0 < sl.np; i0 += WARPS) {
       const int b0 = u0 + i0 * PU;
       const uint32_t st = used % STAGES;
       const uint8_t* mem = ring + st * PIECE_BYTES<T> + lane * UB;
-      if (!mbar_try_wait(full + st, (used / STAGES) & 1u))
-        mbar_wait_for(full + st, (used / STAGES) & 1u, TIMEOUT_NS, &sh.failed);
+      if (!__all_sync(0xffffffffu, mbar_try_wait(full + st, (used / STAGES) & 1u)) &&
+          !__all_sync(0xffffffffu, mbar_wait_for(full + st, (used / STAGES) & 1u, TIMEOUT_NS, &sh.failed))) {
+        used |= LOST;
+        break;
+      }
       // where every lane's maximum stays below `lim`, the units add to the
       // sums alone (the warp decides as one: both ways would cost their sum)
       float lim = fminf(ref_hi, xr), Mp = LOWEST;
@@ -645,7 +652,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
     Stat st;
     if (warp == 0) {
       st = warp_join(lane < WARPS ? rs.stat[lane] : Stat{LOWEST, 0.f, 0.f, 0}, k);
-      if (sh.failed) st.S = __uint_as_float(0x7FC00000u);
+      if (sh.failed) {
+        st.S = __uint_as_float(0x7FC00000u);
+        st.above = -1;
+      }
       if (lane == 0) rs.n = rs.nhot = 0;  // for the row after the next
     }
     if (a.cl > 1) {
@@ -675,24 +685,25 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
     if (rank == 0 && warp == 0) {
       __syncwarp();
       const float inf = pos_inf(), nan = __uint_as_float(0x7FC00000u);
-      const bool empty = st.S == 0.f;
+      const bool empty = st.S == 0.f, failed = st.above < 0;
       const float ls = logf(st.S);
       if (lane == 0) {
         if (p.lse) p.lse[r] = empty ? -inf : st.M * rt + ls;
         if (p.entropy) p.entropy[r] = empty ? 0.f : ls - st.U / st.S * 0.69314718055994531f;
         if (p.logprob) p.logprob[r] = scored ? (empty ? -inf : (xt - st.M) * rt - ls) : (t == -1 ? 0.f : nan);
-        if (p.rank) p.rank[r] = scored ? st.above + 1 : (t == -1 ? 0 : -1);
+        if (p.rank) p.rank[r] = scored && !failed ? st.above + 1 : (t == -1 ? 0 : -1);
       }
       if (lane < K) {
         const u64 key = rs.best[lane];
-        p.top_logprob[(long long)r * K + lane] = key == 0 || empty ? -inf : (key_value(key) - st.M) * rt - ls;
-        p.top_id[(long long)r * K + lane] = key ? key_id(key) : -1;
+        p.top_logprob[(long long)r * K + lane] =
+            failed ? nan : key == 0 || empty ? -inf : (key_value(key) - st.M) * rt - ls;
+        p.top_id[(long long)r * K + lane] = key && !failed ? key_id(key) : -1;
       }
     }
   }
-  if (sh.failed && lane == 0) {  // the copies in flight land before the block leaves
+  if (used >= LOST && lane == 0) {  // the warp's copies in flight land before the block leaves
     const uint64_t d2 = globaltimer_ns() + TIMEOUT_NS;
-    for (uint32_t v = used; v < sh.cursor[warp].fetched; ++v)
+    for (uint32_t v = used - LOST; v < sh.cursor[warp].fetched; ++v)
       mbar_wait_bounded(full + v % STAGES, (v / STAGES) & 1u, d2, &sh.failed);
   }
 }

@@ -29,4 +29,15 @@ __attribute__((visibility("default"))) int block_norm(const moe_v41_norm_cfg* cf
 }
 #endif
 
+#ifdef LOGPROB
+__attribute__((visibility("default"))) int token_logprobs(const moe_v41_logprob_cfg* cfg, const void* logits, int m,
+                                                          const int* target, float* logprob, int* rank, float* lse,
+                                                          float* entropy, float* top_logprob, int* top_id) {
+  moe::LogprobParams p{};
+  p.c = *cfg; p.m = m; p.logits = logits; p.ld = cfg->vocab; p.target = target; p.logprob = logprob; p.rank = rank;
+  p.lse = lse; p.entropy = entropy; p.top_logprob = top_logprob; p.top_id = top_id;
+  return moe::launch_token_logprobs(p, nullptr);
+}
+#endif
+
 }  // extern "C"

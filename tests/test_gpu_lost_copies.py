@@ -8,7 +8,7 @@ import time
 
 import pytest
 import torch
-from test_gpu_ops import Norm, Q  # noqa: F401
+from test_gpu_ops import Lp, Norm, Q  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,35 @@ def test_norm_marks_the_rows_of_a_lost_copy(Q, tmp_path_factory, lose):  # noqa:
     assert lib.block_norm(ctypes.byref(t.cfg), m, *vp(t.y, t.h, t.h_out, t.x_out)) == 0
     torch.cuda.synchronize()
     assert torch.equal(t.h_out, want[0]) and torch.equal(t.x_out, want[1])
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_logprob_marks_the_rows_of_a_lost_copy(Q, tmp_path_factory, t):  # noqa: F811
+    """the first piece of one row of a block that walks through several, and of a row that a cluster shares"""
+    lib = build(tmp_path_factory.getbasetemp(), "k_logprob.cu", "LOGPROB")
+    for m, v, at in ((2000, 6400, 900), (3, 64000, 1)):
+        c = Lp(Q, m, v, t, 5, seed=3)
+        c.call()
+        floats, ints = (c.logprob, c.lse, c.entropy, c.top), (c.rank, c.ids)
+        want = [o.clone() for o in floats + ints]
+        for o in floats + ints:
+            o.fill_(7)
+        torch.cuda.synchronize()
+
+        def call():
+            begin = time.monotonic()
+            assert lib.token_logprobs(ctypes.byref(c.cfg), *vp(c.x), m,
+                                      *vp(c.target, c.logprob, c.rank, c.lse, c.entropy, c.top, c.ids)) == 0
+            torch.cuda.synchronize()
+            assert time.monotonic() - begin < 20
+
+        assert lib.lose(c.x[at].data_ptr()) == 0
+        call()
+        bad = torch.isnan(c.lse)
+        assert spaced(bad.nonzero()[:, 0].tolist(), at, m)
+        for o, w in zip(floats + ints, want):
+            assert torch.equal(o[~bad], w[~bad])
+            assert torch.isnan(o[bad]).all() if o.is_floating_point() else (o[bad] == -1).all()
+        assert lib.lose(0) == 0                                    # the same kernel with every copy
+        call()
+        assert all(torch.equal(o, w) for o, w in zip(floats + ints, want))
