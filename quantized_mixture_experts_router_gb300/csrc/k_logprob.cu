@@ -24,9 +24,11 @@
 //    largest ones bounds the k-th largest key (value, then lower id: a 64-bit
 //    number) from below, and the top entries belong to the few threads or pieces
 //    whose maximum reaches the bound: those are read again, what reaches the
-//    bound goes to a buffer, and the places in order are counted.  Where the
-//    buffer overflows (many equal entries), the k-th largest key of what it holds
-//    is a better bound, and the slice is gone through again.
+//    bound goes to a buffer, and the places in order are counted.  Where a mask
+//    leaves some warp too few values, the bound is the k-th largest of them all.
+//    Where the buffer overflows (many equal entries, or a row's allowed entries
+//    in few pieces), they are gone through once more, an entry a thread at a time,
+//    and the bound rises whenever the buffer is nearly full.
 // Sums follow the fixed order of threads, warps and blocks; the buffer's order
 // varies, its sorted content does not.
 // Measured: 512 f32 rows of 131072, top 20: 56 us, 4.8 TB/s (43 us and 6.2 TB/s
@@ -346,8 +348,75 @@ struct Slice {
   }
 };
 
+// The threads' or pieces' maxima that are to be read again, as units of the row.
 template <int T, bool MASK, bool by_piece>
-__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(const LogprobArgs a) {
+struct HotUnits {
+  const Slice<T, MASK>& s;
+  const RowState& rs;
+  int per, lg;  // units of a hot thread or segment, and log2 of the next power of two
+  __device__ __forceinline__ HotUnits(const Slice<T, MASK>& s, const RowState& rs) : s(s), rs(rs) {
+    constexpr int B = PIECE_UNITS<T> / 32;
+    per = by_piece ? PIECE_UNITS<T> << seg_shift(s.np) : (s.np + WARPS - 1) / WARPS * B;
+    lg = per > 1 ? 32 - __clz(per - 1) : 0;
+  }
+  __device__ __forceinline__ int items() const { return rs.nhot << lg; }
+  // the unit of item q, or -1
+  __device__ __forceinline__ int operator()(int q) const {
+    constexpr int B = PIECE_UNITS<T> / 32;
+    const int h = rs.hot[q >> lg], j = q & ((1 << lg) - 1);
+    const int u = s.u0 + (by_piece ? h * per + j : ((h >> 5) + WARPS * (j / B)) * PIECE_UNITS<T> + (j % B) * 32 + (h & 31));
+    return j < per && u < s.u1 ? u : -1;
+  }
+};
+
+// The k-th largest of the block's values, one or two a thread (0 where there are
+// fewer).  The buffer is not in use yet.
+template <bool TWO>
+__device__ __forceinline__ unsigned kth_value(Shared& sh, RowState& rs, unsigned v0, unsigned v1, int k) {
+  rs.buf[threadIdx.x] = (u64)v0 << 32;
+  if (TWO) rs.buf[threadIdx.x + THREADS] = (u64)v1 << 32;
+  __syncthreads();
+  block_top(sh, rs.buf, (TWO ? 2 : 1) * THREADS);
+  return (unsigned)(sh.lists[0][k - 1] >> 32);
+}
+
+// Where more keys than the buffer takes reach thr: fills it anew from the hot
+// units, an entry of every thread at a time, and keeps the 32 largest whenever
+// the next entries might not fit.  Returns the number of keys.
+template <int T, bool MASK, bool by_piece>
+__device__ __forceinline__ int refill(const LogprobArgs& a, Shared& sh, RowState& rs, int r, uint32_t rank, u64 thr) {
+  const Slice<T, MASK> s(a, r, rank);
+  const HotUnits<T, MASK, by_piece> hot(s, rs);
+  const int items = hot.items();
+  int n = 0;
+  if (threadIdx.x == 0) rs.n = 0;
+  __syncthreads();
+  for (int q0 = 0; q0 < items; q0 += THREADS) {
+    const int q = q0 + (int)threadIdx.x, u = q < items ? hot(q) : -1;
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      const int id = 8 * u - s.row.off + e;
+      u64 key = 0;
+      if (u >= 0 && id >= 0 && id < s.row.V && s.row.allowed(id)) key = rank_key(Elem<T>::get(s.row.row[id]), id);
+      const bool in = key != 0 && key >= thr;
+      if (in) rs.buf[atomicAdd(&rs.n, 1)] = key;
+      n += __syncthreads_count(in);
+      if (n > CAP - THREADS) {
+        block_top(sh, rs.buf, n);
+        thr = sh.lists[0][a.p.c.top_k - 1];
+        n = 32;
+        if (threadIdx.x < 32) rs.buf[threadIdx.x] = sh.lists[0][threadIdx.x];
+        if (threadIdx.x == 0) rs.n = n;
+        __syncthreads();
+      }
+    }
+  }
+  return n;
+}
+static_assert(CAP >= 2 * THREADS + 32, "an entry of every thread fits after the 32 largest");
+
+template <int T, bool MASK, bool by_piece>
+__global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(const __grid_constant__ LogprobArgs a) {
   extern __shared__ __align__(128) uint8_t rings[];
   __shared__ Shared sh;
   const LogprobParams& p = a.p;
@@ -560,7 +629,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
       }
       if (tid < 32) rs.best[tid] = 0;
       __syncthreads();
-      const unsigned bound = __reduce_min_sync(0xffffffffu, lane < busy ? rs.bound[lane] : 0xFFFFFFFFu);
+      unsigned bound = __reduce_min_sync(0xffffffffu, lane < busy ? rs.bound[lane] : 0xFFFFFFFFu);
+      if (bound == 0) bound = kth_value<by_piece>(sh, rs, v0, v1, K);
       u64 thr = (u64)bound << 32;  // keys below it are not among the top k; 0: no bound, NaN may be among them
       float tf = bound ? from_ordered(bound) : -pos_inf();
       const bool live = !by_piece || tid < nseg;
@@ -603,35 +673,16 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
             if (c[i].ok) push(c[i], base + i * 32);
         }
       } else {  // (hot thread, unit of its own) over all threads
-        const int upt = (sl.np + WARPS - 1) / WARPS * B, lg = upt > 1 ? 32 - __clz(upt - 1) : 0;
-        const int items = rs.nhot << lg;
+        const HotUnits<T, MASK, false> hot(sl, rs);
+        const int items = hot.items();
         for (int q = tid; q < items; q += THREADS) {
-          const int h = rs.hot[q >> lg], j = q & ((1 << lg) - 1);
-          const int u = u0 + ((h >> 5) + WARPS * (j / B)) * PU + (j % B) * 32 + (h & 31);
-          if (j < upt && u < u1) push(unit_at(u), u);
+          const int u = hot(q);
+          if (u >= 0) push(unit_at(u), u);
         }
       }
       __syncthreads();
       int n = rs.n;
-      while (n > CAP) {
-        block_top(sh, rs.buf, CAP);
-        thr = sh.lists[0][K - 1];
-        tf = thr >> 32 ? key_value(thr) : -pos_inf();
-        if (tid == 0) rs.n = 0;
-        __syncthreads();
-        for (int j = max(0, 8 * u0 - row.off) + tid; j < min(row.V, 8 * u1 - row.off); j += THREADS) {
-          if (!row.allowed(j)) continue;
-          const float x = Elem<T>::get(row.row[j]);
-          if (x < tf) continue;
-          const u64 key = rank_key(x, j);
-          if (key < thr) continue;
-          const int at = atomicAdd(&rs.n, 1);
-          if (at < CAP) rs.buf[at] = key;
-        }
-        __syncthreads();
-        n = rs.n;
-        __syncthreads();
-      }
+      if (n > CAP) n = refill<T, MASK, by_piece>(a, sh, rs, r, rank, thr);
       if (n <= THREADS) {  // each key's place is the number of larger ones
         const u64 key = tid < n ? rs.buf[tid] : 0;
         if (warp * 32 < n) {

@@ -81,3 +81,45 @@ def test_q4_x_near_the_end_of_bf16(Q, m):  # noqa: F811
     t.call()
     want = t.x.double() @ t.weights().t()                          # 512 2^126 2^-12 times 2, 1 or 0: powers of two
     assert torch.equal(t.out.double(), want) and (want < 2.0 ** 125).all()
+
+
+def range_mask(c, lo, hi):
+    """allows the entries lo .. hi - 1 of every row"""
+    j = torch.arange(c.bits.shape[1] * 32, device="cuda")
+    on = ((j >= lo) & (j < hi)).view(-1, 32).long() << torch.arange(32, device="cuda")
+    c.bits[:] = on.sum(1).to(torch.int32)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("m,v,lo,hi", [(3, 131072, 0, 5000), (2, 131072, 40000, 40007), (40, 70000, 0, 35001),
+                                       (610, 9000, 100, 1500), (2, 9000, 8999, 9000), (310, 131072, 0, 65536)])
+def test_logprob_of_a_range_of_the_vocabulary(Q, t, m, v, lo, hi):  # noqa: F811
+    """masks that leave most warps and pieces nothing, over rows that rise, fall, or hold few values"""
+    j = torch.arange(v, device="cuda", dtype=torch.float32)
+    rows = torch.stack((j / v * 8, -j / v * 8, torch.zeros_like(j), j % 5, torch.full_like(j, -INF)))
+    c = Lp(Q, m, v, t, 20, mask=True, pad=1, logits=rows[torch.arange(m, device="cuda") % 5])
+    range_mask(c, lo, hi)
+    c.call()
+    if m > 40:                                                     # the check goes row by row
+        first = [o.clone() for o in (c.logprob, c.lse, c.entropy, c.top, c.rank, c.ids)]
+        assert all(torch.equal(c.ids[k], c.ids[k % 5]) for k in range(5, m))   # rows repeat but for their targets
+        c.m, c.x, c.bits = 10, c.x[-10:], c.bits[-10:]
+        c.target, c.logprob, c.lse, c.entropy, c.top, c.rank, c.ids = [c.target[-10:]] + [o[-10:] for o in first]
+    c.check()
+
+
+def test_logprob_of_a_range_takes_one_more_pass_not_many(Q):  # noqa: F811
+    """rising rows of which half is allowed: without top entries about 50 us, with them a pass over the allowed half
+    (an entry a thread at a time, 256 steps of about a microsecond, two rows a block) at the most"""
+    m, v = 512, 131072
+    c = Lp(Q, m, v, "f32", 20, mask=True, logits=torch.arange(v, device="cuda", dtype=torch.float32).expand(m, v) / v)
+    range_mask(c, 0, v // 2)
+    c.call()
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    begin.record()
+    c.call()
+    end.record()
+    torch.cuda.synchronize()
+    assert c.ids[m // 2].tolist() == list(range(v // 2 - 1, v // 2 - 21, -1))
+    assert begin.elapsed_time(end) < 5.0
