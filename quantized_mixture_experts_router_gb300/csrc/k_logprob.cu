@@ -761,26 +761,21 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM<T>) k_token_logprobs(co
 
 template <int T, bool MASK, bool BY_PIECE>
 int launch(const LogprobArgs& a, int sms, cudaStream_t s) {
-  static int attr_dev = -1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-  if (attr_dev != dev) {
-    if (cudaFuncSetAttribute(k_token_logprobs<T, MASK, BY_PIECE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaFuncSetAttribute(k_token_logprobs<T, MASK, BY_PIECE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)RING_BYTES<T>) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    attr_dev = dev;
-  }
+  const auto kernel = k_token_logprobs<T, MASK, BY_PIECE>;
+  static PerDevice ready;
+  if (ready.get(dev, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+               cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES<T>) == cudaSuccess;
+      }) < 1)
+    return MOE_ERR_CUDA;
   // as many blocks as the SMs hold; clusters of more than two blocks leave some SMs out, so
   // that their number comes from the runtime
   int clusters = BLOCKS_PER_SM<T> * sms / a.cl;
   if (a.cl > 2) {
-    static int fit[MAX_CLUSTER + 1] = {}, fit_dev = -1;
-    if (fit_dev != dev) {
-      for (int& f : fit) f = 0;
-      fit_dev = dev;
-    }
-    if (!fit[a.cl]) {
+    static PerDevice fit[MAX_CLUSTER + 1];
+    clusters = fit[a.cl].get(dev, [&] {
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeClusterDimension;
       at[0].val.clusterDim.x = (unsigned)a.cl;
@@ -791,14 +786,13 @@ int launch(const LogprobArgs& a, int sms, cudaStream_t s) {
       lc.dynamicSmemBytes = RING_BYTES<T>;
       lc.attrs = at;
       lc.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&fit[a.cl], k_token_logprobs<T, MASK, BY_PIECE>, &lc) != cudaSuccess || fit[a.cl] < 1)
-        return MOE_ERR_CUDA;
-    }
-    clusters = fit[a.cl];
+      int n = 0;
+      return cudaOccupancyMaxActiveClusters(&n, kernel, &lc) == cudaSuccess ? n : 0;
+    });
+    if (clusters < 1) return MOE_ERR_CUDA;
   }
   const int grid = (a.p.m < clusters ? a.p.m : clusters) * a.cl;
-  return launch_overlapped(k_token_logprobs<T, MASK, BY_PIECE>, dim3((unsigned)grid), dim3(THREADS),
-                           RING_BYTES<T>, s, a, a.cl);
+  return launch_overlapped(kernel, dim3((unsigned)grid), dim3(THREADS), RING_BYTES<T>, s, a, a.cl);
 }
 
 template <int T>

@@ -359,15 +359,15 @@ bool vec_ok(const void* p, long long ld, int t) {
 template <int MAX_THREADS, int BLOCKS>
 int launch_rows_t(const NormRowsArgs& a, int threads, uint32_t smem, int sms, int dev, cudaStream_t s) {
   const auto kernel = k_norm_rows<4, MAX_THREADS, BLOCKS>;
-  static int attr_dev = -1, regs = 0;
-  if (attr_dev != dev) {
+  static PerDevice allocated;  // registers a thread
+  const int regs = allocated.get(dev, [&] {
     cudaFuncAttributes fa{};
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024) != cudaSuccess ||
-        cudaFuncGetAttributes(&fa, kernel) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    regs = (fa.numRegs + 7) / 8 * 8;
-    attr_dev = dev;
-  }
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024) == cudaSuccess &&
+                   cudaFuncGetAttributes(&fa, kernel) == cudaSuccess
+               ? (fa.numRegs + 7) / 8 * 8
+               : 0;
+  });
+  if (regs < 1) return MOE_ERR_CUDA;
   // blocks an SM holds
   int occ = (int)(228u * 1024u / (smem + 2048u));
   if (occ > 65536 / (threads * regs)) occ = 65536 / (threads * regs);

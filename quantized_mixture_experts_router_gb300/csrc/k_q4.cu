@@ -623,16 +623,15 @@ uint32_t fixed_bytes(int tokens, int k, int warps) {
 
 template <int G, bool ZEROS, bool VEC>
 int launch_rows(const Q4Args& a, unsigned grid, int warps, uint32_t smem, cudaStream_t s) {
-  static int attr_dev = -1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-  if (attr_dev != dev) {
-    if (cudaFuncSetAttribute(k_q4_rows<G, ZEROS, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) !=
-        cudaSuccess)
-      return MOE_ERR_CUDA;
-    attr_dev = dev;
-  }
-  return launch_overlapped(k_q4_rows<G, ZEROS, VEC>, dim3(grid), dim3((unsigned)warps * 32), smem, s, a);
+  const auto kernel = k_q4_rows<G, ZEROS, VEC>;
+  static PerDevice ready;
+  if (ready.get(dev, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX) == cudaSuccess;
+      }) < 1)
+    return MOE_ERR_CUDA;
+  return launch_overlapped(kernel, dim3(grid), dim3((unsigned)warps * 32), smem, s, a);
 }
 
 template <int G>

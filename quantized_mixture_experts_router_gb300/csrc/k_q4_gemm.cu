@@ -507,20 +507,19 @@ __global__ void __launch_bounds__(NTHR, 1) k_q4_gemm(const __grid_constant__ Q4G
 
 template <bool BF, int G>
 int launch_gemm(const Q4GemmArgs& a, int sms, cudaStream_t s) {
-  static int attr_dev = -1;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-  if (attr_dev != dev) {
-    // the register trade needs the launch to hold what the shares add up to
-    cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, k_q4_gemm<BF, G>) != cudaSuccess || fa.numRegs != REG_LAUNCH) return MOE_ERR_CUDA;
-    if (cudaFuncSetAttribute(k_q4_gemm<BF, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES<G>) !=
-        cudaSuccess)
-      return MOE_ERR_CUDA;
-    attr_dev = dev;
-  }
+  const auto kernel = k_q4_gemm<BF, G>;
+  static PerDevice ready;
+  if (ready.get(dev, [&] {
+        // the register trade needs the launch to hold what the shares add up to
+        cudaFuncAttributes fa{};
+        return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == REG_LAUNCH &&
+               cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES<G>) == cudaSuccess;
+      }) < 1)
+    return MOE_ERR_CUDA;
   const int grid = a.tiles < sms ? a.tiles : sms;
-  return launch_overlapped(k_q4_gemm<BF, G>, dim3((unsigned)grid), dim3(NTHR), SMEM_BYTES<G>, s, a);
+  return launch_overlapped(kernel, dim3((unsigned)grid), dim3(NTHR), SMEM_BYTES<G>, s, a);
 }
 
 }  // namespace

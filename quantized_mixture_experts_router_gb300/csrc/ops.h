@@ -6,6 +6,7 @@
 
 #include "../../include/moe_v41_ops.h"
 #include "common.cuh"
+#include "per_device.h"
 
 namespace moe {
 
