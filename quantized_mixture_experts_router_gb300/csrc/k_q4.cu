@@ -677,7 +677,11 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
     const long long passes = (p0.m + DECODE_MAX_M - 1) / DECODE_MAX_M;
     const long long ns_passes = passes * (6500 + (long long)p0.n * p0.k / 2 / 5600);
     const long long ns_tiles = 3000 + 500ll * (((p0.n + 127) / 128 + sms - 1) / sms) * ((p0.k + 127) / 128);
-    if (ns_tiles < ns_passes) return launch_q4_gemm(p0, a.status, sms, s);
+    if (ns_tiles < ns_passes) {
+      bool taken = false;
+      const int rc = launch_q4_gemm(p0, a.status, sms, &taken, s);
+      if (rc || taken) return rc;
+    }
   }
   if (!make_map_2d(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p0.w, (uint64_t)p0.k / 2, (uint64_t)p0.n, (uint64_t)p0.k / 2,
                    BOX_K / 2, BOX_ROWS, 128))

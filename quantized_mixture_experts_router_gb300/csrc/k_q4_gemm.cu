@@ -506,25 +506,31 @@ __global__ void __launch_bounds__(NTHR, 1) k_q4_gemm(const __grid_constant__ Q4G
 }
 
 template <bool BF, int G>
-int launch_gemm(const Q4GemmArgs& a, int sms, cudaStream_t s) {
+int launch_gemm(const Q4GemmArgs& a, int sms, bool* taken, cudaStream_t s) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   const auto kernel = k_q4_gemm<BF, G>;
-  static PerDevice ready;
-  if (ready.get(dev, [&] {
-        // the register trade needs the launch to hold what the shares add up to
-        cudaFuncAttributes fa{};
-        return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == REG_LAUNCH &&
-               cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES<G>) == cudaSuccess;
-      }) < 1)
-    return MOE_ERR_CUDA;
+  static PerDevice allocated;  // registers a thread
+  const int regs = allocated.get(dev, [&] {
+    cudaFuncAttributes fa{};
+    return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess &&
+                   cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES<G>) == cudaSuccess
+               ? fa.numRegs
+               : 0;
+  });
+  if (regs < 1) return MOE_ERR_CUDA;
+  // The register trade waits until the launch holds what the shares add up to: a
+  // compiler that gave the kernel other than REG_LAUNCH leaves the call to the
+  // passes of eight tokens.
+  *taken = regs == REG_LAUNCH;
+  if (!*taken) return MOE_OK;
   const int grid = a.tiles < sms ? a.tiles : sms;
   return launch_overlapped(kernel, dim3((unsigned)grid), dim3(NTHR), SMEM_BYTES<G>, s, a);
 }
 
 }  // namespace
 
-int launch_q4_gemm(const Q4Params& p, unsigned* status, int sms, cudaStream_t s) {
+int launch_q4_gemm(const Q4Params& p, unsigned* status, int sms, bool* taken, cudaStream_t s) {
   Q4GemmArgs a{};
   if (!make_map_2d(&a.map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, (uint64_t)p.k / 2, (uint64_t)p.n, (uint64_t)p.k / 2,
                    RAW_K / 2, TM, 64) ||
@@ -550,9 +556,9 @@ int launch_q4_gemm(const Q4Params& p, unsigned* status, int sms, cudaStream_t s)
   }
   a.tiles = mt * a.nt;
   const bool bf = p.x_type == MOE_T_BF16;
-  if (p.group == 128) return bf ? launch_gemm<true, 128>(a, sms, s) : launch_gemm<false, 128>(a, sms, s);
-  if (p.group == 64) return bf ? launch_gemm<true, 64>(a, sms, s) : launch_gemm<false, 64>(a, sms, s);
-  return bf ? launch_gemm<true, 32>(a, sms, s) : launch_gemm<false, 32>(a, sms, s);
+  if (p.group == 128) return bf ? launch_gemm<true, 128>(a, sms, taken, s) : launch_gemm<false, 128>(a, sms, taken, s);
+  if (p.group == 64) return bf ? launch_gemm<true, 64>(a, sms, taken, s) : launch_gemm<false, 64>(a, sms, taken, s);
+  return bf ? launch_gemm<true, 32>(a, sms, taken, s) : launch_gemm<false, 32>(a, sms, taken, s);
 }
 
 }  // namespace moe

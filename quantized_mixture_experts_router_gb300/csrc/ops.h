@@ -52,8 +52,8 @@ struct LogprobParams {
 bool make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t cols, uint64_t rows,
                  uint64_t pitch, uint32_t box_cols, uint32_t box_rows, int swizzle);
 
-// Many tokens (k_q4_gemm.cu).
-int launch_q4_gemm(const Q4Params& p, unsigned* status, int sms, cudaStream_t s);
+// Many tokens (k_q4_gemm.cu); *taken: whether it was launched (see there).
+int launch_q4_gemm(const Q4Params& p, unsigned* status, int sms, bool* taken, cudaStream_t s);
 int launch_q4_linear(const Q4Params& p, void* ws, cudaStream_t s);
 size_t q4_workspace_bytes(const moe_v41_q4_cfg& c);
 int launch_block_norm(const NormParams& p, cudaStream_t s);

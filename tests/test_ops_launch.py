@@ -33,3 +33,15 @@ def test_calls_from_many_threads_on_two_devices(fake):
     assert fake.call_from_threads(threads, calls) == 0
     launches, bad, _ = counts(fake)
     assert launches == threads * calls * 4 and bad == 0
+
+
+def test_q4_many_tokens_whatever_registers_the_compiler_chose(fake, Q):  # noqa: F811
+    """the tile kernel trades the registers of a launch of 96 a thread; with others the call takes passes of eight"""
+    cfg = Q.make_q4_cfg(131072, 5120, 128, max_tokens=512)
+    a = 1 << 20
+    args = [ctypes.byref(cfg), ctypes.c_void_p(a), 512, ctypes.c_int64(5120), *map(ctypes.c_void_p, (a, a, None, a)),
+            ctypes.c_int64(131072), ctypes.c_void_p(a), ctypes.c_size_t(1 << 40), None]
+    fake.set_registers(88)
+    for _ in range(2):
+        assert fake.moe_v41_q4_linear(*args) == Q.MOE_OK
+        assert counts(fake)[:2] == [64, 0]
