@@ -45,7 +45,10 @@ MOE_API size_t moe_v41_q4_workspace_bytes(const moe_v41_q4_cfg* cfg);
  * aligned; the even k of a pair in the low nibble), scales [n, ceil(k/group)],
  * zeros u8 of the same shape or NULL for 8 throughout (codes 0..15), out
  * [m, n] (pitch ldo, aligned to its element).  0 <= m <= cfg->max_tokens.
- * Results do not depend on the order in which blocks run. */
+ * Results do not depend on the order in which blocks run.  When a wait runs
+ * out (MOE_STATUS_TIMEOUT), the outputs are invalid: those it concerns are NaN
+ * with up to eight tokens, and unwritten with more; the workspace is ready for
+ * the next call all the same. */
 MOE_API int moe_v41_q4_linear(const moe_v41_q4_cfg* cfg, const void* x, int m, int64_t ldx, const void* w,
                               const void* scales, const uint8_t* zeros, void* out, int64_t ldo, void* ws,
                               size_t ws_bytes, void* stream);

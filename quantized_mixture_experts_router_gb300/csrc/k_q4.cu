@@ -475,17 +475,28 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
   const int first_tile = tile;
   int st = 0, b0 = b;             // ring slot; where this row tile's share of the run began
   uint32_t phase = 0;
+  // Cleared when a wait runs out: from then on the warp copies and waits no more,
+  // and its sums are NaN, which join the other parts like any others, so that
+  // every count ends where it began.
   bool ok = true;
-  int f = f0;
-  for (; f < f1; ++f) {
+  for (int f = f0; f < f1; ++f) {
     const bool wrap = b + 1 == a.nb;
     const int tile1 = wrap ? tile + 1 : tile, b1 = wrap ? 0 : b + 1;
     const int hop = wrap ? BOX_ROWS * p.ng - b * NGB : NGB;
     sp += hop;
     if (ZEROS) zp += hop;
     if (f + 1 < f1) load_scales(sc_next, tile1, b1);
-    if (!mbar_try_wait(barp + st, phase) && !mbar_wait_for(barp + st, phase, a.timeout_ns, a.status)) ok = false;
-    if (!__all_sync(0xffffffffu, ok)) break;
+    if (ok && !__all_sync(0xffffffffu, mbar_try_wait(barp + st, phase)) &&
+        !__all_sync(0xffffffffu, mbar_wait_for(barp + st, phase, a.timeout_ns, a.status))) {
+      ok = false;
+      if (lane == 0) {  // the copies in flight land first
+        const uint64_t d2 = globaltimer_ns() + a.timeout_ns;
+        for (int e = f; e < f1 - left; ++e)
+          mbar_wait_bounded(barp + (e - f0) % a.stages, (uint32_t)((e - f0) / a.stages) & 1u, d2, a.status);
+        left = 0;
+      }
+      __syncwarp();
+    }
     const uint32_t buf = ring + (uint32_t)st * BOX_BYTES + alane;
     const uint32_t xb = xlane + (uint32_t)(b * (BOX_K / 32)) * xchunk;
     if (b < whole) do_box<G, ZEROS, true>(p.scale_type, sc, buf, xb, xchunk, BOX_K / 32, acc);
@@ -498,6 +509,10 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
       phase ^= 1u;
     }
     if (wrap || f + 1 == f1) {  // the run leaves this row tile
+      if (!ok) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = __uint_as_float(0x7FC00000u);
+      }
       const int mine = b + 1 - b0;
       if (mine == a.nb) {
         store_tile(p, C, tile, acc);
@@ -583,11 +598,6 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) k_q4_rows(const __grid_cons
     }
     tile = tile1;
     b = b1;
-  }
-  if (f < f1 && lane == 0) {  // a wait ran out: the copies in flight land before the block leaves
-    const uint64_t d2 = globaltimer_ns() + a.timeout_ns;
-    for (int e = f; e < f1 - left; ++e)
-      mbar_wait_bounded(barp + (e - f0) % a.stages, (uint32_t)((e - f0) / a.stages) & 1u, d2, a.status);
   }
 }
 

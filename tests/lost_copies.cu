@@ -1,6 +1,7 @@
-// A kernel of the operators, built with a bulk copy that can get lost: the one
-// whose source is `lost`.  KERNEL is the kernel's file.  Its waits are bounded,
-// so a lost copy ends in the kernel's own error handling.
+// A kernel of the operators, built with copies that can get lost: the bulk copy
+// whose source is `lost`, or (LINEAR) part of each box that a block's first warp
+// expects, the block being `lost` - 1.  KERNEL is the kernel's file.  Its waits
+// are bounded, so a lost copy ends in the kernel's own error handling.
 #include "ops.h"
 
 namespace moe {
@@ -8,9 +9,19 @@ __device__ unsigned long long lost;
 __device__ __forceinline__ void bulk_g2s_or_lose(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   if (reinterpret_cast<unsigned long long>(src) != lost) bulk_g2s(dst, src, bytes, bar);
 }
+__device__ __forceinline__ void expect_more(uint64_t* bar, uint32_t bytes) {
+  mbar_arrive_expect_tx(bar, threadIdx.x == 0 && blockIdx.x + 1 == lost ? bytes + 16 : bytes);
+}
 }  // namespace moe
 
+#ifdef LINEAR
+#define mbar_arrive_expect_tx expect_more
+namespace moe {
+int launch_q4_gemm(const Q4Params&, unsigned*, int, bool*, cudaStream_t) { return MOE_ERR_CUDA; }  // not under test
+}  // namespace moe
+#else
 #define bulk_g2s bulk_g2s_or_lose
+#endif
 #include KERNEL
 
 extern "C" {
@@ -37,6 +48,18 @@ __attribute__((visibility("default"))) int token_logprobs(const moe_v41_logprob_
   p.c = *cfg; p.m = m; p.logits = logits; p.ld = cfg->vocab; p.target = target; p.logprob = logprob; p.rank = rank;
   p.lse = lse; p.entropy = entropy; p.top_logprob = top_logprob; p.top_id = top_id;
   return moe::launch_token_logprobs(p, nullptr);
+}
+#endif
+
+#ifdef LINEAR
+__attribute__((visibility("default"))) int q4_linear(const moe_v41_q4_cfg* cfg, const void* x, int m, const void* w,
+                                                     const void* scales, void* out, void* ws) {
+  moe::Q4Params p{};
+  p.m = m; p.n = cfg->n; p.k = cfg->k; p.group = cfg->group; p.ng = (cfg->k + cfg->group - 1) / cfg->group;
+  p.x_type = cfg->x_type; p.scale_type = cfg->scale_type; p.out_type = cfg->out_type;
+  p.x = static_cast<const uint16_t*>(x); p.ldx = cfg->k; p.w = static_cast<const uint8_t*>(w);
+  p.scales = static_cast<const uint16_t*>(scales); p.out = out; p.ldo = cfg->n;
+  return moe::launch_q4_linear(p, ws, nullptr);
 }
 #endif
 

@@ -8,7 +8,7 @@ import time
 
 import pytest
 import torch
-from test_gpu_ops import Lp, Norm, Q  # noqa: F401
+from test_gpu_ops import Lp, Norm, Q, Q4  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -19,8 +19,9 @@ CSRC = os.path.join(os.path.dirname(HERE), "quantized_mixture_experts_router_gb3
 def build(tmp, kernel, define):
     import quantized_mixture_experts_router_gb300.build as qb
     so = os.path.join(str(tmp), define.lower() + ".so")
-    subprocess.run([qb.NVCC, *qb.ARCH, *qb.FLAGS, "-I", CSRC, f"-DKERNEL=\"{kernel}\"", f"-D{define}", "-shared",
-                    os.path.join(HERE, "lost_copies.cu"), "-o", so, "-lcudart"], check=True)
+    if not os.path.exists(so):
+        subprocess.run([qb.NVCC, *qb.ARCH, *qb.FLAGS, "-I", CSRC, f"-DKERNEL=\"{kernel}\"", f"-D{define}", "-shared",
+                        os.path.join(HERE, "lost_copies.cu"), "-o", so, "-lcudart"], check=True)
     lib = ctypes.CDLL(so)
     lib.lose.argtypes = [ctypes.c_uint64]
     return lib
@@ -92,3 +93,36 @@ def test_logprob_marks_the_rows_of_a_lost_copy(Q, tmp_path_factory, t):  # noqa:
         assert lib.lose(0) == 0                                    # the same kernel with every copy
         call()
         assert all(torch.equal(o, w) for o, w in zip(floats + ints, want))
+
+
+# row tiles shared by many blocks; whole row tiles a block, two tokens; runs of several boxes
+@pytest.mark.parametrize("m,n,k,group,block", [(1, 64, 32768, 128, 3), (2, 20001, 512, 64, 7), (8, 700, 5120, 32, 9)])
+def test_q4_marks_the_rows_of_a_lost_copy(Q, tmp_path_factory, m, n, k, group, block):  # noqa: F811
+    """the outputs of the row tiles that the block's first warp has a part of are NaN; the workspace stays ready"""
+    lib = build(tmp_path_factory.getbasetemp(), "k_q4.cu", "LINEAR")
+    t = Q4(Q, m, n, k, group, seed=5)
+    t.call()
+    want = t.out.clone()
+
+    def call():
+        t.out.fill_(7.0)
+        torch.cuda.synchronize()
+        begin = time.monotonic()
+        assert lib.q4_linear(ctypes.byref(t.cfg), *vp(t.x), m, *vp(t.w, t.scales, t.out, t.ws)) == 0
+        torch.cuda.synchronize()
+        assert time.monotonic() - begin < 20
+
+    for _ in range(2):
+        assert lib.lose(block + 1) == 0
+        call()
+        bad = torch.isnan(t.out).any(0)
+        tiles = (bad.nonzero()[:, 0] // 32).unique().tolist()
+        assert 1 <= len(tiles) <= 3 and tiles == list(range(tiles[0], tiles[-1] + 1))
+        rows = torch.arange(n, device="cuda") // 32
+        assert torch.equal(bad, (rows >= tiles[0]) & (rows <= tiles[-1])) and torch.isnan(t.out[:, bad]).all()
+        assert torch.equal(t.out[:, ~bad], want[:, ~bad])
+        assert Q.moe_v41_read_status(t.ws, clear=True) == Q.MOE_STATUS_TIMEOUT
+        assert lib.lose(0) == 0
+        call()
+        assert torch.equal(t.out, want)
+        assert Q.moe_v41_read_status(t.ws) == 0
