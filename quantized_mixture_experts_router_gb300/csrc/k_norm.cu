@@ -22,6 +22,8 @@ namespace {
 
 constexpr int MAX_WARPS = 32;
 constexpr int STAGES = 2;             // rows in shared memory (k_norm_rows)
+constexpr int MAX_STREAMED = 8192;    // elements of a row there: 512 threads of 16
+constexpr int MAX_STAGES_BYTES = STAGES * 2 * 4 * MAX_STREAMED;
 constexpr uint64_t TIMEOUT_NS = 2000000000ull;  // of one wait for a copy
 
 // Sum over the block; one barrier.  Two buffers alternate: a thread writes the
@@ -362,7 +364,7 @@ int launch_rows_t(const NormRowsArgs& a, int threads, uint32_t smem, int sms, in
   static PerDevice allocated;  // registers a thread
   const int regs = allocated.get(dev, [&] {
     cudaFuncAttributes fa{};
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024) == cudaSuccess &&
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_STAGES_BYTES) == cudaSuccess &&
                    cudaFuncGetAttributes(&fa, kernel) == cudaSuccess
                ? (fa.numRegs + 7) / 8 * 8
                : 0;
@@ -387,10 +389,11 @@ int row_threads(int dim) {
 
 int launch_rows(const NormParams& p, int sms, int dev, bool* taken, cudaStream_t s) {
   // From more rows on than blocks of k_norm_row (64 registers a thread: 1024
-  // threads an SM) are resident at once, if two stages of a row fit beside another
-  // block's.  f32 rows of 5120: 152 rows 4.0 us here, 3.3 us a block each; 180
-  // rows 5.3 and 5.6, 600 rows 8.4 and 11.1, 4096 rows 51.7 and 82.1.  bf16 rows
-  // of 2304: 420 rows 4.4 and 3.4, 500 rows 4.4 and 5.4.
+  // threads an SM) are resident at once.  f32 rows of 5120: 152 rows 4.0 us here,
+  // 3.3 us a block each; 180 rows 5.3 and 5.6, 600 rows 8.4 and 11.1, 4096 rows 52
+  // and 82.  f32 rows of 8192, whose stages leave an SM one block: 153 rows 6.4 and
+  // 7.5, 4096 rows 74 and 111.  bf16 rows of 2304: 420 rows 4.4 and 3.4, 500 rows
+  // 4.4 and 5.4.
   *taken = false;
   NormRowsArgs a{};
   a.p = p;
@@ -398,7 +401,7 @@ int launch_rows(const NormParams& p, int sms, int dev, bool* taken, cudaStream_t
   a.h_bytes = (uint32_t)(p.c.dim * type_bytes(p.c.h_type));
   const uint32_t smem = STAGES * (a.y_bytes + a.h_bytes);
   const int threads = (p.c.dim + 16 * 32 - 1) / (16 * 32) * 32;  // 16 elements each
-  if (threads > 512 || smem > 110000u || p.m <= 1024 / row_threads(p.c.dim) * sms) return MOE_OK;
+  if (p.c.dim > MAX_STREAMED || p.m <= 1024 / row_threads(p.c.dim) * sms) return MOE_OK;
   *taken = true;
   return threads <= 320 ? launch_rows_t<320, 2>(a, threads, smem, sms, dev, s)
                         : launch_rows_t<512, 1>(a, threads, smem, sms, dev, s);

@@ -14,7 +14,8 @@
 
 namespace {
 thread_local int device = 0;
-std::atomic<int> registers{64}, launches{0}, bad{0}, largest_block{0};
+std::atomic<int> registers{64}, launches{0}, bad{0}, grid{0};
+std::atomic<const void*> kernel{nullptr};
 
 CUresult encode(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
@@ -50,13 +51,14 @@ cudaError_t cudaGetDriverEntryPointByVersion(const char*, void** f, unsigned, un
   *r = cudaDriverEntryPointSuccess;
   return cudaSuccess;
 }
-cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void*, void**) {
+cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* func, void**) {
   unsigned cluster = 1;
   for (unsigned i = 0; i < c->numAttrs; ++i)
     if (c->attrs[i].id == cudaLaunchAttributeClusterDimension) cluster = c->attrs[i].val.clusterDim.x;
   ++launches;
   if (c->gridDim.x == 0 || c->gridDim.x % cluster || c->blockDim.x == 0 || c->blockDim.x > 1024) ++bad;
-  if ((int)c->blockDim.x > largest_block) largest_block = (int)c->blockDim.x;
+  grid = (int)c->gridDim.x;
+  kernel = func;
   return cudaSuccess;
 }
 
@@ -77,12 +79,13 @@ cudaError_t __cudaPopCallConfiguration(dim3*, dim3*, size_t*, void*) { return cu
 
 void set_registers(int n) { registers = n; }
 
-// counts since the last call: launches, those that a GPU would refuse, the largest block
+// since the last call: launches, and those that a GPU would refuse; and the last one's blocks
 void counts(int* out) {
   out[0] = launches.exchange(0);
   out[1] = bad.exchange(0);
-  out[2] = largest_block.exchange(0);
+  out[2] = grid;
 }
+const void* last_kernel() { return kernel; }
 
 // `threads` threads, on two devices by turns, call every operator `calls` times.
 // Returns the number of calls that failed.

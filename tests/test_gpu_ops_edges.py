@@ -3,7 +3,7 @@ through in parts: several tiles a block, ranges and places at the ends of what
 the calls take.  Tolerances as in test_gpu_ops.py."""
 import pytest
 import torch
-from test_gpu_ops import INF, Lp, Q, Q4, gen  # noqa: F401
+from test_gpu_ops import INF, Lp, Norm, Q, Q4, gen  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,20 @@ def test_logprob_of_a_range_takes_one_more_pass_not_many(Q):  # noqa: F811
     torch.cuda.synchronize()
     assert c.ids[m // 2].tolist() == list(range(v // 2 - 1, v // 2 - 21, -1))
     assert begin.elapsed_time(end) < 5.0
+
+
+@pytest.mark.parametrize("c", [
+    dict(m=700, dim=7168, y="f32", h="f32"), dict(m=153, dim=8192, y="f32", h="f32", x="f32"),
+    dict(m=500, dim=8192, y="f32", h="f32", post="layer", pre="layer", bias=True, gate="row", group=7),
+    dict(m=310, dim=6880, y="f32", h="f32", gate="token", gt="bf16", group=3), dict(m=400, dim=8192, y="f32", h="bf16"),
+    dict(m=900, dim=2304, post="layer", pre="layer", bias=True, gate="row", group=64, y="bf16", w="bf16"),
+    dict(m=1300, dim=1024, bias=True, gate="row", gt="bf16", group=1, pad=8, h="f32", x="f16"),
+], ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_norm_streamed_rows(Q, c):  # noqa: F811
+    """more rows than blocks fit at once: the widest rows, and what is loaded beside a row (gate rows, biases)"""
+    t = Norm(Q, seed=c["m"] + c["dim"], **c)
+    t.call()
+    t.check()
+    want = t.h_out.clone(), t.x_out.clone()
+    t.call(h_out=t.h)                                              # in place
+    assert torch.equal(t.h, want[0]) and torch.equal(t.x_out, want[1])

@@ -45,3 +45,17 @@ def test_q4_many_tokens_whatever_registers_the_compiler_chose(fake, Q):  # noqa:
     for _ in range(2):
         assert fake.moe_v41_q4_linear(*args) == Q.MOE_OK
         assert counts(fake)[:2] == [64, 0]
+
+
+@pytest.mark.parametrize("dim,m,streamed", [(5120, 4096, True), (7168, 4096, True), (8192, 153, True), (8192, 152, False),
+                                            (8200, 4096, False)])
+def test_norm_streams_rows_of_every_width_that_fits(fake, Q, dim, m, streamed):  # noqa: F811
+    """f32 rows: more of them than a block each fills the GPU with are streamed, by a few blocks an SM"""
+    cfg = Q.make_norm_cfg(dim, y_type=Q.MOE_T_F32, h_type=Q.MOE_T_F32)
+    a, d = 1 << 20, ctypes.c_int64(dim)
+    p = ctypes.c_void_p
+    assert fake.moe_v41_block_norm(ctypes.byref(cfg), m, p(a), d, None, None, None, d, p(a), d, p(a), d, None, None, p(a),
+                                   d, None) == Q.MOE_OK
+    launches, bad, grid = counts(fake)
+    assert launches == 1 and bad == 0
+    assert (grid < m) == streamed
