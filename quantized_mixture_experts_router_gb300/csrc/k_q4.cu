@@ -44,7 +44,7 @@ namespace {
 constexpr int BOX_ROWS = 32;
 constexpr int BOX_K = 256;
 constexpr uint32_t BOX_BYTES = BOX_ROWS * BOX_K / 2;
-constexpr int MAX_WARPS = 20;
+constexpr int MAX_WARPS = 20, MIN_WARPS = 8;
 constexpr int MAX_CTAS = 152;
 constexpr int MAX_STAGES = 4;
 constexpr int PREFETCH = 1;                    // boxes a warp sends for before the stream's previous kernel has ended
@@ -677,16 +677,28 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
   const Ws w = q4_ws();
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.status = &reinterpret_cast<Ctrl*>(base + w.ctrl)->status;
-  // More than eight tokens: passes of eight over the weights (6.5 us each and
-  // the weights at 5.6 TB/s) against tiles of 128 rows (3 us, and 0.5 us for each
-  // 128 k of the tiles an SM takes).  Measured at 16 tokens: 131072 x 5120, 125
-  // us in passes, 143 us in tiles; 5120 x 2304, 16.5 us against 12.4 us.  (The
-  // tiles address out by 32-bit offsets within a tile: not for pitches above
+  // More than eight tokens: passes of eight over the weights (5 us each, 0.1 ns for
+  // each value of x that is laid out, and the weights at 6.0, 5.5 or 4.5 TB/s for
+  // groups of 128, 64 and 32) against tiles of 128 rows (3 us, and 0.5, 0.84 or 1.4
+  // us for each 128 k of the tiles an SM takes).  Measured, passes and tiles in us:
+  //   131072 x 5120   16 tokens  125 142 (groups of 128)  168 398 (of 32)
+  //                   24 tokens  187 142                  251 397
+  //                   48 tokens  373 142                  501 397
+  //   5120 x 2304      9 tokens   13.5 12.0                14.1 28.1
+  //                   32 tokens   30.4 12.0                32.1 28.3
+  // (The tiles address out by 32-bit offsets within a tile: not for pitches above
   // 2^24.)
+  auto fits = [&](int wps, int toks) {
+    return fixed_bytes(toks, p0.k, wps) + (uint32_t)wps * 2 * BOX_BYTES <= SMEM_MAX;
+  };
   if (p0.m > DECODE_MAX_M && p0.ldo <= (1 << 24)) {
-    const long long passes = (p0.m + DECODE_MAX_M - 1) / DECODE_MAX_M;
-    const long long ns_passes = passes * (6500 + (long long)p0.n * p0.k / 2 / 5600);
-    const long long ns_tiles = 3000 + 500ll * (((p0.n + 127) / 128 + sms - 1) / sms) * ((p0.k + 127) / 128);
+    int per_pass = DECODE_MAX_M;
+    while (per_pass > 1 && !fits(MIN_WARPS, per_pass)) --per_pass;
+    const long long passes = (p0.m + per_pass - 1) / per_pass, bytes = (long long)p0.n * p0.k / 2;
+    const int tbs10 = p0.group == 128 ? 60 : p0.group == 64 ? 55 : 45;         // weights in a pass: TB/s times ten
+    const int ns_chunk = p0.group == 128 ? 500 : p0.group == 64 ? 840 : 1400;  // 128 k of a tile
+    const long long ns_passes = passes * (5000 + bytes / (100 * tbs10)) + (long long)p0.m * p0.k / 10;
+    const long long ns_tiles = 3000 + (long long)ns_chunk * (((p0.n + 127) / 128 + sms - 1) / sms) * ((p0.k + 127) / 128);
     if (ns_tiles < ns_passes) {
       bool taken = false;
       const int rc = launch_q4_gemm(p0, a.status, sms, &taken, s);
@@ -710,10 +722,7 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
     // x of the pass's tokens stays in shared memory beside two boxes per warp:
     // 20 warps while it leaves them room, else 16, 12 or 8, else fewer tokens
     int warps = MAX_WARPS, tokens = min(p0.m - t0, DECODE_MAX_M);
-    auto fits = [&](int wps, int toks) {
-      return fixed_bytes(toks, p0.k, wps) + (uint32_t)wps * 2 * BOX_BYTES <= SMEM_MAX;
-    };
-    while (warps > 8 && !fits(warps, tokens)) warps -= 4;
+    while (warps > MIN_WARPS && !fits(warps, tokens)) warps -= 4;
     while (tokens > 1 && !fits(warps, tokens)) --tokens;
     const uint32_t fixed = fixed_bytes(tokens, p0.k, warps);
     a.stages = min(MAX_STAGES, (int)((SMEM_MAX - fixed) / ((uint32_t)warps * BOX_BYTES)));

@@ -59,3 +59,19 @@ def test_norm_streams_rows_of_every_width_that_fits(fake, Q, dim, m, streamed): 
     launches, bad, grid = counts(fake)
     assert launches == 1 and bad == 0
     assert (grid < m) == streamed
+
+
+# passes of eight tokens, or 1 for the tile kernel: what was the faster of the two when both were measured
+@pytest.mark.parametrize("m,n,k,group,launches", [
+    (16, 131072, 5120, 128, 2), (17, 131072, 5120, 128, 1), (24, 131072, 5120, 64, 3), (32, 131072, 5120, 64, 1),
+    (32, 131072, 5120, 32, 4), (48, 131072, 5120, 32, 1), (9, 5120, 2304, 128, 1), (9, 5120, 2304, 64, 2),
+    (24, 5120, 2304, 32, 3), (32, 5120, 2304, 32, 1), (16, 20000, 4096, 32, 2), (32, 20000, 4096, 64, 1),
+    (16, 512, 5120, 128, 2), (17, 512, 5120, 128, 1), (32, 4608, 5120, 32, 4), (64, 4608, 5120, 32, 1)])
+def test_q4_passes_or_tiles(fake, Q, m, n, k, group, launches):  # noqa: F811
+    cfg = Q.make_q4_cfg(n, k, group, max_tokens=m)
+    a = 1 << 20
+    fake.set_registers(96)
+    assert fake.moe_v41_q4_linear(ctypes.byref(cfg), ctypes.c_void_p(a), m, ctypes.c_int64(k),
+                                  *map(ctypes.c_void_p, (a, a, None, a)), ctypes.c_int64(n), ctypes.c_void_p(a),
+                                  ctypes.c_size_t(1 << 40), None) == Q.MOE_OK
+    assert counts(fake)[:2] == [launches, 0]
