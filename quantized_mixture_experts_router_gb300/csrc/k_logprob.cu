@@ -9,17 +9,17 @@
 //  - A row belongs to a cluster of 1..16 blocks (the fewer rows the more), a
 //    contiguous slice each, whose results meet in distributed shared memory; a
 //    cluster walks through several rows when there are many.
-//  - Each warp streams its own pieces (4 KB of f32, 2 KB of 16 bits) of the slice with bulk copies into a
-//    ring of its own, across the ends of rows, so that the loads in flight cost
-//    no registers and warps meet twice a row only.  (Units of eight entries that
-//    the row begins or ends inside are read entry by entry.)
+//  - Each warp streams its own pieces (4 KB of f32, 2 KB of 16 bits) of the slice
+//    with bulk copies into a ring of its own, across the ends of rows, so that the
+//    loads in flight cost no registers and warps meet twice a row only.  (Units of
+//    eight entries that the row begins or ends inside are read entry by entry.)
 //  - A thread keeps S and U of its own, around a reference that moves only when
 //    an entry exceeds it by a factor of 2^8 (the first unit's maximum at first),
 //    so that a warp hardly ever diverges to rescale them; they are packed pairs
 //    of f32 (two sums an instruction).  Rank and reference cost one comparison
 //    of the unit's maximum with min(reference + 8 bits, the target's logit).
 //  - Top entries take nothing from the stream but maxima: each thread's (short
-//    slices), or each piece's (from 64 pieces on).  They are distinct entries,
+//    slices), or each piece's (long ones).  They are distinct entries,
 //    so with w warps holding a value a lane the least of the warps' ceil(k / w)-th
 //    largest ones bounds the k-th largest key (value, then lower id: a 64-bit
 //    number) from below, and the top entries belong to the few threads or pieces
@@ -52,8 +52,8 @@ constexpr int SEGS = 2 * THREADS;     // piece maxima of a row
 constexpr int STAGES = 2;             // pieces of a warp's ring
 // Bytes of a piece and blocks an SM holds: f32 rows are long and take few
 // instructions a byte, 16-bit rows need the warps (512 f32 rows of 131072: 60 us
-// with 4 KB pieces and two blocks, 66 us with 2 KB and four, when this was chosen; 1000 bf16 rows of
-// 50001: 55 and 43 us).
+// with 4 KB pieces and two blocks, 66 us with 2 KB and four, when this was
+// chosen; 1000 bf16 rows of 50001: 55 and 43 us).
 template <int T>
 constexpr uint32_t PIECE_BYTES = T == MOE_T_F32 ? 4096 : 2048;
 template <int T>
@@ -797,11 +797,15 @@ int launch(const LogprobArgs& a, int sms, cudaStream_t s) {
 
 template <int T>
 int launch_m(const LogprobArgs& a, int sms, cudaStream_t s) {
-  // the maxima of pieces rather than threads from 64 pieces a slice on: with
-  // 128 pieces (512 rows of 131072 f32) a thread's units are spread over so much
-  // memory that reading them again makes 75 us of 58; with 49 pieces (1000 rows of
-  // 50001 bf16) the pieces' maxima make 50 us of 42
-  const bool by_piece = a.p.c.vocab / a.cl >= 64 * (int)PIECE_BYTES<T> / type_bytes(T);
+  // the maxima of pieces rather than threads: reading a thread's units again is
+  // reading a little of many pieces, but the pieces' maxima cost the stream.  From 62
+  // pieces a slice on for f32, 98 for 16 bits.  Measured, pieces and threads in us:
+  //   f32   512 x 50000   49 pieces  35.3 32.9    bf16  1000 x 50001   49 pieces  49.9 42.7
+  //         400 x 64000   63         33.9 34.8          1000 x 65536   64         59.4 53.3
+  //         512 x 131072 128         57.0 72.5          1000 x 100000  98         82.2 82.7
+  //                                                     1000 x 131072 128         96.3 100.3
+  const int pieces = a.p.c.vocab / a.cl / (int)(PIECE_BYTES<T> / type_bytes(T));
+  const bool by_piece = pieces >= (T == MOE_T_F32 ? 62 : 97);
   if (by_piece) return a.p.allowed ? launch<T, true, true>(a, sms, s) : launch<T, false, true>(a, sms, s);
   return a.p.allowed ? launch<T, true, false>(a, sms, s) : launch<T, false, false>(a, sms, s);
 }

@@ -75,3 +75,21 @@ def test_q4_passes_or_tiles(fake, Q, m, n, k, group, launches):  # noqa: F811
                                   *map(ctypes.c_void_p, (a, a, None, a)), ctypes.c_int64(n), ctypes.c_void_p(a),
                                   ctypes.c_size_t(1 << 40), None) == Q.MOE_OK
     assert counts(fake)[:2] == [launches, 0]
+
+
+def test_logprob_bounds_from_pieces_or_threads(fake, Q):  # noqa: F811
+    """one kernel for short slices and one for long ones, by what was the faster: f32 from 62 pieces of 4 KB on, 16 bits
+    from 97 pieces of 2 KB (many rows: one block a row)"""
+    fake.last_kernel.restype = ctypes.c_void_p
+    a = ctypes.c_void_p(1 << 20)
+
+    def kernel(vocab, t):
+        cfg = Q.make_logprob_cfg(vocab, t, 20)
+        assert fake.moe_v41_token_logprobs(ctypes.byref(cfg), a, 1000, ctypes.c_int64(vocab), None, ctypes.c_int64(0),
+                                           *[a] * 7, None) == Q.MOE_OK
+        return fake.last_kernel()
+
+    for t, short, long in ((Q.MOE_T_F32, (1000, 50000), (64000, 131072)), (Q.MOE_T_BF16, (50001, 65536), (100000, 131072)),
+                           (Q.MOE_T_F16, (50001, 65536), (100000, 131072))):
+        assert len({kernel(v, t) for v in short}) == 1 and len({kernel(v, t) for v in long}) == 1
+        assert kernel(short[0], t) != kernel(long[0], t)
