@@ -726,13 +726,15 @@ int launch_q4_linear(const Q4Params& p0, void* ws, cudaStream_t s) {
     while (tokens > 1 && !fits(warps, tokens)) --tokens;
     const uint32_t fixed = fixed_bytes(tokens, p0.k, warps);
     a.stages = min(MAX_STAGES, (int)((SMEM_MAX - fixed) / ((uint32_t)warps * BOX_BYTES)));
-    // Whole row tiles per block save the join between blocks, about as long as
-    // four boxes of a warp; blocks that share row tiles are more even (4608 x 5120,
-    // eight tokens: 11.4 us by tile, 14.0 us shared; 512 x 32768, one token: 17.6
-    // and 10.2 us).
+    // Whole row tiles per block save the join between blocks, about as long as a
+    // box of a warp or two; blocks that share row tiles are more even.  By tile and
+    // shared, where the warps' boxes differ by 0: 4608 x 5120, eight tokens, groups of
+    // 32, 10.3 and 13.1 us; by 1: 6000 x 6144, one token, 8.5 and 9.0; by 2: 7168 x
+    // 18432, 19.0 and 17.4; by 3: 1024 x 16384, 10.7 and 8.0; by 6: 512 x 32768, 17.9
+    // and 9.1.
     const int even = (total + sms * warps - 1) / (sms * warps);
     const int by_tile = ((tiles + sms - 1) / sms * a.nb + warps - 1) / warps;
-    a.by_tile = by_tile <= even + 4;
+    a.by_tile = by_tile <= even + 1;
     const int ctas = min(sms, a.by_tile ? tiles : total);
     a.deal = Deal::of(a.by_tile ? tiles : total, ctas);
     a.dwarps = FastDiv::of((unsigned)warps);

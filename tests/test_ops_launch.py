@@ -93,3 +93,16 @@ def test_logprob_bounds_from_pieces_or_threads(fake, Q):  # noqa: F811
                            (Q.MOE_T_F16, (50001, 65536), (100000, 131072))):
         assert len({kernel(v, t) for v in short}) == 1 and len({kernel(v, t) for v in long}) == 1
         assert kernel(short[0], t) != kernel(long[0], t)
+
+
+# blocks of whole row tiles of 32 (as many as there are, up to the 152 SMs), or sharing them (152): the faster of the two
+@pytest.mark.parametrize("m,n,k,group,grid", [(8, 4608, 5120, 32, 144), (1, 512, 5120, 128, 16), (5, 500, 6144, 128, 16),
+                                              (1, 1024, 16384, 128, 152), (2, 700, 20480, 128, 152),
+                                              (8, 600, 9216, 128, 152), (1, 512, 32768, 128, 152)])
+def test_q4_whole_or_shared_row_tiles(fake, Q, m, n, k, group, grid):  # noqa: F811
+    cfg = Q.make_q4_cfg(n, k, group, max_tokens=m)
+    a = 1 << 20
+    assert fake.moe_v41_q4_linear(ctypes.byref(cfg), ctypes.c_void_p(a), m, ctypes.c_int64(k),
+                                  *map(ctypes.c_void_p, (a, a, None, a)), ctypes.c_int64(n), ctypes.c_void_p(a),
+                                  ctypes.c_size_t(1 << 40), None) == Q.MOE_OK
+    assert counts(fake) == [1, 0, grid]
