@@ -391,6 +391,7 @@ __device__ __forceinline__ int refill(const LogprobArgs& a, Shared& sh, RowState
   const HotUnits<T, MASK, by_piece> hot(s, rs);
   const int items = hot.items();
   int n = 0;
+  __syncthreads();  // every thread has read the count that brought it here
   if (threadIdx.x == 0) rs.n = 0;
   __syncthreads();
   for (int q0 = 0; q0 < items; q0 += THREADS) {

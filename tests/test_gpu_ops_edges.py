@@ -140,3 +140,14 @@ def test_norm_streamed_rows(Q, c):  # noqa: F811
     want = t.h_out.clone(), t.x_out.clone()
     t.call(h_out=t.h)                                              # in place
     assert torch.equal(t.h, want[0]) and torch.equal(t.x_out, want[1])
+
+
+@pytest.mark.parametrize("t,m,v", [("bf16", 700, 100741), ("f32", 700, 20001), ("f32", 400, 131072), ("f16", 1300, 6000)])
+def test_logprob_of_equal_entries_in_many_rows(Q, t, m, v):  # noqa: F811
+    """more equal entries than the candidate buffer takes, in every block's rows one after the other: the lowest ids"""
+    c = Lp(Q, m, v, t, 5, pad=8, logits=torch.full((m, v), 1.5))
+    for _ in range(5):
+        c.ids.fill_(7)
+        c.call()
+        assert torch.equal(c.ids, torch.arange(5, dtype=torch.int32, device="cuda").expand(m, 5))
+        assert (c.rank == 1).all() and (c.top == c.top[0, 0]).all()
