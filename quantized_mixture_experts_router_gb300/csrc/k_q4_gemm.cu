@@ -319,14 +319,15 @@ __device__ void run_dequant(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, cons
         zz[j] = base + (p.zeros ? (zrow && k < p.k ? (uint32_t)__ldg(zrow + k / p.group) : 0u) : 8u) * 0x00010001u;
       }
       if (!wt.warp(C.r_full[rs], (ru / NSR) & 1u)) return;
+      if (KC == 64 && k0 >= p.k) {  // the row ends in the first half
+        if (lane == 0) mbar_arrive(bp(C.r_empty[rs]));
+        continue;
+      }
       // 64-byte rows, 16-byte piece j of row r at j ^ (r / 2 % 4)
       const uint8_t* row = raw + rs * RAW_STAGE + r * 64;
       uint4 v[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) v[j] = *reinterpret_cast<const uint4*>(row + (((2 * hi + j) ^ ((r >> 1) & 3)) << 4));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bp(C.r_empty[rs]));
-      if (KC == 64 && k0 >= p.k) continue;  // the row ends in the first half
       if (!wt.warp(C.empty[as], ((par >> as) & 1u) ^ 1u)) return;
       par ^= 1u << as;
       tc_fence_after();
@@ -342,6 +343,9 @@ __device__ void run_dequant(const Q4GemmArgs& a, GemmCtl& C, uint32_t tmem, cons
       }
       tmem_wait_st();
       warp_arrive(C.full[as]);
+      // The raw stage goes back only now that its codes have been used: a load that
+      // has merely been issued may still be on its way when the next copy lands.
+      if (lane == 0) mbar_arrive(bp(C.r_empty[rs]));
       as = KC == 128 ? (as + 1 == NS ? 0u : as + 1) : (as + 2) % NS;
     }
   }

@@ -3,7 +3,7 @@ through in parts: several tiles a block, ranges and places at the ends of what
 the calls take.  Tolerances as in test_gpu_ops.py."""
 import pytest
 import torch
-from test_gpu_ops import INF, Lp, Norm, Q, Q4, gen  # noqa: F401
+from test_gpu_ops import INF, U, Lp, Norm, Q, Q4, gen  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +151,18 @@ def test_logprob_of_equal_entries_in_many_rows(Q, t, m, v):  # noqa: F811
         c.call()
         assert torch.equal(c.ids, torch.arange(5, dtype=torch.int32, device="cuda").expand(m, 5))
         assert (c.rank == 1).all() and (c.top == c.top[0, 0]).all()
+
+
+@pytest.mark.parametrize("group", [128, 64, 32])
+def test_q4_many_tokens_with_cold_zeros(Q, group):  # noqa: F811
+    """long rows whose weights, scales and zeros come from memory: the dequantising warps wait for zeros while the copies
+    run ahead, and may not be overtaken by them"""
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i, (m, n, k, x) in enumerate([(128, 3372, 26784, "bf16"), (64, 2193, 21056, "bf16"), (256, 1537, 27008, "f16"),
+                                      (172, 3268, 28352, "f16"), (73, 20744, 10560, "bf16"), (71, 40030, 7456, "f16")]):
+        t = Q4(Q, m, n, k, group, zeros=True, x=x, seed=i)
+        want = t.x.double() @ t.weights().t()
+        for _ in range(30):
+            flush.fill_(i)
+            t.call()
+            assert (t.out.double() - want).norm() / want.norm() <= 2 * U * max(32, k / 16), (m, n, k)
