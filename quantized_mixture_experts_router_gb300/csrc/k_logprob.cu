@@ -31,7 +31,7 @@
 //    and the bound rises whenever the buffer is nearly full.
 // Sums follow the fixed order of threads, warps and blocks; the buffer's order
 // varies, its sorted content does not.
-// Measured: 512 f32 rows of 131072, top 20: 56 us, 4.8 TB/s (43 us and 6.2 TB/s
+// Measured: 512 f32 rows of 131072, top 20: 57 us, 4.7 TB/s (43 us and 6.2 TB/s
 // without top entries; copies reach 6.8).  1000 bf16 rows of 50001, top 5: 42 us,
 // 2.4 TB/s: instructions bound it, and 1000 rows over 608 blocks leave the second
 // turn a third empty.  One f32 row of 131072 under a mask, top 20: 8.3 us.

@@ -29,9 +29,9 @@
 //    one shared by several blocks through the workspace; the last to arrive
 //    adds all the parts in the order of the runs, so that the result does not
 //    depend on which one that was.
-// Measured: 131072 x 5120, one token: 54 us, 6.4 TB/s (copies reach 6.8).  8 x
-// 131072 x 5120, groups of 32: 83 us, where instructions bound it.  50001 x 2336,
-// five tokens, zeros: 19.2 us, 3.2 TB/s.  512 x 5120, one token: 5.4 us, of which
+// Measured: 131072 x 5120, one token: 55 us, 6.3 TB/s (copies reach 6.8).  Eight
+// tokens, 131072 x 5120, groups of 32: 84 us, where instructions bound it.  50001 x
+// 2336, five tokens, zeros: 19.3 us, 3.2 TB/s.  512 x 5120, one token: 5.4 us, of which
 // about 3 are the launch, x and the first box's latency one after the other.
 #include <cudaTypedefs.h>
 

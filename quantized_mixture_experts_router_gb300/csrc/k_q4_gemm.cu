@@ -21,8 +21,8 @@
 // The running sums of 128 outputs per thread need more registers than an even
 // split of the register file: the warpgroups trade them (setmaxnreg).
 //
-// Measured: 512 tokens, 131072 x 5120, groups of 128: 497 us in a graph, 1.38
-// PFLOP/s (a library bf16 product reaches 1.92); groups of 64: 773 us.  The
+// Measured: 512 tokens, 131072 x 5120, groups of 128: 498 us in a graph, 1.38
+// PFLOP/s (a library bf16 product reaches 1.92); groups of 64: 772 us.  The
 // hand-overs between the warps that dequantise, issue and drain bound it.
 #include <cudaTypedefs.h>
 
@@ -45,11 +45,11 @@ constexpr uint32_t RAW_STAGE = TM * RAW_K / 2;
 constexpr int NSR = 4;             // raw stages
 
 // Groups of 128: stages of 128 k and two accumulators; a drain and its two
-// hand-overs fit behind the other half's MMAs, and fewer hand-overs of stages
-// count more (512 tokens, 131072 x 5120: 513 us against 579 with the other
-// choice).  Shorter groups: stages of 64 k leave tensor memory for a third
-// accumulator, which doubles the time for a drain (groups of 64: 777 us
-// against 1095; of 32: 1410 against 1360).
+// hand-overs fit behind the other half's MMAs (a group has to lie in one stage).
+// Shorter groups: stages of 64 k leave tensor memory for a third accumulator,
+// which doubles the time for a drain.  512 tokens, 131072 x 5120, and the same
+// with stages of 128 k: groups of 32, 1400 us and 1963; of 64, 772 and 760, but
+// 225 and 226 for 1000 tokens, 20000 x 4096.
 template <int G>
 struct Cfg {
   static constexpr int KC = G == 128 ? 128 : 64;   // k per stage of A and B
