@@ -1,5 +1,5 @@
-"""Python binding of libmoe_v41 (include/moe_v41.h, moe_v41_cache.h and
-moe_v41_ops.h): argument marshalling only.
+"""Python binding of libmoe_v41 (include/moe_v41.h, moe_v41_cache.h,
+moe_v41_ops.h and moe_v41_attn.h): argument marshalling only.
 
 Every step of the MoE layer runs in the library's sm_103a kernels; this
 module converts torch tensors (device memory) and streams into the C-ABI's
@@ -18,10 +18,12 @@ MOE_PATH_AUTO, MOE_PATH_DECODE, MOE_PATH_PREFILL = 0, 1, 2
 MOE_SCORE_SQRTSOFTPLUS, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1, 2
 MOE_SHARED_BF16, MOE_SHARED_KQUANT = 0, 1
 MOE_OK, MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_CUDA = 0, 1, 2, 3, 4
-MOE_STATUS_NAN_KEY, MOE_STATUS_MISSING_EXPERT, MOE_STATUS_TIMEOUT = 1, 2, 4
+MOE_STATUS_NAN_KEY, MOE_STATUS_MISSING_EXPERT, MOE_STATUS_TIMEOUT, MOE_STATUS_BAD_PAGE = 1, 2, 4, 8
 MOE_T_F32, MOE_T_BF16, MOE_T_F16 = 0, 1, 2
 MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1, 2
 MOE_GATE_NONE, MOE_GATE_ROW, MOE_GATE_TOKEN = 0, 1, 2
+MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 0, 1
+MOE_ROPE_SCALE_NONE, MOE_ROPE_SCALE_LINEAR, MOE_ROPE_SCALE_BASE, MOE_ROPE_SCALE_PARTS = 0, 1, 2, 3
 
 
 class MoeError(RuntimeError):
@@ -68,6 +70,28 @@ class moe_v41_logprob_cfg(ctypes.Structure):
                 ("temperature", ctypes.c_float)]
 
 
+class moe_v41_rope_cfg(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("rot_first", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("x_type", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
+
+
+class moe_v41_kv_cfg(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("type", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("page_pitch", ctypes.c_int64), ("token_pitch", ctypes.c_int64), ("head_pitch", ctypes.c_int64)]
+
+
+class moe_v41_seqs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("cu_new", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p), ("ld_table", ctypes.c_int64)]
+
+
+class moe_v41_attn_cfg(ctypes.Structure):
+    _fields_ = [("kv", moe_v41_kv_cfg), ("heads", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -112,12 +136,23 @@ def lib():
         L.moe_v41_q4_linear.argtypes = [q4p, vp, i32, i64, vp, vp, vp, vp, i64, vp, sz, vp]
         L.moe_v41_block_norm.argtypes = [nmp, i32, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp]
         L.moe_v41_token_logprobs.argtypes = [lpp, vp, i32, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+        rpp, kvp, sqp, atp = (ctypes.POINTER(c) for c in (moe_v41_rope_cfg, moe_v41_kv_cfg, moe_v41_seqs,
+                                                          moe_v41_attn_cfg))
+        f64 = ctypes.c_double
+        L.moe_v41_rope_freqs.argtypes = [i32, f64, i32, f64, i32, vp, vp]
+        L.moe_v41_rope.argtypes = [rpp, i32, i32, vp, i64, i64, vp, vp, vp, i64, i64, vp]
+        L.moe_v41_kv_append.argtypes = [kvp, rpp, sqp, i32, vp, i64, vp, i64, vp, vp, i32, vp, i64, vp, i64, vp, vp,
+                                        vp, vp]
+        L.moe_v41_attn_workspace_bytes.restype = sz
+        L.moe_v41_attn_workspace_bytes.argtypes = [atp]
+        L.moe_v41_paged_attention.argtypes = [atp, sqp, i32, i32, vp, i64, vp, vp, vp, i64, vp, i64, vp, sz, vp]
         for f in ("moe_v41_workspace_init", "moe_v41_quantize_q8_1", "moe_v41_select_from_logits", "moe_v41_route",
                   "moe_v41_forward", "moe_v41_read_status", "moe_v41_forward_noalloc",
                   "moe_v41_select_from_logits_vl", "moe_v41_route_vl", "moe_v41_forward_vl", "moe_v41_cache_create",
                   "moe_v41_cache_destroy", "moe_v41_cache_fetch", "moe_v41_cache_wait", "moe_v41_cache_reads",
                   "moe_v41_cache_slot_of", "moe_v41_cache_get_stats", "moe_v41_forward_streamed",
-                  "moe_v41_q4_linear", "moe_v41_block_norm", "moe_v41_token_logprobs"):
+                  "moe_v41_q4_linear", "moe_v41_block_norm", "moe_v41_token_logprobs", "moe_v41_rope_freqs",
+                  "moe_v41_rope", "moe_v41_kv_append", "moe_v41_paged_attention"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -368,3 +403,62 @@ def moe_v41_token_logprobs(cfg, logits, m, ld, allowed, ld_allowed, target, logp
     _check(lib().moe_v41_token_logprobs(ctypes.byref(cfg), _p(logits), m, ld, _p(allowed), ld_allowed, _p(target),
                                         _p(logprob), _p(rank), _p(lse), _p(entropy), _p(top_logprob), _p(top_id),
                                         _s(stream)), "moe_v41_token_logprobs")
+
+
+# ------------------------------------- operators of an attention block (moe_v41_attn.h)
+
+def moe_v41_rope_freqs(rot_dim, base=10000.0, kind=MOE_ROPE_SCALE_NONE, factor=1.0, trained=0):
+    """(angles per position of each pair, magnitude) on the host; the angles go to the device as f64"""
+    out, magnitude = (ctypes.c_double * max(1, rot_dim // 2))(), ctypes.c_float(1.0)
+    _check(lib().moe_v41_rope_freqs(rot_dim, base, kind, factor, trained, out, ctypes.byref(magnitude)),
+           "moe_v41_rope_freqs")
+    return list(out)[:rot_dim // 2], magnitude.value
+
+
+def make_rope_cfg(head_dim, rot_dim=None, rot_first=0, layout=MOE_ROPE_HALF, x_type=MOE_T_BF16, inverse=False,
+                  magnitude=1.0) -> moe_v41_rope_cfg:
+    return moe_v41_rope_cfg(head_dim, head_dim if rot_dim is None else rot_dim, rot_first, layout, x_type,
+                            int(bool(inverse)), magnitude)
+
+
+def moe_v41_rope(cfg, m, heads, x, ldx, ldx_head, pos, freqs, out, ldo, ldo_head, stream=None):
+    _check(lib().moe_v41_rope(ctypes.byref(cfg), m, heads, _p(x), ldx, ldx_head, _p(pos), _p(freqs), _p(out), ldo,
+                              ldo_head, _s(stream)), "moe_v41_rope")
+
+
+def make_kv_cfg(kv_heads, head_dim, page_size, n_pages, type=MOE_T_BF16, page_pitch=None, token_pitch=None,
+                head_pitch=None) -> moe_v41_kv_cfg:
+    """without pitches: a cache of [n_pages, page_size, kv_heads, head_dim] in memory"""
+    token_pitch = kv_heads * head_dim if token_pitch is None else token_pitch
+    return moe_v41_kv_cfg(kv_heads, head_dim, page_size, n_pages, type, 0,
+                          page_size * token_pitch if page_pitch is None else page_pitch, token_pitch,
+                          head_dim if head_pitch is None else head_pitch)
+
+
+def make_seqs(batch, cu_new, kv_len, table, max_pages, ld_table=None) -> moe_v41_seqs:
+    """holds the tensors' addresses, and the tensors themselves as long as it lives"""
+    s = moe_v41_seqs(batch, max_pages, _p(cu_new), _p(kv_len), _p(table),
+                     max_pages if ld_table is None else ld_table)
+    s.keep = (cu_new, kv_len, table)
+    return s
+
+
+def moe_v41_kv_append(kv, rope, seqs, m, k, ldk, v, ldv, k_cache, v_cache, q_heads, q, ldq, q_out, ldq_out, freqs,
+                      pos, status, stream=None):
+    _check(lib().moe_v41_kv_append(ctypes.byref(kv), ctypes.byref(rope), ctypes.byref(seqs), m, _p(k), ldk, _p(v),
+                                   ldv, _p(k_cache), _p(v_cache), q_heads, _p(q), ldq, _p(q_out), ldq_out, _p(freqs),
+                                   _p(pos), _p(status), _s(stream)), "moe_v41_kv_append")
+
+
+def make_attn_cfg(kv, heads, causal=True, window=0, scale=1.0) -> moe_v41_attn_cfg:
+    return moe_v41_attn_cfg(kv, heads, int(bool(causal)), window, scale)
+
+
+def moe_v41_attn_workspace_bytes(cfg: moe_v41_attn_cfg) -> int:
+    return int(lib().moe_v41_attn_workspace_bytes(ctypes.byref(cfg)))
+
+
+def moe_v41_paged_attention(cfg, seqs, m, max_new, q, ldq, k_cache, v_cache, out, ldo, lse, ld_lse, ws, stream=None):
+    _check(lib().moe_v41_paged_attention(ctypes.byref(cfg), ctypes.byref(seqs), m, max_new, _p(q), ldq, _p(k_cache),
+                                         _p(v_cache), _p(out), ldo, _p(lse), ld_lse, _p(ws), _nbytes(ws),
+                                         _s(stream)), "moe_v41_paged_attention")

@@ -1,0 +1,312 @@
+// How the attention kernels cut a call into work.  An item is a tile of R rows
+// (new tokens x the query heads that share a key head, token by token) of one
+// sequence and key head, against the tiles of TK keys that any of its rows sees.
+// The items, numbered sequence by sequence, in it head by head, in it row tile by
+// row tile, make one line of key tiles (an item that sees none counts as one),
+// which is cut into equal runs, one for each block: whatever the lengths, the
+// blocks have the same work.  An item that a cut goes through is joined
+// by the last of its blocks to finish, in the order of the runs.
+//
+// Lengths are on the device, so every block works the cut out for itself.
+#pragma once
+
+#include "attn.h"
+
+namespace moe {
+
+constexpr int ATTN_MAX_CTAS = 152;
+
+// One sequence: its first row, new tokens, cached tokens that can be read, and
+// the first new token's position.
+struct AttnSeq {
+  int row0, n, len, pos0;
+};
+
+__device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
+  const int c0 = p.s.cu_new[b], c1 = p.s.cu_new[b + 1], kv = max(p.s.kv_len[b], 0);
+  AttnSeq q;
+  q.row0 = min(max(c0, 0), p.m);
+  q.n = min(max(c1, q.row0), p.m) - q.row0;
+  q.len = min(kv, p.s.max_pages * p.c.kv.page_size);
+  q.pos0 = kv - (c1 - q.row0);
+  return q;
+}
+
+// Keys lo .. hi - 1 that rows r0 .. r1 - 1 of a sequence see between them.
+struct AttnRange {
+  int lo, hi;
+};
+__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, const AttnSeq& q, int group, int r0, int r1) {
+  AttnRange g{0, q.len};
+  if (p.c.causal) {
+    g.hi = min(max(q.pos0 + (r1 - 1) / group + 1, 0), q.len);
+    if (p.c.window) g.lo = min(max(q.pos0 + r0 / group - p.c.window + 1, 0), g.hi);
+  }
+  return g;
+}
+
+template <int R, int TK>
+struct AttnWork {
+  static __device__ __forceinline__ int row_tiles(const AttnSeq& q, int group) {
+    return q.n > 0 ? (q.n * group - 1) / R + 1 : 0;
+  }
+  static __device__ __forceinline__ AttnRange range(const AttnParams& p, const AttnSeq& q, int group, int i) {
+    return attn_range(p, q, group, i * R, min((i + 1) * R, q.n * group));
+  }
+  static __device__ __forceinline__ int key_tiles(const AttnRange& g) {
+    return g.hi > g.lo ? (g.hi - 1) / TK + 1 - g.lo / TK : 0;
+  }
+  static __device__ __forceinline__ int cost(const AttnParams& p, const AttnSeq& q, int group, int i) {
+    return max(1, key_tiles(range(p, q, group, i)));
+  }
+  // Key tiles of one key head of each lane's sequence (0 where !valid), by a whole warp.
+  static __device__ long long seq_cost(const AttnParams& p, int group, int b, bool valid) {
+    const int lane = threadIdx.x & 31;
+    AttnSeq q{};
+    if (valid) q = attn_seq(p, b);
+    const int nt = row_tiles(q, group);
+    long long c = nt == 1 ? cost(p, q, group, 0) : 0;
+    unsigned many = __ballot_sync(0xffffffffu, nt > 1);
+    while (many) {
+      const int src = __ffs((int)many) - 1;
+      many &= many - 1;
+      AttnSeq o;
+      o.row0 = __shfl_sync(0xffffffffu, q.row0, src);
+      o.n = __shfl_sync(0xffffffffu, q.n, src);
+      o.len = __shfl_sync(0xffffffffu, q.len, src);
+      o.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
+      const int n = __shfl_sync(0xffffffffu, nt, src);
+      long long sum = 0;
+      for (int i = lane; i < n; i += 32) sum += cost(p, o, group, i);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == src) c = sum;
+    }
+    return c;
+  }
+};
+
+// The cut, and where this block's run begins.
+struct AttnPlan {
+  long long warp_sum[32];
+  long long total;         // key tiles of the call
+  long long base, per_head;  // of the sequence in which the run begins: its place, and a head's key tiles
+  int runs;                // blocks that have work
+  int b, h, i, skip;       // the run's first item, and its key tiles that belong to the run before
+};
+
+__device__ __forceinline__ long long attn_run_begin(const AttnPlan& S, int run) { return S.total * run / S.runs; }
+// The run that holds place x of the line.
+__device__ __forceinline__ int attn_run_of(const AttnPlan& S, long long x) {
+  return (int)(((x + 1) * S.runs + S.total - 1) / S.total) - 1;
+}
+
+// By all NT threads of the block; ends with a barrier.
+template <int R, int TK, int NT>
+__device__ void attn_plan(const AttnParams& p, int group, AttnPlan& S) {
+  using W = AttnWork<R, TK>;
+  constexpr int NWARP = NT / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int batch = p.s.batch, kh = p.c.kv.kv_heads;
+  long long mine = 0, first = 0;  // all of this thread's sequences; the first
+  for (int b0 = 0; b0 < batch; b0 += NT) {
+    const long long c = W::seq_cost(p, group, b0 + tid, b0 + tid < batch) * kh;
+    mine += c;
+    if (b0 == 0) first = c;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+  if (lane == 0) S.warp_sum[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+  for (int w = 0; w < NWARP; ++w) total += S.warp_sum[w];
+  __syncthreads();
+  const int runs = (int)min((long long)gridDim.x, total);
+  if (tid == 0) {
+    S.total = total;
+    S.runs = runs;
+  }
+  if ((int)blockIdx.x < runs) {
+    const long long x0 = total * (int)blockIdx.x / runs;
+    long long base = 0;
+    for (int b0 = 0; b0 < batch && base <= x0; b0 += NT) {
+      const long long c = b0 == 0 ? first : W::seq_cost(p, group, b0 + tid, b0 + tid < batch) * kh;
+      long long s = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += v;
+      }
+      if (lane == 31) S.warp_sum[warp] = s;
+      __syncthreads();
+      long long before = base;
+      for (int w = 0; w < NWARP; ++w) {
+        if (w < warp) before += S.warp_sum[w];
+        base += S.warp_sum[w];
+      }
+      __syncthreads();
+      const long long at = before + s - c;
+      if (at <= x0 && x0 < at + c) {
+        S.b = b0 + tid;
+        S.base = at;
+        S.per_head = c / kh;
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const AttnSeq q = attn_seq(p, S.b);
+      const int nt = W::row_tiles(q, group);
+      long long rem = x0 - S.base;
+      const int h = (int)(rem / S.per_head);
+      rem -= h * S.per_head;
+      for (int i0 = 0; i0 < nt; i0 += 32) {
+        const int i = i0 + lane;
+        const long long c = i < nt ? W::cost(p, q, group, i) : 0;
+        long long s = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, s, d);
+          if (lane >= d) s += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, rem < s);
+        if (past) {
+          if (lane == __ffs((int)past) - 1) {
+            S.h = h;
+            S.i = i;
+            S.skip = (int)(rem - (s - c));
+          }
+          break;
+        }
+        rem -= __shfl_sync(0xffffffffu, s, 31);
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// The items of this block's run, one after the other; every warp that needs them
+// walks for itself.
+template <int R, int TK>
+struct AttnWalk {
+  using W = AttnWork<R, TK>;
+  const AttnParams& p;
+  const int group;
+  long long at, left;      // place of the item's part in the line; what is left of the run from there on
+  int b, h, i, row_tiles;
+  AttnSeq q;
+  AttnRange keys;
+  int tiles;               // key tiles of the item
+  int skip, take;          // the part: its first key tile and how many (of max(1, tiles))
+  bool live;
+
+  __device__ __forceinline__ AttnWalk(const AttnParams& p_, int group_, const AttnPlan& S) : p(p_), group(group_) {
+    live = (int)blockIdx.x < S.runs;
+    if (!live) return;
+    at = attn_run_begin(S, (int)blockIdx.x);
+    left = attn_run_begin(S, (int)blockIdx.x + 1) - at;
+    b = S.b;
+    h = S.h;
+    i = S.i;
+    skip = S.skip;
+    q = attn_seq(p, b);
+    row_tiles = W::row_tiles(q, group);
+    set();
+  }
+  __device__ __forceinline__ void set() {
+    keys = W::range(p, q, group, i);
+    tiles = W::key_tiles(keys);
+    take = (int)min((long long)(max(1, tiles) - skip), left);
+  }
+  __device__ __forceinline__ void next() {
+    at += take;
+    left -= take;
+    if (left <= 0) {
+      live = false;
+      return;
+    }
+    skip = 0;
+    if (++i == row_tiles) {
+      i = 0;
+      if (++h == p.c.kv.kv_heads) {
+        h = 0;
+        do {
+          if (++b >= p.s.batch) {
+            live = false;
+            return;
+          }
+          q = attn_seq(p, b);
+        } while (q.n == 0);
+        row_tiles = W::row_tiles(q, group);
+      }
+    }
+    set();
+  }
+  __device__ __forceinline__ int row0() const { return i * R; }                              // of the sequence
+  __device__ __forceinline__ int rows() const { return min(R, q.n * group - i * R); }
+  __device__ __forceinline__ int key0() const { return (keys.lo / TK + skip) * TK; }         // first key of the part
+  __device__ __forceinline__ int key_steps() const { return tiles ? take : 0; }              // key tiles to read
+  __device__ __forceinline__ bool whole() const { return take == max(1, tiles); }
+  __device__ __forceinline__ long long begin() const { return at - skip; }                   // place of the whole item
+  __device__ __forceinline__ long long end() const { return begin() + max(1, tiles); }
+};
+
+// Workspace of a call: status, a counter and two partial results for each block
+// (of an item that begins before its run, and of one that ends behind it).
+struct AttnWs {
+  size_t count, part, slot, total;  // byte offsets; bytes of a partial result
+};
+constexpr int ATTN_MAX_ROWS = 256;
+inline AttnWs attn_ws(const moe_v41_attn_cfg& c) {
+  AttnWs w{};
+  w.count = align256(sizeof(Ctrl));
+  w.part = w.count + align256(ATTN_MAX_CTAS * 4);
+  w.slot = (size_t)ATTN_MAX_ROWS * (c.kv.head_dim + 2) * 4;
+  w.total = align256(w.part + (size_t)ATTN_MAX_CTAS * 2 * w.slot);
+  return w;
+}
+
+// 2^x; 0 for -inf
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Box {64 values, rows of a page, 1, 1} of the cache seen as [page][head][slot][value].
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x, int slot, int head, int page,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Pages of a sequence, 64 at a time in two registers of a warp's lanes.
+struct AttnPages {
+  const int* row;
+  int base, last, a, b;
+  __device__ __forceinline__ int load(int i) const { return i <= last ? __ldg(row + i) : -1; }
+  __device__ __forceinline__ void begin(const int* row_, int first, int last_) {
+    row = row_;
+    base = first;
+    last = last_;
+    a = load(base + (int)(threadIdx.x & 31));
+    b = load(base + 32 + (int)(threadIdx.x & 31));
+  }
+  // from here on, pages from `first` on are asked for (at most 32 of them at once)
+  __device__ __forceinline__ void advance(int first) {
+    while (first - base >= 32) {
+      a = b;
+      base += 32;
+      b = load(base + 32 + (int)(threadIdx.x & 31));
+    }
+  }
+  // page i, by every lane for an i of its own
+  __device__ __forceinline__ int at(int i) const {
+    const int u = __shfl_sync(0xffffffffu, a, (i - base) & 31), v = __shfl_sync(0xffffffffu, b, (i - base) & 31);
+    return i - base < 32 ? u : v;
+  }
+};
+
+}  // namespace moe
