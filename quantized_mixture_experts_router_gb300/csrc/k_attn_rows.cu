@@ -35,7 +35,11 @@ template <int DH>
 struct Cfg {
   static constexpr int D = DH * 64;        // values of a head, rounded up
   static constexpr uint32_t STAGE = 2 * DH * HALF;
-  static constexpr int NS = DH == 2 ? 9 : 18;
+  // Every stage belongs to one warp (a multiple of their number): a warp that waited
+  // for a stage's next use while another's was still on its way would take that
+  // use's phase for done, as a phase's parity tells it from its neighbours alone.
+  static constexpr int NS = DH == 2 ? NW : 2 * NW;
+  static_assert(NS % NW == 0, "a stage is one warp's");
   static constexpr int OPITCH = D + 8;     // floats of a row of a warp's output in shared memory
 };
 

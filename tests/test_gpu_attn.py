@@ -289,6 +289,29 @@ def test_attention_of_few_tokens(Q, c, waste):  # noqa: F811
     a.check()
 
 
+@pytest.mark.parametrize("c", [
+    dict(new=[1], kv=[200000], heads=8, kv_heads=8, dim=128, page=64),
+    dict(new=[1] * 30, kv=[3000 + 17 * i for i in range(30)], heads=8, kv_heads=8, dim=128, page=16),
+    dict(new=[1] * 30, kv=[6000 + 17 * i for i in range(30)], heads=12, kv_heads=6, dim=64, page=8, t="f16"),
+], ids=desc)
+def test_attention_of_single_tokens_over_many_tiles_a_block(Q, c):  # noqa: F811
+    """rings that go round many times, with copies that land in any order"""
+    a = Attn(Q, seed=8, **c)
+    a.spoil(NAN)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    a.call()
+    a.check(only=range(min(a.batch, 3)))
+    first = a.out.clone()
+    for i in range(20):
+        flush.fill_(i)
+        a.out.zero_()
+        a.call()
+        assert torch.equal(a.out, first)
+    for i in range(200):                                              # one behind the other
+        a.call()
+    assert torch.equal(a.out, first) and Q.moe_v41_read_status(a.ws) == 0
+
+
 # chunks, prompts, drafts of several tokens
 MANY = [
     dict(new=[128], kv=[128], heads=2, kv_heads=2, dim=128, page=16),
