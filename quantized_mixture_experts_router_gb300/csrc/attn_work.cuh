@@ -16,6 +16,9 @@ namespace moe {
 
 constexpr int ATTN_MAX_CTAS = 152;
 
+// Rows and keys of an item's tiles in the kernel for few rows, and in that for many.
+constexpr int ATTN_ROWS_TILE = 16, ATTN_ROWS_KEYS = 32, ATTN_TILES_TILE = 256, ATTN_TILES_KEYS = 128;
+
 // One sequence: its first row, new tokens, cached tokens that can be read, and
 // the first new token's position.
 struct AttnSeq {
@@ -250,19 +253,111 @@ struct AttnWalk {
   __device__ __forceinline__ long long end() const { return begin() + max(1, tiles); }
 };
 
-// Workspace of a call: status, a counter and two partial results for each block
-// (of an item that begins before its run, and of one that ends behind it).
+// Workspace of a call: status, and for each block two counters (of the item that
+// begins in its run and ends behind it, one for each half of its rows) and two
+// partial results (of an item that begins before its run, and of one that ends
+// behind it).
 struct AttnWs {
   size_t count, part, slot, total;  // byte offsets; bytes of a partial result
 };
-constexpr int ATTN_MAX_ROWS = 256;
 inline AttnWs attn_ws(const moe_v41_attn_cfg& c) {
   AttnWs w{};
   w.count = align256(sizeof(Ctrl));
-  w.part = w.count + align256(ATTN_MAX_CTAS * 4);
-  w.slot = (size_t)ATTN_MAX_ROWS * (c.kv.head_dim + 2) * 4;
+  w.part = w.count + align256(ATTN_MAX_CTAS * 2 * 4);
+  w.slot = (size_t)ATTN_TILES_TILE * (c.kv.head_dim + 2) * 4;
   w.total = align256(w.part + (size_t)ATTN_MAX_CTAS * 2 * w.slot);
   return w;
+}
+
+// What a kernel needs beside the call's parameters.
+struct AttnArgs {
+  CUtensorMap map_k, map_v;
+  AttnParams p;
+  int group;               // query heads of a key head
+  int page_shift, box_rows;
+  float c;                 // scale log2 e
+  unsigned* status;
+  unsigned* count;         // [blocks][2]
+  char* part;              // [blocks][2] of slot bytes each
+  size_t slot;
+  unsigned long long timeout_ns;
+};
+int launch_attn_rows(const AttnArgs& a, int ctas, cudaStream_t s);
+int launch_attn_tiles(const AttnArgs& a, int ctas, bool* taken, cudaStream_t s);  // *taken: whether it was launched
+__device__ __forceinline__ uint64_t* attn_bar(unsigned long long& b) { return reinterpret_cast<uint64_t*>(&b); }
+
+// Bounded wait of a warp; once one ran out, the block's later waits do not wait.
+__device__ __forceinline__ bool attn_wait(unsigned long long& bar, uint32_t parity, volatile uint32_t* abort,
+                                          uint64_t timeout_ns, unsigned* status) {
+  bool ok = mbar_try_wait(attn_bar(bar), parity);
+  if (!ok && !*abort) {
+    ok = mbar_wait_for(attn_bar(bar), parity, timeout_ns, status);
+    if (!ok) *abort = 1u;
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t attn_pack2(float lo, float hi) {
+  if (BF) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The reference maximum of a row is moved only when the true one is more than this
+// above it (in exponents of two), so that outputs are rescaled a few times an item;
+// weights are at most 2^8.  For fp16 they are 2^6 times as large, so that those of
+// 2^-31 of the largest still count.
+constexpr float ATTN_SLACK = 8.0f;
+template <bool BF>
+constexpr float ATTN_BIAS = BF ? 0.f : 6.f;
+
+// Four values of a row, over n parts of its keys: part i has reference maximum and
+// sum ml(i) and unscaled values o(i).
+struct AttnJoined {
+  float m, l;
+  float4 o;
+};
+template <class ML, class O>
+__device__ __forceinline__ AttnJoined attn_join(int n, ML ml, O o) {
+  AttnJoined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int i = 0; i < n; ++i) j.m = fmaxf(j.m, ml(i).x);
+  const float ref = j.m == -INFINITY ? 0.f : j.m;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float2 v = ml(i);
+    if (v.y == 0.f) continue;  // nothing seen: its outputs were never written
+    float f;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(v.x - ref));
+    const float4 x = o(i);
+    j.l += f * v.y;
+    j.o.x += f * x.x;
+    j.o.y += f * x.y;
+    j.o.z += f * x.z;
+    j.o.w += f * x.w;
+  }
+  return j;
+}
+
+// log sum exp of a row from its reference maximum and sum
+template <bool BF>
+__device__ __forceinline__ float attn_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l) - ATTN_BIAS<BF>) * 0.69314718055994531f;
+}
+
+template <bool BF>
+__device__ __forceinline__ void attn_store(const AttnArgs& a, int tok0, int h, int row, int d, const AttnJoined& j) {
+  const int tok = row / a.group, hd = h * a.group + row - tok * a.group;
+  const long long t = tok0 + tok;
+  const float s = j.l == 0.f ? 0.f : 1.f / j.l;
+  uint2 v;
+  v.x = attn_pack2<BF>(j.o.x * s, j.o.y * s);
+  v.y = attn_pack2<BF>(j.o.z * s, j.o.w * s);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.p.out) + t * a.p.ldo + (long long)hd * a.p.c.kv.head_dim + d) = v;
+  if (d == 0 && a.p.lse) a.p.lse[t * a.p.ld_lse + hd] = attn_lse<BF>(j.m, j.l);
 }
 
 // 2^x; 0 for -inf

@@ -12,24 +12,16 @@
 // empty, and p would have to pass through tensor memory; here it goes from the
 // accumulators of the first product straight into the operands of the second.
 //
-// The maximum that p refers to follows the true one only when that is 8 (a factor
-// of 256) above it: p is then at most 256, and outputs are rescaled a few
-// times an item.  For fp16, p is 64 times as large, so that weights of 2^-31 of the
-// largest still count.
 #include "attn_work.cuh"
-#include "tc.cuh"
 
 namespace moe {
 
-bool make_cache_map(CUtensorMap* m, const moe_v41_kv_cfg& c, const void* base, int box_rows);
-
 namespace {
 
-constexpr int R = 16, TK = 32;
+constexpr int R = ATTN_ROWS_TILE, TK = ATTN_ROWS_KEYS;
 constexpr int NW = 8;                      // warps that compute
 constexpr int NTHR = (NW + 1) * 32;
 constexpr uint32_t HALF = TK * 128;        // 64 values of a tile's keys
-constexpr float SLACK = 8.0f;
 
 template <int DH>
 struct Cfg {
@@ -43,19 +35,6 @@ struct Cfg {
   static constexpr int OPITCH = D + 8;     // floats of a row of a warp's output in shared memory
 };
 
-struct RowsArgs {
-  CUtensorMap map_k, map_v;
-  AttnParams p;
-  int group;               // query heads of a key head
-  int page_shift, box_rows;
-  float c;                 // scale log2 e
-  unsigned* status;
-  unsigned* count;         // [blocks] parts of the item that begins in the block's run and ends behind it
-  char* part;
-  size_t slot;             // bytes of a partial result
-  unsigned long long timeout_ns;
-};
-
 template <int DH>
 struct Shared {
   alignas(1024) uint8_t ring[Cfg<DH>::NS * Cfg<DH>::STAGE];
@@ -65,19 +44,6 @@ struct Shared {
   AttnPlan plan;
   uint32_t abort, last;
 };
-
-__device__ __forceinline__ uint64_t* bp(unsigned long long& b) { return reinterpret_cast<uint64_t*>(&b); }
-
-// Bounded wait of a warp; once one ran out, the block's later waits do not wait.
-__device__ __forceinline__ bool warp_wait(unsigned long long& bar, uint32_t parity, volatile uint32_t* abort,
-                                          uint64_t timeout_ns, unsigned* status) {
-  bool ok = mbar_try_wait(bp(bar), parity);
-  if (!ok && !*abort) {
-    ok = mbar_wait_for(bp(bar), parity, timeout_ns, status);
-    if (!ok) *abort = 1u;
-  }
-  return __all_sync(0xffffffffu, ok);
-}
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -107,21 +73,11 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <bool BF>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if (BF) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 using Walk = AttnWalk<R, TK>;
 
 // ------------------------------------------------------------ the copying warp
 template <int DH>
-__device__ void run_copies(const RowsArgs& a, Shared<DH>& S) {
+__device__ void run_copies(const AttnArgs& a, Shared<DH>& S) {
   constexpr int NS = Cfg<DH>::NS;
   const int lane = threadIdx.x & 31;
   const int br = a.box_rows, nb = TK / br;
@@ -137,7 +93,7 @@ __device__ void run_copies(const RowsArgs& a, Shared<DH>& S) {
     int key = w.key0();
     pages.begin(a.p.s.table + w.b * a.p.s.ld_table, max(key, w.keys.lo) >> a.page_shift, (w.keys.hi - 1) >> a.page_shift);
     for (int j = 0; j < steps; ++j, key += TK) {
-      if (((used >> st) & 1u) && !warp_wait(S.empty[st], (par >> st) & 1u, &S.abort, a.timeout_ns, a.status)) {
+      if (((used >> st) & 1u) && !attn_wait(S.empty[st], (par >> st) & 1u, &S.abort, a.timeout_ns, a.status)) {
         ok = false;
         break;
       }
@@ -152,11 +108,11 @@ __device__ void run_copies(const RowsArgs& a, Shared<DH>& S) {
         atomicOr(a.status, (unsigned)MOE_STATUS_BAD_PAGE);
         id = a.p.c.kv.n_pages;  // outside: filled with zeros
       }
-      if (lane == 0) mbar_arrive_expect_tx(bp(S.full[st]), (uint32_t)__popc(boxes) * (uint32_t)br * 128u);
+      if (lane == 0) mbar_arrive_expect_tx(attn_bar(S.full[st]), (uint32_t)__popc(boxes) * (uint32_t)br * 128u);
       __syncwarp();
       if (mine)
         tma_load_4d(ring + st * Cfg<DH>::STAGE + dst0, val ? &a.map_v : &a.map_k, half * 64,
-                    k & (a.p.c.kv.page_size - 1), w.h, id, bp(S.full[st]));
+                    k & (a.p.c.kv.page_size - 1), w.h, id, attn_bar(S.full[st]));
       st = st + 1 == NS ? 0 : st + 1;
     }
   }
@@ -164,12 +120,12 @@ __device__ void run_copies(const RowsArgs& a, Shared<DH>& S) {
   // barrier's phase flips with every use, as `par` does from the second use on).
   const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
   for (uint32_t i = 0; i < NS; ++i)
-    if ((used >> i) & 1u) mbar_wait_bounded(bp(S.full[i]), (par >> i) & 1u, deadline, a.status);
+    if ((used >> i) & 1u) mbar_wait_bounded(attn_bar(S.full[i]), (par >> i) & 1u, deadline, a.status);
 }
 
 // ------------------------------------------------------------- the computing warps
 template <int DH, bool BF>
-__device__ __forceinline__ void load_q(const RowsArgs& a, const Walk& w, uint32_t (&qf)[DH * 4][4]) {
+__device__ __forceinline__ void load_q(const AttnArgs& a, const Walk& w, uint32_t (&qf)[DH * 4][4]) {
   const int lane = threadIdx.x & 31, t = lane & 3, D = a.p.c.kv.head_dim;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -193,7 +149,6 @@ template <int DH, bool BF>
 __device__ __forceinline__ void do_tile(const uint32_t base, int key, const AttnRange& keys, bool masked,
                                         const int (&lo)[2], const int (&hi)[2], float c, const uint32_t (&qf)[DH * 4][4],
                                         float (&o)[DH * 8][4], float (&m)[2], float (&l)[2]) {
-  constexpr float BIAS = BF ? 0.f : 6.f;
   const int lane = threadIdx.x & 31, t = lane & 3;
   const int mi = lane >> 3, r8 = lane & 7;
   float s[4][4] = {};
@@ -231,7 +186,7 @@ __device__ __forceinline__ void do_tile(const uint32_t base, int key, const Attn
   for (int i = 0; i < 2; ++i) {
     top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
     top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2)) * c;
-    rise |= top[i] > m[i] + SLACK;  // from -inf: by anything
+    rise |= top[i] > m[i] + ATTN_SLACK;  // from -inf: by anything
   }
   if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -249,7 +204,7 @@ __device__ __forceinline__ void do_tile(const uint32_t base, int key, const Attn
   }
   uint32_t pf[2][4];
   {
-    const float ref[2] = {(m[0] == -INFINITY ? 0.f : m[0]) - BIAS, (m[1] == -INFINITY ? 0.f : m[1]) - BIAS};
+    const float ref[2] = {(m[0] == -INFINITY ? 0.f : m[0]) - ATTN_BIAS<BF>, (m[1] == -INFINITY ? 0.f : m[1]) - ATTN_BIAS<BF>};
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       float e[4];
@@ -258,8 +213,8 @@ __device__ __forceinline__ void do_tile(const uint32_t base, int key, const Attn
         e[i] = exp2_fast(fmaf(s[n][i], c, -ref[i >> 1]));
         l[i >> 1] += e[i];
       }
-      pf[n >> 1][2 * (n & 1)] = pack2<BF>(e[0], e[1]);
-      pf[n >> 1][2 * (n & 1) + 1] = pack2<BF>(e[2], e[3]);
+      pf[n >> 1][2 * (n & 1)] = attn_pack2<BF>(e[0], e[1]);
+      pf[n >> 1][2 * (n & 1) + 1] = attn_pack2<BF>(e[2], e[3]);
     }
   }
   // values of slots that none of the rows sees may be anything: zeros
@@ -286,47 +241,8 @@ __device__ __forceinline__ void do_tile(const uint32_t base, int key, const Attn
   }
 }
 
-// Four values of one row: out of the sums over `n` parts (m, l, o of part i given by the functions).
-struct Joined {
-  float m, l;
-  float4 o;
-};
-template <class ML, class O>
-__device__ __forceinline__ Joined join(int n, ML ml, O o) {
-  Joined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int i = 0; i < n; ++i) j.m = fmaxf(j.m, ml(i).x);
-  const float ref = j.m == -INFINITY ? 0.f : j.m;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float2 v = ml(i);
-    if (v.y == 0.f) continue;  // nothing seen: its outputs were never written
-    const float f = exp2_fast(v.x - ref);
-    const float4 x = o(i);
-    j.l += f * v.y;
-    j.o.x += f * x.x;
-    j.o.y += f * x.y;
-    j.o.z += f * x.z;
-    j.o.w += f * x.w;
-  }
-  return j;
-}
-
-template <bool BF>
-__device__ __forceinline__ void store_out(const RowsArgs& a, const Walk& w, int r, int d, const Joined& j) {
-  constexpr float BIAS = BF ? 0.f : 6.f;
-  const int row = w.row0() + r, tok = row / a.group, hd = w.h * a.group + row - tok * a.group;
-  const long long t = w.q.row0 + tok;
-  const float s = j.l == 0.f ? 0.f : 1.f / j.l;
-  uint2 v;
-  v.x = pack2<BF>(j.o.x * s, j.o.y * s);
-  v.y = pack2<BF>(j.o.z * s, j.o.w * s);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.p.out) + t * a.p.ldo + (long long)hd * a.p.c.kv.head_dim + d) = v;
-  if (d == 0 && a.p.lse)
-    a.p.lse[t * a.p.ld_lse + hd] = j.l == 0.f ? -INFINITY : (j.m + log2f(j.l) - BIAS) * 0.69314718055994531f;
-}
-
 template <int DH, bool BF>
-__device__ void run_rows(const RowsArgs& a, Shared<DH>& S) {
+__device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
   constexpr int NS = Cfg<DH>::NS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int D = a.p.c.kv.head_dim, d4 = D / 4;
@@ -356,13 +272,13 @@ __device__ void run_rows(const RowsArgs& a, Shared<DH>& S) {
       for (; j < (uint32_t)steps; j += NW) {
         const uint32_t st = (u + j) % NS, par = ((u + j) / NS) & 1u;
         const int key = w.key0() + (int)j * TK;
-        if (warp_wait(S.full[st], par, &S.abort, a.timeout_ns, a.status))
+        if (attn_wait(S.full[st], par, &S.abort, a.timeout_ns, a.status))
           do_tile<DH, BF>(ring + st * Cfg<DH>::STAGE, key, w.keys, key < lo_all || key + TK > hi_all, lo, hi, a.c, qf, o,
                           m, l);
         else
           l[0] = l[1] = NAN;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bp(S.empty[st]));
+        if (lane == 0) mbar_arrive(attn_bar(S.empty[st]));
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -389,11 +305,11 @@ __device__ void run_rows(const RowsArgs& a, Shared<DH>& S) {
     float* part = reinterpret_cast<float*>(a.part + (2 * (size_t)blockIdx.x + (w.skip ? 0 : 1)) * a.slot);
     for (int i = tid; i < rows * d4; i += NW * 32) {
       const int r = i / d4, d = (i - r * d4) * 4;
-      const Joined v = join(
+      const AttnJoined v = attn_join(
           NW, [&](int x) { return *reinterpret_cast<const float2*>(S.ml[x][r]); },
           [&](int x) { return *reinterpret_cast<const float4*>(&S.o[x][r][d]); });
       if (whole) {
-        store_out<BF>(a, w, r, d, v);
+        attn_store<BF>(a, w.q.row0, w.h, w.row0() + r, d, v);
       } else {
         *reinterpret_cast<float4*>(part + (size_t)R * 2 + r * D + d) = v.o;
         if (d == 0) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(v.m, v.l);
@@ -404,8 +320,8 @@ __device__ void run_rows(const RowsArgs& a, Shared<DH>& S) {
       named_bar_sync(1, NW * 32);
       if (tid == 0) {
         __threadfence();
-        const bool last = atomicAdd(a.count + c0, 1u) == (unsigned)(n - 1);
-        if (last) a.count[c0] = 0u;
+        const bool last = atomicAdd(a.count + 2 * c0, 1u) == (unsigned)(n - 1);
+        if (last) a.count[2 * c0] = 0u;
         S.last = last;
       }
       named_bar_sync(1, NW * 32);
@@ -416,10 +332,10 @@ __device__ void run_rows(const RowsArgs& a, Shared<DH>& S) {
         };
         for (int i = tid; i < rows * d4; i += NW * 32) {
           const int r = i / d4, d = (i - r * d4) * 4;
-          const Joined v = join(
+          const AttnJoined v = attn_join(
               n, [&](int x) { return __ldcg(reinterpret_cast<const float2*>(at(x) + 2 * r)); },
               [&](int x) { return __ldcg(reinterpret_cast<const float4*>(at(x) + R * 2 + r * D + d)); });
-          store_out<BF>(a, w, r, d, v);
+          attn_store<BF>(a, w.q.row0, w.h, w.row0() + r, d, v);
         }
       }
     }
@@ -428,14 +344,14 @@ __device__ void run_rows(const RowsArgs& a, Shared<DH>& S) {
 }
 
 template <int DH, bool BF>
-__global__ void __launch_bounds__(NTHR, 1) k_attn_rows(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(NTHR, 1) k_attn_rows(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t raw_smem[];
   Shared<DH>& S = *reinterpret_cast<Shared<DH>*>(raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u));
   grid_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < Cfg<DH>::NS; ++i) {
-      mbar_init(bp(S.full[i]), 1);
-      mbar_init(bp(S.empty[i]), 1);
+      mbar_init(attn_bar(S.full[i]), 1);
+      mbar_init(attn_bar(S.empty[i]), 1);
     }
     S.abort = 0u;
     fence_mbar_init();
@@ -447,7 +363,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_rows(const __grid_constant__ R
 }
 
 template <int DH, bool BF>
-int launch(const RowsArgs& a, int ctas, cudaStream_t s) {
+int launch(const AttnArgs& a, int ctas, cudaStream_t s) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   const auto kernel = k_attn_rows<DH, BF>;
@@ -461,62 +377,11 @@ int launch(const RowsArgs& a, int ctas, cudaStream_t s) {
   return launch_overlapped(kernel, dim3((unsigned)ctas), dim3(NTHR), (size_t)SMEM, s, a);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
 }  // namespace
 
-// The cache as [n_pages][kv_heads][page_size][head_dim] in boxes of 64 values x
-// box_rows slots (128-byte swizzle); values past head_dim read zero.
-bool make_cache_map(CUtensorMap* m, const moe_v41_kv_cfg& c, const void* base, int box_rows) {
-  auto fn = encode_fn();
-  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads,
-                              (cuuint64_t)c.n_pages};
-  // a pitch that is never stepped by may be anything to the caller, but not to the map
-  const cuuint64_t strides[3] = {(cuuint64_t)c.token_pitch * 2, (cuuint64_t)(c.kv_heads > 1 ? c.head_pitch : c.head_dim) * 2,
-                                 (cuuint64_t)(c.n_pages > 1 ? c.page_pitch : c.head_dim) * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-size_t attn_workspace_bytes(const moe_v41_attn_cfg& c) { return attn_ws(c).total; }
-
-int launch_paged_attention(const AttnParams& p, int max_new, void* ws, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    return MOE_ERR_CUDA;
-  const moe_v41_kv_cfg& kv = p.c.kv;
-  RowsArgs a{};
-  a.box_rows = kv.page_size < TK ? kv.page_size : TK;
-  if (!make_cache_map(&a.map_k, kv, p.k_cache, a.box_rows) || !make_cache_map(&a.map_v, kv, p.v_cache, a.box_rows))
-    return MOE_ERR_CUDA;
-  const AttnWs w = attn_ws(p.c);
-  uint8_t* base = static_cast<uint8_t*>(ws);
-  a.p = p;
-  a.group = p.c.heads / kv.kv_heads;
-  a.page_shift = __builtin_ctz((unsigned)kv.page_size);
-  a.c = p.c.scale * 1.4426950408889634f;
-  a.status = &reinterpret_cast<Ctrl*>(base)->status;
-  a.count = reinterpret_cast<unsigned*>(base + w.count);
-  a.part = reinterpret_cast<char*>(base + w.part);
-  a.slot = w.slot;
-  a.timeout_ns = 2000000000ull;
-  const int ctas = sms < ATTN_MAX_CTAS ? sms : ATTN_MAX_CTAS;
-  const bool bf = kv.type == MOE_T_BF16;
-  if (kv.head_dim > 64) return bf ? launch<2, true>(a, ctas, s) : launch<2, false>(a, ctas, s);
+int launch_attn_rows(const AttnArgs& a, int ctas, cudaStream_t s) {
+  const bool bf = a.p.c.kv.type == MOE_T_BF16;
+  if (a.p.c.kv.head_dim > 64) return bf ? launch<2, true>(a, ctas, s) : launch<2, false>(a, ctas, s);
   return bf ? launch<1, true>(a, ctas, s) : launch<1, false>(a, ctas, s);
 }
 
