@@ -3,7 +3,7 @@
 // sequence and key head, against the tiles of TK keys that any of its rows sees.
 // The items, numbered sequence by sequence, in it head by head, in it row tile by
 // row tile, make one line of key tiles (an item that sees none counts as one),
-// which is cut into equal runs, one for each block: whatever the lengths, the
+// which is cut into about equal runs, one for each block: whatever the lengths, the
 // blocks have the same work.  An item that a cut goes through is joined
 // by the last of its blocks to finish, in the order of the runs.
 //
@@ -62,12 +62,13 @@ struct AttnWork {
   static __device__ __forceinline__ int cost(const AttnParams& p, const AttnSeq& q, int group, int i) {
     return max(1, key_tiles(range(p, q, group, i)));
   }
-  // Key tiles of one key head of each lane's sequence (0 where !valid), by a whole warp.
-  static __device__ long long seq_cost(const AttnParams& p, int group, int b, bool valid) {
+  // Key tiles of one key head of each lane's sequence (0 where !valid), and its row tiles, by a whole warp.
+  static __device__ long long seq_cost(const AttnParams& p, int group, int b, bool valid, int* rows = nullptr) {
     const int lane = threadIdx.x & 31;
     AttnSeq q{};
     if (valid) q = attn_seq(p, b);
     const int nt = row_tiles(q, group);
+    if (rows) *rows = nt;
     long long c = nt == 1 ? cost(p, q, group, 0) : 0;
     unsigned many = __ballot_sync(0xffffffffu, nt > 1);
     while (many) {
@@ -89,50 +90,79 @@ struct AttnWork {
   }
 };
 
-// The cut, and where this block's run begins.
+// The cut, and where this block's run begins and ends.
 struct AttnPlan {
-  long long warp_sum[32];
-  long long total;         // key tiles of the call
-  long long base, per_head;  // of the sequence in which the run begins: its place, and a head's key tiles
-  int runs;                // blocks that have work
-  int b, h, i, skip;       // the run's first item, and its key tiles that belong to the run before
+  long long sum[32], items[32];
+  long long total;           // key tiles of the call
+  int runs;                  // blocks that have work
+  long long base[2], per_head[2];  // of the sequences in which the run begins and ends: place, a head's key tiles
+  int b[2];
+  long long begin, end;      // the run
+  int h, i, skip;            // its first item (of sequence b[0]), and the key tiles of it that belong to the run before
 };
 
-__device__ __forceinline__ long long attn_run_begin(const AttnPlan& S, int run) { return S.total * run / S.runs; }
-// The run that holds place x of the line.
-__device__ __forceinline__ int attn_run_of(const AttnPlan& S, long long x) {
-  return (int)(((x + 1) * S.runs + S.total - 1) / S.total) - 1;
-}
+// Places x where an even cut would fall, moved to an item's end if that is less
+// than SNAP key tiles away: an item is cut only where both parts are worth the join.
+template <int SNAP>
+struct AttnCut {
+  static __device__ __forceinline__ long long even(const AttnPlan& S, int run) { return S.total * run / S.runs; }
+  static __device__ __forceinline__ long long moved(long long x, long long begin, long long end) {
+    return x - begin >= SNAP && end - x >= SNAP ? x : x - begin <= end - x ? begin : end;
+  }
+  // The runs that hold parts of the item begin .. end - 1: first, and how many.
+  static __device__ __forceinline__ int parts(const AttnPlan& S, long long begin, long long end, int* first) {
+    const long long lo = ((begin + SNAP) * S.runs + S.total - 1) / S.total;      // first cut inside
+    const long long hi = ((end - SNAP + 1) * S.runs + S.total - 1) / S.total - 1;  // last cut inside
+    *first = (int)lo - 1;
+    return (int)(hi - lo) + 2;
+  }
+};
 
-// By all NT threads of the block; ends with a barrier.
-template <int R, int TK, int NT>
+// By all NT threads of the block; ends with a barrier.  As many runs as there are
+// blocks, if each has MIN_RUN key tiles or an item.
+template <int R, int TK, int NT, int MIN_RUN, int SNAP>
 __device__ void attn_plan(const AttnParams& p, int group, AttnPlan& S) {
   using W = AttnWork<R, TK>;
+  using Cut = AttnCut<SNAP>;
   constexpr int NWARP = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int batch = p.s.batch, kh = p.c.kv.kv_heads;
-  long long mine = 0, first = 0;  // all of this thread's sequences; the first
+  long long mine = 0, first = 0, items = 0;  // all of this thread's sequences; the first
   for (int b0 = 0; b0 < batch; b0 += NT) {
-    const long long c = W::seq_cost(p, group, b0 + tid, b0 + tid < batch) * kh;
+    int n = 0;
+    const long long c = W::seq_cost(p, group, b0 + tid, b0 + tid < batch, &n) * kh;
     mine += c;
+    items += (long long)n * kh;
     if (b0 == 0) first = c;
   }
 #pragma unroll
-  for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-  if (lane == 0) S.warp_sum[warp] = mine;
+  for (int d = 16; d; d >>= 1) {
+    mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    items += __shfl_xor_sync(0xffffffffu, items, d);
+  }
+  if (lane == 0) {
+    S.sum[warp] = mine;
+    S.items[warp] = items;
+  }
   __syncthreads();
-  long long total = 0;
-  for (int w = 0; w < NWARP; ++w) total += S.warp_sum[w];
+  long long total = 0, all = 0;
+  for (int w = 0; w < NWARP; ++w) {
+    total += S.sum[w];
+    all += S.items[w];
+  }
   __syncthreads();
-  const int runs = (int)min((long long)gridDim.x, total);
+  const int runs = (int)min((long long)gridDim.x, max(total / MIN_RUN, all));
   if (tid == 0) {
     S.total = total;
     S.runs = runs;
+    S.begin = S.end = 0;
   }
-  if ((int)blockIdx.x < runs) {
-    const long long x0 = total * (int)blockIdx.x / runs;
+  const int run = (int)blockIdx.x;
+  if (run < runs) {
+    // the items that the even cuts fall into: the run's first and the next run's
+    const long long x[2] = {total * run / runs, total * (run + 1) / runs};
     long long base = 0;
-    for (int b0 = 0; b0 < batch && base <= x0; b0 += NT) {
+    for (int b0 = 0; b0 < batch && base <= x[1]; b0 += NT) {
       const long long c = b0 == 0 ? first : W::seq_cost(p, group, b0 + tid, b0 + tid < batch) * kh;
       long long s = c;
 #pragma unroll
@@ -140,47 +170,60 @@ __device__ void attn_plan(const AttnParams& p, int group, AttnPlan& S) {
         const long long v = __shfl_up_sync(0xffffffffu, s, d);
         if (lane >= d) s += v;
       }
-      if (lane == 31) S.warp_sum[warp] = s;
+      if (lane == 31) S.sum[warp] = s;
       __syncthreads();
       long long before = base;
       for (int w = 0; w < NWARP; ++w) {
-        if (w < warp) before += S.warp_sum[w];
-        base += S.warp_sum[w];
+        if (w < warp) before += S.sum[w];
+        base += S.sum[w];
       }
       __syncthreads();
       const long long at = before + s - c;
-      if (at <= x0 && x0 < at + c) {
-        S.b = b0 + tid;
-        S.base = at;
-        S.per_head = c / kh;
-      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (at <= x[e] && x[e] < at + c) {
+          S.b[e] = b0 + tid;
+          S.base[e] = at;
+          S.per_head[e] = c / kh;
+        }
     }
     __syncthreads();
-    if (warp == 0) {
-      const AttnSeq q = attn_seq(p, S.b);
-      const int nt = W::row_tiles(q, group);
-      long long rem = x0 - S.base;
-      const int h = (int)(rem / S.per_head);
-      rem -= h * S.per_head;
-      for (int i0 = 0; i0 < nt; i0 += 32) {
-        const int i = i0 + lane;
-        const long long c = i < nt ? W::cost(p, q, group, i) : 0;
-        long long s = c;
+    if (warp < 2) {
+      const long long xe = warp ? x[1] : x[0];
+      if (xe == total) {
+        if (lane == 0) S.end = total;
+      } else {
+        const AttnSeq q = attn_seq(p, S.b[warp]);
+        const int nt = W::row_tiles(q, group);
+        long long rem = xe - S.base[warp];
+        const int h = (int)(rem / S.per_head[warp]);
+        rem -= h * S.per_head[warp];
+        for (int i0 = 0; i0 < nt; i0 += 32) {
+          const int i = i0 + lane;
+          const long long c = i < nt ? W::cost(p, q, group, i) : 0;
+          long long s = c;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, s, d);
-          if (lane >= d) s += v;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, rem < s);
-        if (past) {
-          if (lane == __ffs((int)past) - 1) {
-            S.h = h;
-            S.i = i;
-            S.skip = (int)(rem - (s - c));
+          for (int d = 1; d < 32; d <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += v;
           }
-          break;
+          const unsigned past = __ballot_sync(0xffffffffu, rem < s);
+          if (past) {
+            if (lane == __ffs((int)past) - 1) {
+              const long long begin = xe - (rem - (s - c)), to = Cut::moved(xe, begin, begin + c);
+              if (warp == 0) {
+                S.begin = to;
+                S.h = h;
+                S.i = i;
+                S.skip = (int)(to - begin);
+              } else {
+                S.end = to;
+              }
+            }
+            break;
+          }
+          rem -= __shfl_sync(0xffffffffu, s, 31);
         }
-        rem -= __shfl_sync(0xffffffffu, s, 31);
       }
     }
   }
@@ -203,17 +246,18 @@ struct AttnWalk {
   bool live;
 
   __device__ __forceinline__ AttnWalk(const AttnParams& p_, int group_, const AttnPlan& S) : p(p_), group(group_) {
-    live = (int)blockIdx.x < S.runs;
+    at = S.begin;
+    left = S.end - at;
+    live = left > 0;
     if (!live) return;
-    at = attn_run_begin(S, (int)blockIdx.x);
-    left = attn_run_begin(S, (int)blockIdx.x + 1) - at;
-    b = S.b;
+    b = S.b[0];
     h = S.h;
     i = S.i;
     skip = S.skip;
     q = attn_seq(p, b);
     row_tiles = W::row_tiles(q, group);
     set();
+    if (take == 0) next();  // the cut was moved to the item's end
   }
   __device__ __forceinline__ void set() {
     keys = W::range(p, q, group, i);
@@ -326,13 +370,13 @@ __device__ __forceinline__ AttnJoined attn_join(int n, ML ml, O o) {
   AttnJoined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   for (int i = 0; i < n; ++i) j.m = fmaxf(j.m, ml(i).x);
   const float ref = j.m == -INFINITY ? 0.f : j.m;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < n; ++i) {
     const float2 v = ml(i);
-    if (v.y == 0.f) continue;  // nothing seen: its outputs were never written
+    const float4 x = o(i);
+    if (v.y == 0.f) continue;  // nothing seen: its outputs may never have been written
     float f;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(v.x - ref));
-    const float4 x = o(i);
     j.l += f * v.y;
     j.o.x += f * x.x;
     j.o.y += f * x.y;

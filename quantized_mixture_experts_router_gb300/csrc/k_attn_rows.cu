@@ -3,7 +3,7 @@
 // head) an item.
 //   o = sum_j p_j v_j / sum_j p_j,   p_j = exp2(c s_j - m),   s = q k_j,   c = scale log2 e
 //
-// Bound by the cache's bytes.  A block a SM, with a warp that copies tiles of 32
+// Bound by the cache's bytes.  A block a SM, with warps that copy tiles of 32
 // keys and values (TMA boxes of a page's slots, 128-byte swizzle) into one ring
 // and eight warps that take the tiles in turn, each with its own running maximum,
 // sum and output (rows x values, in registers), so that no barrier is passed
@@ -20,7 +20,10 @@ namespace {
 
 constexpr int R = ATTN_ROWS_TILE, TK = ATTN_ROWS_KEYS;
 constexpr int NW = 8;                      // warps that compute
-constexpr int NTHR = (NW + 1) * 32;
+constexpr int NP = 4;                      // warps that copy
+constexpr int NTHR = (NW + NP) * 32;
+// A block's warps work on eight tiles at once, so that a run of fewer is no shorter.
+constexpr int MIN_RUN = NW, SNAP = NW / 2;
 constexpr uint32_t HALF = TK * 128;        // 64 values of a tile's keys
 
 template <int DH>
@@ -75,13 +78,16 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 
 using Walk = AttnWalk<R, TK>;
 
-// ------------------------------------------------------------ the copying warp
+// ------------------------------------------------------------ the copying warps
+// A warp issues one box after the other, about 100 cycles each, which for small
+// pages is more than a tile may take: each copies a quarter of a tile's boxes, those
+// of its half of the keys' or values' widths, or every other page's.
 template <int DH>
-__device__ void run_copies(const AttnArgs& a, Shared<DH>& S) {
+__device__ void run_copies(const AttnArgs& a, Shared<DH>& S, int pw) {
   constexpr int NS = Cfg<DH>::NS;
   const int lane = threadIdx.x & 31;
   const int br = a.box_rows, nb = TK / br;
-  const int box = lane % nb, half = lane / nb % DH, val = lane / nb / DH;
+  const int val = pw & 1, half = DH == 2 ? pw >> 1 : 0, box = DH == 2 ? lane : 2 * lane + (pw >> 1);
   const uint32_t ring = smem_u32(S.ring);
   const uint32_t dst0 = (uint32_t)(val * DH + half) * HALF + (uint32_t)(box * br) * 128u;
   uint32_t st = 0, par = 0, used = 0;  // par: the phase of each stage's empty barrier that is waited for next
@@ -93,14 +99,16 @@ __device__ void run_copies(const AttnArgs& a, Shared<DH>& S) {
     int key = w.key0();
     pages.begin(a.p.s.table + w.b * a.p.s.ld_table, max(key, w.keys.lo) >> a.page_shift, (w.keys.hi - 1) >> a.page_shift);
     for (int j = 0; j < steps; ++j, key += TK) {
-      if (((used >> st) & 1u) && !attn_wait(S.empty[st], (par >> st) & 1u, &S.abort, a.timeout_ns, a.status)) {
-        ok = false;
-        break;
+      if ((used >> st) & 1u) {
+        if (!attn_wait(S.empty[st], (par >> st) & 1u, &S.abort, a.timeout_ns, a.status)) {
+          ok = false;
+          break;
+        }
+        par ^= 1u << st;
       }
-      if ((used >> st) & 1u) par ^= 1u << st;
       used |= 1u << st;
       const int k = key + box * br;
-      const bool mine = val < 2 && k + br > w.keys.lo && k < w.keys.hi;
+      const bool mine = box < nb && k + br > w.keys.lo && k < w.keys.hi;
       pages.advance(max(key, w.keys.lo) >> a.page_shift);
       int id = pages.at(min(max(k, w.keys.lo), w.keys.hi - 1) >> a.page_shift);
       const unsigned boxes = __ballot_sync(0xffffffffu, mine);
@@ -316,7 +324,8 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
       }
     }
     if (!whole) {
-      const int c0 = attn_run_of(S.plan, w.begin()), c1 = attn_run_of(S.plan, w.end() - 1), n = c1 - c0 + 1;
+      int c0;
+      const int n = AttnCut<SNAP>::parts(S.plan, w.begin(), w.end(), &c0);
       named_bar_sync(1, NW * 32);
       if (tid == 0) {
         __threadfence();
@@ -330,10 +339,16 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
         auto at = [&](int x) {
           return reinterpret_cast<const float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot);
         };
+        float2* ml = reinterpret_cast<float2*>(&S.o[0][0][0]);  // [n][rows]
+        for (int i = tid; i < n * rows; i += NW * 32) {
+          const int x = i / rows;
+          ml[i] = __ldcg(reinterpret_cast<const float2*>(at(x)) + i - x * rows);
+        }
+        named_bar_sync(1, NW * 32);
         for (int i = tid; i < rows * d4; i += NW * 32) {
           const int r = i / d4, d = (i - r * d4) * 4;
           const AttnJoined v = attn_join(
-              n, [&](int x) { return __ldcg(reinterpret_cast<const float2*>(at(x) + 2 * r)); },
+              n, [&](int x) { return ml[x * rows + r]; },
               [&](int x) { return __ldcg(reinterpret_cast<const float4*>(at(x) + R * 2 + r * D + d)); });
           attn_store<BF>(a, w.q.row0, w.h, w.row0() + r, d, v);
         }
@@ -350,16 +365,16 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_rows(const __grid_constant__ A
   grid_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < Cfg<DH>::NS; ++i) {
-      mbar_init(attn_bar(S.full[i]), 1);
+      mbar_init(attn_bar(S.full[i]), NP);
       mbar_init(attn_bar(S.empty[i]), 1);
     }
     S.abort = 0u;
     fence_mbar_init();
   }
   grid_wait();
-  attn_plan<R, TK, NTHR>(a.p, a.group, S.plan);
+  attn_plan<R, TK, NTHR, MIN_RUN, SNAP>(a.p, a.group, S.plan);
   if (threadIdx.x < NW * 32) run_rows<DH, BF>(a, S);
-  else run_copies<DH>(a, S);
+  else run_copies<DH>(a, S, (int)(threadIdx.x >> 5) - NW);
 }
 
 template <int DH, bool BF>

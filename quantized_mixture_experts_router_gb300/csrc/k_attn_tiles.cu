@@ -8,8 +8,8 @@
 //   warps 0-3, 4-7   softmax of the first and second row tile, a row a thread: S out
 //                    of tensor memory, maximum, P as 16-bit values over S, sum
 //   warp 8           issues the products; zeroes value slots that nobody sees
-//   warp 9           copies keys and values (TMA boxes of a page's slots) into a ring
-//   warps 10, 11     copy the queries of the first and second tile
+//   warps 9, 10      copy keys and values (TMA boxes of a page's slots) into rings
+//   warp 11          copies the queries
 // While one row tile is in its softmax the tensor cores work on the other:
 //   Q0 K(u) | P1 V(u-1) | Q1 K(u) | P0 V(u) | Q0 K(u+1) ...
 // V lies in shared memory as it lies in the cache, [key][value], and is read as an
@@ -24,7 +24,9 @@ namespace moe {
 namespace {
 
 constexpr int R = ATTN_TILES_TILE, TK = ATTN_TILES_KEYS, TR = 128;
-constexpr int W_MMA = 8, W_KV = 9, W_Q = 10;
+constexpr int W_MMA = 8, W_K = 9, W_V = 10, W_Q = 11;
+// A join costs about as much as four key tiles.
+constexpr int MIN_RUN = 4, SNAP = 4;
 constexpr int NTHR = 384;
 // Registers a thread: 168 at launch; the softmax warps take what the others leave.
 constexpr int REG_LAUNCH = 168, REG_SOFT = 216, REG_REST = 72;
@@ -34,7 +36,9 @@ constexpr uint32_t HALF = TK * 128;  // 64 values of 128 keys or rows
 template <int DH>
 struct Cfg {
   static constexpr uint32_t SLOT = DH * HALF;   // keys or values of a tile; queries of a row tile
-  static constexpr int NS = DH == 2 ? 5 : 10;
+  // A key tile is done with once both row tiles' scores are, a value tile half a tile later.
+  static constexpr int NK = DH == 2 ? 2 : 4, NV = DH == 2 ? 3 : 6;
+  static constexpr int NS = NK + NV;
 };
 
 struct TilesCtl {
@@ -92,10 +96,11 @@ __device__ __forceinline__ void warp_arrive(unsigned long long& b) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(attn_bar(b));
 }
 
-// ------------------------------------------------------------ keys and values
-template <int DH>
-__device__ void run_kv(const AttnArgs& a, TilesCtl& C, uint32_t ring) {
-  constexpr int NS = Cfg<DH>::NS;
+// ------------------------------------------------------------ keys, values
+// NS slots from `ring` on, their barriers from `full` and `empty` on.
+template <int DH, int NS>
+__device__ void run_copies(const AttnArgs& a, TilesCtl& C, const CUtensorMap* map, uint32_t ring, unsigned long long* full,
+                           unsigned long long* empty) {
   const Env E{a, C};
   const int lane = threadIdx.x & 31, br = a.box_rows, nb = TK / br;
   const int box = lane % nb, half = lane / nb;
@@ -108,79 +113,78 @@ __device__ void run_kv(const AttnArgs& a, TilesCtl& C, uint32_t ring) {
     AttnPages pages;
     int key = w.key0();
     pages.begin(a.p.s.table + w.b * a.p.s.ld_table, max(key, w.keys.lo) >> a.page_shift, (w.keys.hi - 1) >> a.page_shift);
-    for (int j = 0; ok && j < steps; ++j, key += TK) {
+    for (int j = 0; j < steps; ++j, key += TK) {
+      if ((used >> st) & 1u) {
+        if (!E.wait(empty[st], (par >> st) & 1u)) {
+          ok = false;
+          break;
+        }
+        par ^= 1u << st;
+      }
+      used |= 1u << st;
       const int k = key + box * br;
       const bool mine = half < DH && k + br > w.keys.lo && k < w.keys.hi;
       pages.advance(max(key, w.keys.lo) >> a.page_shift);
       int id = pages.at(min(max(k, w.keys.lo), w.keys.hi - 1) >> a.page_shift);
-      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * (uint32_t)br * 128u;
+      const unsigned boxes = __ballot_sync(0xffffffffu, mine);
       if (mine && (id < 0 || id >= a.p.c.kv.n_pages)) {
         atomicOr(a.status, (unsigned)MOE_STATUS_BAD_PAGE);
         id = a.p.c.kv.n_pages;  // outside: filled with zeros
       }
-#pragma unroll 1
-      for (int val = 0; val < 2; ++val) {
-        if ((used >> st) & 1u) {
-          if (!E.wait(C.empty[st], (par >> st) & 1u)) {
-            ok = false;
-            break;
-          }
-          par ^= 1u << st;
-        }
-        used |= 1u << st;
-        if (lane == 0) mbar_arrive_expect_tx(attn_bar(C.full[st]), bytes);
-        __syncwarp();
-        if (mine)
-          tma_load_4d(ring + st * Cfg<DH>::SLOT + dst0, val ? &a.map_v : &a.map_k, half * 64,
-                      k & (a.p.c.kv.page_size - 1), w.h, id, attn_bar(C.full[st]));
-        st = st + 1 == NS ? 0 : st + 1;
-      }
+      if (lane == 0) mbar_arrive_expect_tx(attn_bar(full[st]), (uint32_t)__popc(boxes) * (uint32_t)br * 128u);
+      __syncwarp();
+      if (mine)
+        tma_load_4d(ring + st * Cfg<DH>::SLOT + dst0, map, half * 64, k & (a.p.c.kv.page_size - 1), w.h, id,
+                    attn_bar(full[st]));
+      st = st + 1 == NS ? 0 : st + 1;
     }
   }
   // copies in flight land before the block can exit: each slot's last one
   const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
   for (uint32_t i = 0; i < NS; ++i)
-    if ((used >> i) & 1u) mbar_wait_bounded(attn_bar(C.full[i]), (par >> i) & 1u, deadline, a.status);
+    if ((used >> i) & 1u) mbar_wait_bounded(attn_bar(full[i]), (par >> i) & 1u, deadline, a.status);
 }
 
 // ------------------------------------------------------------ queries
-// A row tile's queries into the swizzled layout, rows and values that there are
+// The row tiles' queries into the swizzled layout, rows and values that there are
 // none of as zeros.
 template <int DH>
-__device__ void run_q(const AttnArgs& a, TilesCtl& C, uint32_t q_smem, int s) {
+__device__ void run_q(const AttnArgs& a, TilesCtl& C, uint32_t q_smem) {
   const Env E{a, C};
   const int lane = threadIdx.x & 31, D = a.p.c.kv.head_dim;
   constexpr int CH = DH * 8;         // 16-byte pieces of a row
   constexpr int RPI = 32 / CH;       // rows an instruction of the warp covers
   const int ch = lane % CH, rr = lane / CH;
   const bool in = ch * 8 < D;
-  uint32_t uses = 0;
+  const uint16_t* q = static_cast<const uint16_t*>(a.p.q);
+  uint32_t uses[2] = {};
   for (Walk w(a.p, a.group, C.plan); w.live; w.next()) {
-    const Tile T(a, w, s);
-    if (T.first >= T.end) continue;
-    if (!E.wait(C.q_empty[s], (uses & 1u) ^ 1u)) return;  // passes at once the first time
-    ++uses;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const Tile T(a, w, s);
+      if (T.first >= T.end) continue;
+      if (!E.wait(C.q_empty[s], (uses[s]++ & 1u) ^ 1u)) return;  // passes at once the first time
 #pragma unroll 1
-    for (int r0 = 0; r0 < TR; r0 += 32) {
-      // each lane finds one of 32 rows
-      const int r = r0 + lane, row = w.row0() + s * TR + r, tok = row / a.group;
-      const long long at = (w.q.row0 + tok) * a.p.ldq + (long long)(w.h * a.group + row - tok * a.group) * D;
-      const long long off = r < T.rows ? at : -1;
+      for (int r0 = 0; r0 < TR; r0 += 32) {
+        // each lane finds one of 32 rows
+        const int r = r0 + lane, row = w.row0() + s * TR + r, tok = row / a.group;
+        const long long at = (w.q.row0 + tok) * a.p.ldq + (long long)(w.h * a.group + row - tok * a.group) * D;
+        const long long off = r < T.rows ? at : -1;
 #pragma unroll 8
-      for (int i = 0; i < 32; i += RPI) {
-        const long long o = __shfl_sync(0xffffffffu, off, i + rr);
-        const int rw = r0 + i + rr;
-        const uint32_t dst = q_smem + (uint32_t)(ch / 8) * HALF + swz(rw, ch & 7);
-        const uint16_t* src = static_cast<const uint16_t*>(a.p.q) + (o >= 0 ? o : 0) + ch * 8;
-        const int n = o >= 0 && in ? 16 : 0;
-        if (n == 0) src = static_cast<const uint16_t*>(a.p.q);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+        for (int i = 0; i < 32; i += RPI) {
+          const long long o = __shfl_sync(0xffffffffu, off, i + rr);
+          const bool there = o >= 0 && in;
+          const uint32_t dst = q_smem + (uint32_t)s * Cfg<DH>::SLOT + (uint32_t)(ch / 8) * HALF + swz(r0 + i + rr, ch & 7);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(there ? q + o + ch * 8 : q),
+                       "r"(there ? 16 : 0)
+                       : "memory");
+        }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(attn_bar(C.q_full[s]));
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(attn_bar(C.q_full[s]));
   }
 }
 
@@ -290,10 +294,10 @@ struct Issuer {
 
 template <int DH, bool BF>
 __device__ __forceinline__ bool issue_all(Issuer<DH, BF>& I, uint8_t* ring_ptr) {
-  constexpr int NS = Cfg<DH>::NS;
+  constexpr int NK = Cfg<DH>::NK, NV = Cfg<DH>::NV;
   const AttnArgs& a = I.a;
   TilesCtl& C = I.C;
-  uint32_t st = 0;
+  uint32_t ks = NK - 1, vs = NK + NV - 1;  // slots
   bool pending = false;  // the second row tile's product of the tile before
   Product P1{};
   for (Walk w(a.p, a.group, C.plan); w.live; w.next()) {
@@ -304,8 +308,8 @@ __device__ __forceinline__ bool issue_all(Issuer<DH, BF>& I, uint8_t* ring_ptr) 
     for (int k = from; k < from + steps; ++k) {
       const int key0 = k * TK;
       const bool h0 = T0.has(k), h1 = T1.has(k);
-      const uint32_t ks = st, vs = ks + 1 == NS ? 0 : ks + 1;
-      st = vs + 1 == NS ? 0 : vs + 1;
+      ks = ks + 1 == NK ? 0 : ks + 1;
+      vs = vs + 1 == NK + NV ? NK : vs + 1;
       auto product = [&](const Tile& T) {
         return Product{vs, max(T.keys.lo - key0, 0) / 16, (min(T.keys.hi - key0, TK) + 15) / 16, k == T.first,
                        k == T.end - 1};
@@ -411,11 +415,62 @@ __device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, in
   tmem_wait_st();
 }
 
+// Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left, a warp 16
+// rows at a time: lane r keeps row r's maximum and sum, and each lane four values
+// of every row, so that 16 loads are in flight.
+template <bool BF>
+__device__ void join_rows(const AttnArgs& a, const Walk& w, int s, int c0, int n, int rows) {
+  const int lane = threadIdx.x & 31, D = a.p.c.kv.head_dim;
+  const bool in = 4 * lane < D;
+  auto part = [&](int x) {
+    return reinterpret_cast<const float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot);
+  };
+#pragma unroll 1
+  for (int r0 = ((threadIdx.x >> 5) & 3) * 16; r0 < rows; r0 += 64) {
+    const int live = min(rows - r0, 16);
+    const int first = s * TR + r0;  // row of the item
+    auto ml = [&](int x) { return __ldcg(reinterpret_cast<const float2*>(part(x)) + first + lane); };
+    float m = -INFINITY, l = 0.f;
+    if (lane < live)
+      for (int x = 0; x < n; ++x) m = fmaxf(m, ml(x).x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float4 acc[16] = {};
+#pragma unroll 1
+    for (int x = 0; x < n; ++x) {
+      const float4* o = reinterpret_cast<const float4*>(part(x) + 2 * R + (size_t)first * D) + lane;
+      float4 v[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v[r] = r < live && in ? __ldcg(o + r * (D / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float f = 0.f;
+      if (lane < live) {
+        const float2 v = ml(x);
+        if (v.y != 0.f) {  // (0: nothing seen)
+          f = exp2_fast(v.x - ref);
+          l += f * v.y;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float g = __shfl_sync(0xffffffffu, f, r);
+        acc[r].x = fmaf(g, v[r].x, acc[r].x);
+        acc[r].y = fmaf(g, v[r].y, acc[r].y);
+        acc[r].z = fmaf(g, v[r].z, acc[r].z);
+        acc[r].w = fmaf(g, v[r].w, acc[r].w);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const AttnJoined j{__shfl_sync(0xffffffffu, m, r), __shfl_sync(0xffffffffu, l, r), acc[r]};
+      if (r < live && in) attn_store<BF>(a, w.q.row0, w.h, w.row0() + first + r, 4 * lane, j);
+    }
+  }
+}
+
 template <int DH, bool BF>
 __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s) {
   const Env E{a, C};
   const int wi = (threadIdx.x >> 5) & 3, tid = threadIdx.x & 127;
-  const int D = a.p.c.kv.head_dim, d4 = D / 4;
+  const int D = a.p.c.kv.head_dim;
   const uint32_t lanes = (uint32_t)(wi * 32) << 16;
   const uint32_t ts = tmem + lanes + (uint32_t)s * 128u, to = tmem + lanes + 256u + (uint32_t)s * (DH * 64);
   uint32_t us = 0, uo = 0;  // uses of s_full and o_full
@@ -491,7 +546,8 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
       else if (a.p.lse) a.p.lse[t * a.p.ld_lse + hd] = attn_lse<BF>(m, l);
     }
     if (!whole) {
-      const int c0 = attn_run_of(C.plan, w.begin()), c1 = attn_run_of(C.plan, w.end() - 1), n = c1 - c0 + 1;
+      int c0;
+      const int n = AttnCut<SNAP>::parts(C.plan, w.begin(), w.end(), &c0);
       named_bar_sync(1 + s, TR);
       if (tid == 0) {
         __threadfence();
@@ -503,16 +559,7 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
       named_bar_sync(1 + s, TR);
       if (C.last[s]) {
         __threadfence();
-        auto at = [&](int x) {
-          return reinterpret_cast<const float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot);
-        };
-        for (int i = tid; i < T.rows * d4; i += TR) {
-          const int r = i / d4, d = (i - r * d4) * 4, q = s * TR + r;
-          const AttnJoined v = attn_join(
-              n, [&](int x) { return __ldcg(reinterpret_cast<const float2*>(at(x) + 2 * q)); },
-              [&](int x) { return __ldcg(reinterpret_cast<const float4*>(at(x) + 2 * R + (size_t)q * D + d)); });
-          attn_store<BF>(a, w.q.row0, w.h, w.row0() + q, d, v);
-        }
+        join_rows<BF>(a, w, s, c0, n, T.rows);
       }
       named_bar_sync(1 + s, TR);  // `last` has been read
     }
@@ -546,7 +593,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
   }
   if (warp == 0) tmem_alloc(&C.tmem, 512);
   grid_wait();
-  attn_plan<R, TK, NTHR>(a.p, a.group, C.plan);
+  attn_plan<R, TK, NTHR, MIN_RUN, SNAP>(a.p, a.group, C.plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -562,10 +609,13 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
       issue_all<DH, BF>(I, ring);
       __syncwarp();
       if (elect_one()) umma_commit(attn_bar(C.done));  // after every product of this thread
-    } else if (warp == W_KV) {
-      run_kv<DH>(a, C, smem_u32(ring));
+    } else if (warp == W_K) {
+      run_copies<DH, Cfg<DH>::NK>(a, C, &a.map_k, smem_u32(ring), C.full, C.empty);
+    } else if (warp == W_V) {
+      constexpr int NK = Cfg<DH>::NK;
+      run_copies<DH, Cfg<DH>::NV>(a, C, &a.map_v, smem_u32(ring) + NK * Cfg<DH>::SLOT, C.full + NK, C.empty + NK);
     } else {
-      run_q<DH>(a, C, smem_u32(sm) + (uint32_t)(warp - W_Q) * Cfg<DH>::SLOT, warp - W_Q);
+      run_q<DH>(a, C, smem_u32(sm));
     }
   }
   __syncwarp();
