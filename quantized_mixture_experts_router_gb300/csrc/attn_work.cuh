@@ -2,8 +2,9 @@
 // (new tokens x the query heads that share a key head, token by token) of one
 // sequence and key head, against the tiles of TK keys that any of its rows sees.
 // The items, numbered sequence by sequence, in it head by head, in it row tile by
-// row tile, make one line of key tiles (an item that sees none counts as one),
-// which is cut into about equal runs, one for each block: whatever the lengths, the
+// row tile, make one line, of which an item takes OVER places (what it costs
+// whatever its length, in key tiles) and one for each of its key tiles.  The line
+// is cut into about equal runs, one for each block: whatever the lengths, the
 // blocks have the same work.  An item that a cut goes through is joined
 // by the last of its blocks to finish, in the order of the runs.
 //
@@ -48,8 +49,13 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, const AttnS
   return g;
 }
 
-template <int R, int TK>
+template <int R_, int TK_, int OVER_, int SNAP_, int MIN_RUN_>
 struct AttnWork {
+  static constexpr int R = R_, TK = TK_;
+  static constexpr int OVER = OVER_;        // places of an item beside its key tiles
+  static constexpr int SNAP = SNAP_;        // an item is cut this far from its ends at the least
+  static constexpr int MIN_RUN = MIN_RUN_;  // more blocks take part only if each has so many places, or an item
+  static_assert(OVER >= 1 && SNAP > OVER, "every part of an item has a key tile");
   static __device__ __forceinline__ int row_tiles(const AttnSeq& q, int group) {
     return q.n > 0 ? (q.n * group - 1) / R + 1 : 0;
   }
@@ -60,9 +66,9 @@ struct AttnWork {
     return g.hi > g.lo ? (g.hi - 1) / TK + 1 - g.lo / TK : 0;
   }
   static __device__ __forceinline__ int cost(const AttnParams& p, const AttnSeq& q, int group, int i) {
-    return max(1, key_tiles(range(p, q, group, i)));
+    return OVER + key_tiles(range(p, q, group, i));
   }
-  // Key tiles of one key head of each lane's sequence (0 where !valid), and its row tiles, by a whole warp.
+  // Places of one key head of each lane's sequence (0 where !valid), and its row tiles, by a whole warp.
   static __device__ long long seq_cost(const AttnParams& p, int group, int b, bool valid, int* rows = nullptr) {
     const int lane = threadIdx.x & 31;
     AttnSeq q{};
@@ -93,19 +99,18 @@ struct AttnWork {
 // The cut, and where this block's run begins and ends.
 struct AttnPlan {
   long long sum[32], items[32];
-  long long total;           // key tiles of the call
+  long long total;           // places of the line
   int runs;                  // blocks that have work
-  long long base[2], per_head[2];  // of the sequences in which the run begins and ends: place, a head's key tiles
+  long long base[2], per_head[2];  // of the sequences in which the run begins and ends: place, a head's places
   int b[2];
   long long begin, end;      // the run
-  int h, i, skip;            // its first item (of sequence b[0]), and the key tiles of it that belong to the run before
+  int h, i, skip;            // its first item (of sequence b[0]), and the places of it that belong to the run before
 };
 
-// Places x where an even cut would fall, moved to an item's end if that is less
-// than SNAP key tiles away: an item is cut only where both parts are worth the join.
+// The place x where an even cut would fall, moved to an item's end if that is less
+// than SNAP places away: an item is cut only where both parts are worth the join.
 template <int SNAP>
 struct AttnCut {
-  static __device__ __forceinline__ long long even(const AttnPlan& S, int run) { return S.total * run / S.runs; }
   static __device__ __forceinline__ long long moved(long long x, long long begin, long long end) {
     return x - begin >= SNAP && end - x >= SNAP ? x : x - begin <= end - x ? begin : end;
   }
@@ -118,12 +123,10 @@ struct AttnCut {
   }
 };
 
-// By all NT threads of the block; ends with a barrier.  As many runs as there are
-// blocks, if each has MIN_RUN key tiles or an item.
-template <int R, int TK, int NT, int MIN_RUN, int SNAP>
+// By all NT threads of the block; ends with a barrier.
+template <class W, int NT>
 __device__ void attn_plan(const AttnParams& p, int group, AttnPlan& S) {
-  using W = AttnWork<R, TK>;
-  using Cut = AttnCut<SNAP>;
+  using Cut = AttnCut<W::SNAP>;
   constexpr int NWARP = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int batch = p.s.batch, kh = p.c.kv.kv_heads;
@@ -151,7 +154,7 @@ __device__ void attn_plan(const AttnParams& p, int group, AttnPlan& S) {
     all += S.items[w];
   }
   __syncthreads();
-  const int runs = (int)min((long long)gridDim.x, max(total / MIN_RUN, all));
+  const int runs = (int)min((long long)gridDim.x, max(total / W::MIN_RUN, all));
   if (tid == 0) {
     S.total = total;
     S.runs = runs;
@@ -232,9 +235,9 @@ __device__ void attn_plan(const AttnParams& p, int group, AttnPlan& S) {
 
 // The items of this block's run, one after the other; every warp that needs them
 // walks for itself.
-template <int R, int TK>
+template <class W>
 struct AttnWalk {
-  using W = AttnWork<R, TK>;
+  static constexpr int R = W::R, TK = W::TK;
   const AttnParams& p;
   const int group;
   long long at, left;      // place of the item's part in the line; what is left of the run from there on
@@ -242,7 +245,7 @@ struct AttnWalk {
   AttnSeq q;
   AttnRange keys;
   int tiles;               // key tiles of the item
-  int skip, take;          // the part: its first key tile and how many (of max(1, tiles))
+  int skip, take;          // the part: its first place in the item and how many
   bool live;
 
   __device__ __forceinline__ AttnWalk(const AttnParams& p_, int group_, const AttnPlan& S) : p(p_), group(group_) {
@@ -262,7 +265,7 @@ struct AttnWalk {
   __device__ __forceinline__ void set() {
     keys = W::range(p, q, group, i);
     tiles = W::key_tiles(keys);
-    take = (int)min((long long)(max(1, tiles) - skip), left);
+    take = (int)min((long long)(cost() - skip), left);
   }
   __device__ __forceinline__ void next() {
     at += take;
@@ -288,13 +291,20 @@ struct AttnWalk {
     }
     set();
   }
-  __device__ __forceinline__ int row0() const { return i * R; }                              // of the sequence
+  __device__ __forceinline__ int cost() const { return W::OVER + tiles; }
+  __device__ __forceinline__ bool whole() const { return take == cost(); }
+  // of the sequence's rows
+  __device__ __forceinline__ int row0() const { return i * R; }
   __device__ __forceinline__ int rows() const { return min(R, q.n * group - i * R); }
-  __device__ __forceinline__ int key0() const { return (keys.lo / TK + skip) * TK; }         // first key of the part
-  __device__ __forceinline__ int key_steps() const { return tiles ? take : 0; }              // key tiles to read
-  __device__ __forceinline__ bool whole() const { return take == max(1, tiles); }
-  __device__ __forceinline__ long long begin() const { return at - skip; }                   // place of the whole item
-  __device__ __forceinline__ long long end() const { return begin() + max(1, tiles); }
+  // key tiles of the part: a cut lies behind the item's first OVER places
+  __device__ __forceinline__ int first_step() const { return skip ? skip - W::OVER : 0; }
+  __device__ __forceinline__ int key_steps() const {
+    return (skip + take == cost() ? tiles : skip + take - W::OVER) - first_step();
+  }
+  __device__ __forceinline__ int key0() const { return (keys.lo / TK + first_step()) * TK; }
+  // places of the whole item
+  __device__ __forceinline__ long long begin() const { return at - skip; }
+  __device__ __forceinline__ long long end() const { return begin() + cost(); }
 };
 
 // Workspace of a call: status, and for each block two counters (of the item that

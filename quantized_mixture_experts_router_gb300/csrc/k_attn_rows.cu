@@ -22,9 +22,13 @@ constexpr int R = ATTN_ROWS_TILE, TK = ATTN_ROWS_KEYS;
 constexpr int NW = 8;                      // warps that compute
 constexpr int NP = 4;                      // warps that copy
 constexpr int NTHR = (NW + NP) * 32;
-// A block's warps work on eight tiles at once, so that a run of fewer is no shorter.
-constexpr int MIN_RUN = NW, SNAP = NW / 2;
+// An item costs about as much as six tiles from memory beside its own, a join twice
+// that; a block's warps work on eight tiles at once, so that a run of fewer is no
+// shorter.
+using Work = AttnWork<R, TK, 6, 12, 14>;
+using Walk = AttnWalk<Work>;
 constexpr uint32_t HALF = TK * 128;        // 64 values of a tile's keys
+constexpr uint32_t QHALF = R * 128;        // 64 values of an item's queries
 
 template <int DH>
 struct Cfg {
@@ -41,9 +45,11 @@ struct Cfg {
 template <int DH>
 struct Shared {
   alignas(1024) uint8_t ring[Cfg<DH>::NS * Cfg<DH>::STAGE];
+  alignas(1024) uint8_t q[2][DH * QHALF];  // queries of this item and the next
   float o[NW][R][Cfg<DH>::OPITCH];
   float ml[NW][R][2];
   unsigned long long full[Cfg<DH>::NS], empty[Cfg<DH>::NS];
+  unsigned long long q_full[2], q_empty[2];
   AttnPlan plan;
   uint32_t abort, last;
 };
@@ -76,9 +82,28 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-using Walk = AttnWalk<R, TK>;
-
 // ------------------------------------------------------------ the copying warps
+// Rows pw, pw + NP, ... of the item's queries, by the copying warp pw, in the
+// swizzled layout; rows and values that there are none of are zeros.  The barrier
+// hears of the copies when they have landed.
+template <int DH>
+__device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, uint32_t q_smem, int pw, unsigned long long& full) {
+  constexpr int CH = DH * 8, RPI = 32 / CH;  // 16-byte pieces of a row; rows an instruction of the warp covers
+  const int lane = threadIdx.x & 31, ch = lane % CH, D = a.p.c.kv.head_dim, rows = w.rows();
+#pragma unroll
+  for (int i = 0; i < R / NP; i += RPI) {
+    const int r = pw + NP * (i + lane / CH), row = w.row0() + r, tok = row / a.group;
+    const bool there = r < rows && ch * 8 < D;
+    const uint16_t* src = static_cast<const uint16_t*>(a.p.q);
+    if (there) src += (w.q.row0 + tok) * a.p.ldq + (long long)(w.h * a.group + row - tok * a.group) * D + ch * 8;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     q_smem + (uint32_t)(ch / 8) * QHALF + (uint32_t)r * 128u + (uint32_t)(((ch & 7) ^ (r & 7)) << 4)),
+                 "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full)) : "memory");
+}
+
 // A warp issues one box after the other, about 100 cycles each, which for small
 // pages is more than a tile may take: each copies a quarter of a tile's boxes, those
 // of its half of the keys' or values' widths, or every other page's.
@@ -91,10 +116,14 @@ __device__ void run_copies(const AttnArgs& a, Shared<DH>& S, int pw) {
   const uint32_t ring = smem_u32(S.ring);
   const uint32_t dst0 = (uint32_t)(val * DH + half) * HALF + (uint32_t)(box * br) * 128u;
   uint32_t st = 0, par = 0, used = 0;  // par: the phase of each stage's empty barrier that is waited for next
+  uint32_t items = 0;                  // with keys, so far
   bool ok = true;
   for (Walk w(a.p, a.group, S.plan); ok && w.live; w.next()) {
     const int steps = w.key_steps();
     if (!steps) continue;
+    if (items >= 2 && !attn_wait(S.q_empty[items & 1], (items / 2 - 1) & 1u, &S.abort, a.timeout_ns, a.status)) break;
+    copy_q<DH>(a, w, smem_u32(S.q[items & 1]), pw, S.q_full[items & 1]);
+    ++items;
     AttnPages pages;
     int key = w.key0();
     pages.begin(a.p.s.table + w.b * a.p.s.ld_table, max(key, w.keys.lo) >> a.page_shift, (w.keys.hi - 1) >> a.page_shift);
@@ -129,26 +158,18 @@ __device__ void run_copies(const AttnArgs& a, Shared<DH>& S, int pw) {
   const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
   for (uint32_t i = 0; i < NS; ++i)
     if ((used >> i) & 1u) mbar_wait_bounded(attn_bar(S.full[i]), (par >> i) & 1u, deadline, a.status);
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ------------------------------------------------------------- the computing warps
-template <int DH, bool BF>
-__device__ __forceinline__ void load_q(const AttnArgs& a, const Walk& w, uint32_t (&qf)[DH * 4][4]) {
-  const int lane = threadIdx.x & 31, t = lane & 3, D = a.p.c.kv.head_dim;
+// The item's queries as operands of the first product.
+template <int DH>
+__device__ __forceinline__ void load_q(uint32_t q_smem, uint32_t (&qf)[DH * 4][4]) {
+  const int lane = threadIdx.x & 31, row = lane & 15, c = lane >> 4;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = (lane >> 2) + 8 * i, row = w.row0() + r;
-    const uint16_t* x = nullptr;
-    if (r < w.rows()) {
-      const int tok = row / a.group, hd = w.h * a.group + row - tok * a.group;
-      x = static_cast<const uint16_t*>(a.p.q) + (w.q.row0 + tok) * a.p.ldq + (long long)hd * D + 2 * t;
-    }
-#pragma unroll
-    for (int ks = 0; ks < DH * 4; ++ks)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        qf[ks][2 * j + i] = x && 16 * ks + 8 * j < D ? *reinterpret_cast<const uint32_t*>(x + 16 * ks + 8 * j) : 0u;
-  }
+  for (int ks = 0; ks < DH * 4; ++ks)
+    ldmatrix4(q_smem + (uint32_t)(ks / 4) * QHALF + (uint32_t)row * 128u + (uint32_t)((((ks & 3) * 2 + c) ^ (row & 7)) << 4),
+              qf[ks]);
 }
 
 // One tile of keys against the rows.  lo, hi: what each of the lane's two rows
@@ -255,14 +276,16 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int D = a.p.c.kv.head_dim, d4 = D / 4;
   const uint32_t ring = smem_u32(S.ring);
-  uint32_t u = 0;  // tiles of the run so far; tile u is warp u % NW's, in stage u % NS
+  uint32_t u = 0;      // tiles of the run so far; tile u is warp u % NW's, in stage u % NS
+  uint32_t items = 0;  // with keys, so far
   for (Walk w(a.p, a.group, S.plan); w.live; w.next()) {
     const int steps = w.key_steps(), rows = w.rows();
     uint32_t j = (uint32_t)(warp + NW - (int)(u % NW)) % NW;  // this warp's first tile of the item
     if (j < (uint32_t)steps) {
       uint32_t qf[DH * 4][4];
       float o[DH * 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {};
-      load_q<DH, BF>(a, w, qf);
+      bool ok = attn_wait(S.q_full[items & 1], (items / 2) & 1u, &S.abort, a.timeout_ns, a.status);
+      load_q<DH>(smem_u32(S.q[items & 1]), qf);
       int lo[2], hi[2], lo_all = 0, hi_all = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -280,7 +303,8 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
       for (; j < (uint32_t)steps; j += NW) {
         const uint32_t st = (u + j) % NS, par = ((u + j) / NS) & 1u;
         const int key = w.key0() + (int)j * TK;
-        if (attn_wait(S.full[st], par, &S.abort, a.timeout_ns, a.status))
+        ok = attn_wait(S.full[st], par, &S.abort, a.timeout_ns, a.status) && ok;
+        if (ok)
           do_tile<DH, BF>(ring + st * Cfg<DH>::STAGE, key, w.keys, key < lo_all || key + TK > hi_all, lo, hi, a.c, qf, o,
                           m, l);
         else
@@ -308,6 +332,11 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
       S.ml[warp][lane][1] = 0.f;
     }
     u += (uint32_t)steps;
+    if (steps) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(attn_bar(S.q_empty[items & 1]));
+      ++items;
+    }
     named_bar_sync(1, NW * 32);
     const bool whole = w.whole();
     float* part = reinterpret_cast<float*>(a.part + (2 * (size_t)blockIdx.x + (w.skip ? 0 : 1)) * a.slot);
@@ -325,7 +354,7 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
     }
     if (!whole) {
       int c0;
-      const int n = AttnCut<SNAP>::parts(S.plan, w.begin(), w.end(), &c0);
+      const int n = AttnCut<Work::SNAP>::parts(S.plan, w.begin(), w.end(), &c0);
       named_bar_sync(1, NW * 32);
       if (tid == 0) {
         __threadfence();
@@ -368,11 +397,15 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_rows(const __grid_constant__ A
       mbar_init(attn_bar(S.full[i]), NP);
       mbar_init(attn_bar(S.empty[i]), 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(attn_bar(S.q_full[i]), NP * 32);
+      mbar_init(attn_bar(S.q_empty[i]), NW);
+    }
     S.abort = 0u;
     fence_mbar_init();
   }
   grid_wait();
-  attn_plan<R, TK, NTHR, MIN_RUN, SNAP>(a.p, a.group, S.plan);
+  attn_plan<Work, NTHR>(a.p, a.group, S.plan);
   if (threadIdx.x < NW * 32) run_rows<DH, BF>(a, S);
   else run_copies<DH>(a, S, (int)(threadIdx.x >> 5) - NW);
 }

@@ -25,8 +25,9 @@ namespace {
 
 constexpr int R = ATTN_TILES_TILE, TK = ATTN_TILES_KEYS, TR = 128;
 constexpr int W_MMA = 8, W_K = 9, W_V = 10, W_Q = 11;
-// A join costs about as much as four key tiles.
-constexpr int MIN_RUN = 4, SNAP = 4;
+// An item costs about as much as three key tiles beside its own, and so does a join.
+using Work = AttnWork<R, TK, 3, 6, 6>;
+using Walk = AttnWalk<Work>;
 constexpr int NTHR = 384;
 // Registers a thread: 168 at launch; the softmax warps take what the others leave.
 constexpr int REG_LAUNCH = 168, REG_SOFT = 216, REG_REST = 72;
@@ -53,8 +54,6 @@ struct TilesCtl {
 template <int DH>
 constexpr uint32_t SMEM_BYTES = 1024 + (2 + Cfg<DH>::NS) * Cfg<DH>::SLOT + ((sizeof(TilesCtl) + 15) & ~15u);
 static_assert(SMEM_BYTES<1> <= 232448 && SMEM_BYTES<2> <= 232448, "shared memory of a block");
-
-using Walk = AttnWalk<R, TK>;
 
 // What one row tile of an item does in this run's part of it.
 struct Tile {
@@ -415,55 +414,97 @@ __device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, in
   tmem_wait_st();
 }
 
-// Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left, a warp 16
-// rows at a time: lane r keeps row r's maximum and sum, and each lane four values
-// of every row, so that 16 loads are in flight.
-template <bool BF>
-__device__ void join_rows(const AttnArgs& a, const Walk& w, int s, int c0, int n, int rows) {
-  const int lane = threadIdx.x & 31, D = a.p.c.kv.head_dim;
-  const bool in = 4 * lane < D;
-  auto part = [&](int x) {
-    return reinterpret_cast<const float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot);
-  };
-#pragma unroll 1
-  for (int r0 = ((threadIdx.x >> 5) & 3) * 16; r0 < rows; r0 += 64) {
-    const int live = min(rows - r0, 16);
-    const int first = s * TR + r0;  // row of the item
-    auto ml = [&](int x) { return __ldcg(reinterpret_cast<const float2*>(part(x)) + first + lane); };
-    float m = -INFINITY, l = 0.f;
-    if (lane < live)
-      for (int x = 0; x < n; ++x) m = fmaxf(m, ml(x).x);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float4 acc[16] = {};
-#pragma unroll 1
-    for (int x = 0; x < n; ++x) {
-      const float4* o = reinterpret_cast<const float4*>(part(x) + 2 * R + (size_t)first * D) + lane;
-      float4 v[16];
+// A partial result: (maximum, sum) of 256 rows, then their values, four of all rows
+// after four of all rows, so that the threads of a warp write and read side by side.
+__device__ __forceinline__ float4* part_values(float* part, int row, int d) {
+  return reinterpret_cast<float4*>(part + 2 * R) + (d / 4) * R + row;
+}
+
+// Eight values of a row, rounded, of each of four 8-value pieces; the four threads
+// of a quad trade theirs, so that each writes a piece of every row of the quad and
+// they write 64 bytes side by side.
+__device__ __forceinline__ void quad_transpose(uint4 (&x)[4]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) v[r] = r < live && in ? __ldcg(o + r * (D / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      float f = 0.f;
-      if (lane < live) {
-        const float2 v = ml(x);
-        if (v.y != 0.f) {  // (0: nothing seen)
-          f = exp2_fast(v.x - ref);
-          l += f * v.y;
-        }
-      }
+  for (int b = 1; b < 4; b <<= 1) {
+    const bool up = lane & b;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float g = __shfl_sync(0xffffffffu, f, r);
-        acc[r].x = fmaf(g, v[r].x, acc[r].x);
-        acc[r].y = fmaf(g, v[r].y, acc[r].y);
-        acc[r].z = fmaf(g, v[r].z, acc[r].z);
-        acc[r].w = fmaf(g, v[r].w, acc[r].w);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const AttnJoined j{__shfl_sync(0xffffffffu, m, r), __shfl_sync(0xffffffffu, l, r), acc[r]};
-      if (r < live && in) attn_store<BF>(a, w.q.row0, w.h, w.row0() + first + r, 4 * lane, j);
+    for (int i = 0; i < 4; ++i) {
+      if (i & b) continue;
+      // keeps piece (i | own bit), gives the other away
+      uint4 give = up ? x[i] : x[i | b];
+      give.x = __shfl_xor_sync(0xffffffffu, give.x, b);
+      give.y = __shfl_xor_sync(0xffffffffu, give.y, b);
+      give.z = __shfl_xor_sync(0xffffffffu, give.z, b);
+      give.w = __shfl_xor_sync(0xffffffffu, give.w, b);
+      if (up) x[i] = give;
+      else x[i | b] = give;
     }
   }
+}
+
+// 32 values of this thread's row from value c0 on, times inv, out of the row tile's
+// rows that there are; by whole warps.  off: where each row's output begins, -1 for none.
+template <bool BF>
+__device__ __forceinline__ void store_32(const AttnArgs& a, long long off, int c0, const float (&f)[32], float inv) {
+  const int lane = threadIdx.x & 31, D = a.p.c.kv.head_dim;
+  uint4 x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // a row that saw nothing, or scores of -inf alone: zeros
+    const float* g = f + 8 * i;
+    x[i].x = inv == 0.f ? 0u : attn_pack2<BF>(g[0] * inv, g[1] * inv);
+    x[i].y = inv == 0.f ? 0u : attn_pack2<BF>(g[2] * inv, g[3] * inv);
+    x[i].z = inv == 0.f ? 0u : attn_pack2<BF>(g[4] * inv, g[5] * inv);
+    x[i].w = inv == 0.f ? 0u : attn_pack2<BF>(g[6] * inv, g[7] * inv);
+  }
+  quad_transpose(x);  // now piece lane & 3 of the quad's rows
+  const int d = c0 + 8 * (lane & 3);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long long o = __shfl_sync(0xffffffffu, off, (lane & ~3) + i);
+    if (o >= 0 && d < D) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.p.out) + o + d) = x[i];
+  }
+}
+
+// Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left; this thread's row.
+template <bool BF>
+__device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int row, bool there, long long off, float* lse) {
+  const int D = a.p.c.kv.head_dim;
+  auto part = [&](int x) { return reinterpret_cast<float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot); };
+  auto ml = [&](int x) { return there ? __ldcg(reinterpret_cast<const float2*>(part(x)) + row) : make_float2(-INFINITY, 0.f); };
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int x = 0; x < n; ++x) m = fmaxf(m, ml(x).x);
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+  for (int x = 0; x < n; ++x) {
+    const float2 v = ml(x);
+    l += v.y == 0.f ? 0.f : exp2_fast(v.x - ref) * v.y;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+  for (int d0 = 0; d0 < D; d0 += 32) {
+    float acc[32] = {};
+#pragma unroll 2
+    for (int x = 0; x < n; ++x) {
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = there && d0 + 4 * i < D ? __ldcg(part_values(part(x), row, d0 + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float2 y = ml(x);
+      const float f = y.y == 0.f ? 0.f : exp2_fast(y.x - ref);  // (0: nothing seen)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[4 * i] = fmaf(f, v[i].x, acc[4 * i]);
+        acc[4 * i + 1] = fmaf(f, v[i].y, acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(f, v[i].z, acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(f, v[i].w, acc[4 * i + 3]);
+      }
+    }
+    store_32<BF>(a, off, d0, acc, inv);
+  }
+  if (there && lse) *lse = attn_lse<BF>(m, l);
 }
 
 template <int DH, bool BF>
@@ -504,50 +545,36 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
     const int pr = s * TR + tid;
     const int tok = row / a.group, hd = w.h * a.group + row - tok * a.group;
     const long long t = w.q.row0 + tok;
+    const bool there = tid < T.rows;
+    const long long off = there ? t * a.p.ldo + (long long)hd * D : -1;
+    float* lse = a.p.lse ? a.p.lse + t * a.p.ld_lse + hd : nullptr;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* out = static_cast<uint16_t*>(a.p.out) + t * a.p.ldo + (long long)hd * D;
 #pragma unroll 1
-    for (int c0 = 0; c0 < DH * 64; c0 += 32) {
-      uint32_t o[32];
+    for (int c0 = 0; c0 < D; c0 += 32) {
+      float f[32];
       if (some && ok) {
-        tmem_ld32(to + (uint32_t)c0, o);
+        tmem_ld32(to + (uint32_t)c0, reinterpret_cast<uint32_t*>(f));
         tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = ok ? 0u : 0x7fc00000u;
+        for (int j = 0; j < 32; ++j) f[j] = ok ? 0.f : NAN;
       }
-      if (tid < T.rows) {
+      if (whole) {
+        store_32<BF>(a, off, c0, f, inv);
+      } else if (there) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          if (c0 + j < D) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[j + e]);
-            if (whole) {
-              // a row that saw nothing, or scores of -inf alone: zeros
-              uint4 x;
-              x.x = l == 0.f ? 0u : attn_pack2<BF>(f[0] * inv, f[1] * inv);
-              x.y = l == 0.f ? 0u : attn_pack2<BF>(f[2] * inv, f[3] * inv);
-              x.z = l == 0.f ? 0u : attn_pack2<BF>(f[4] * inv, f[5] * inv);
-              x.w = l == 0.f ? 0u : attn_pack2<BF>(f[6] * inv, f[7] * inv);
-              *reinterpret_cast<uint4*>(out + c0 + j) = x;
-            } else {
-              float4* q = reinterpret_cast<float4*>(part + 2 * R + (size_t)pr * D + c0 + j);
-              q[0] = make_float4(f[0], f[1], f[2], f[3]);
-              q[1] = make_float4(f[4], f[5], f[6], f[7]);
-            }
-          }
-        }
+        for (int j = 0; j < 32; j += 4)
+          if (c0 + j < D) *part_values(part, pr, c0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
       }
     }
     if (some) warp_arrive(C.o_free[s]);
-    if (tid < T.rows) {
+    if (there) {
       if (!whole) *reinterpret_cast<float2*>(part + 2 * pr) = make_float2(m, l);
-      else if (a.p.lse) a.p.lse[t * a.p.ld_lse + hd] = attn_lse<BF>(m, l);
+      else if (lse) *lse = attn_lse<BF>(m, l);
     }
     if (!whole) {
       int c0;
-      const int n = AttnCut<SNAP>::parts(C.plan, w.begin(), w.end(), &c0);
+      const int n = AttnCut<Work::SNAP>::parts(C.plan, w.begin(), w.end(), &c0);
       named_bar_sync(1 + s, TR);
       if (tid == 0) {
         __threadfence();
@@ -559,7 +586,7 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
       named_bar_sync(1 + s, TR);
       if (C.last[s]) {
         __threadfence();
-        join_rows<BF>(a, w, s, c0, n, T.rows);
+        join_row<BF>(a, c0, n, pr, there, off, lse);
       }
       named_bar_sync(1 + s, TR);  // `last` has been read
     }
@@ -593,7 +620,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
   }
   if (warp == 0) tmem_alloc(&C.tmem, 512);
   grid_wait();
-  attn_plan<R, TK, NTHR, MIN_RUN, SNAP>(a.p, a.group, C.plan);
+  attn_plan<Work, NTHR>(a.p, a.group, C.plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
