@@ -341,14 +341,21 @@ int launch_attn_tiles(const AttnArgs& a, int ctas, bool* taken, cudaStream_t s);
 __device__ __forceinline__ uint64_t* attn_bar(unsigned long long& b) { return reinterpret_cast<uint64_t*>(&b); }
 
 // Bounded wait of a warp; once one ran out, the block's later waits do not wait.
-__device__ __forceinline__ bool attn_wait(unsigned long long& bar, uint32_t parity, volatile uint32_t* abort,
-                                          uint64_t timeout_ns, unsigned* status) {
-  bool ok = mbar_try_wait(attn_bar(bar), parity);
+__device__ __forceinline__ bool attn_wait_long(uint64_t* bar, uint32_t parity, volatile uint32_t* abort,
+                                                   uint64_t timeout_ns, unsigned* status) {
+  bool ok = false;
+#pragma unroll 1
+  for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
   if (!ok && !*abort) {
-    ok = mbar_wait_for(attn_bar(bar), parity, timeout_ns, status);
+    ok = mbar_wait_for(bar, parity, timeout_ns, status);
     if (!ok) *abort = 1u;
   }
   return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool attn_wait(unsigned long long& bar, uint32_t parity, volatile uint32_t* abort,
+                                          uint64_t timeout_ns, unsigned* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(attn_bar(bar), parity))) return true;
+  return attn_wait_long(attn_bar(bar), parity, abort, timeout_ns, status);
 }
 
 template <bool BF>

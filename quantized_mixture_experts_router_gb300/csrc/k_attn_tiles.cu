@@ -4,14 +4,15 @@
 // tiles of 128 keys.
 //   S = Q K^T,   P = exp2(c S - m),   O += P V   (tcgen05, f32 in tensor memory)
 //
-// Roles of a block (one an SM, persistent over its run of key tiles):
+// Roles of a block (one an SM, persistent over its run of the line):
 //   warps 0-3, 4-7   softmax of the first and second row tile, a row a thread: S out
 //                    of tensor memory, maximum, P as 16-bit values over S, sum
-//   warp 8           issues the products; zeroes value slots that nobody sees
-//   warps 9, 10      copy keys and values (TMA boxes of a page's slots) into rings
-//   warp 11          copies the queries
-// While one row tile is in its softmax the tensor cores work on the other:
-//   Q0 K(u) | P1 V(u-1) | Q1 K(u) | P0 V(u) | Q0 K(u+1) ...
+//   warps 8, 9       issue the products of the first and second row tile
+//   warp 10          copies keys (TMA boxes of a page's slots) into a ring
+//   warp 11          copies queries, and values into a ring
+// While one row tile is in its softmax the tensor cores work on the other.  A warp
+// issues P V of a key tile and Q K of the next one behind another, as the second
+// overwrites the P of the first.
 // V lies in shared memory as it lies in the cache, [key][value], and is read as an
 // operand whose values, not keys, are contiguous.  A row's output is rescaled only
 // when its maximum has grown by more than 2^8 over the reference, which its own
@@ -24,13 +25,13 @@ namespace moe {
 namespace {
 
 constexpr int R = ATTN_TILES_TILE, TK = ATTN_TILES_KEYS, TR = 128;
-constexpr int W_MMA = 8, W_K = 9, W_V = 10, W_Q = 11;
+constexpr int W_MMA = 8, W_K = 10, W_V = 11;
 // An item costs about as much as three key tiles beside its own, and so does a join.
 using Work = AttnWork<R, TK, 3, 6, 6>;
 using Walk = AttnWalk<Work>;
 constexpr int NTHR = 384;
 // Registers a thread: 168 at launch; the softmax warps take what the others leave.
-constexpr int REG_LAUNCH = 168, REG_SOFT = 216, REG_REST = 72;
+constexpr int REG_LAUNCH = 168, REG_SOFT = 200, REG_REST = 104;
 static_assert(256 * REG_SOFT + 128 * REG_REST <= NTHR * REG_LAUNCH, "register shares exceed the launch's");
 constexpr uint32_t HALF = TK * 128;  // 64 values of 128 keys or rows
 
@@ -43,12 +44,12 @@ struct Cfg {
 };
 
 struct TilesCtl {
-  unsigned long long full[10], empty[10];
+  unsigned long long full[10], empty[10], landed;
   unsigned long long q_full[2], q_empty[2];     // queries of a row tile
   unsigned long long s_full[2], p_full[2];      // scores to the softmax; weights to the products
   unsigned long long o_full[2], o_free[2];      // an item's output, complete; read
-  unsigned long long done;
-  uint32_t tmem, abort, last[2];
+  unsigned long long done[2];
+  uint32_t tmem, abort, last[2], turn;
   AttnPlan plan;
 };
 template <int DH>
@@ -60,6 +61,13 @@ struct Tile {
   int rows;        // rows of the tile that there are
   AttnRange keys;  // that any of them sees
   int first, end;  // key tiles to go through
+  __device__ __forceinline__ Tile() {}
+  static __device__ __forceinline__ Tile none() {
+    Tile T;
+    T.rows = T.first = T.end = 0;
+    T.keys = AttnRange{0, 0};
+    return T;
+  }
   __device__ __forceinline__ Tile(const AttnArgs& a, const Walk& w, int s) {
     rows = min(max(w.rows() - s * TR, 0), TR);
     first = end = 0;
@@ -95,244 +103,359 @@ __device__ __forceinline__ void warp_arrive(unsigned long long& b) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(attn_bar(b));
 }
 
-// ------------------------------------------------------------ keys, values
-// NS slots from `ring` on, their barriers from `full` and `empty` on.
+// ------------------------------------------------------------ copies
+// Key or value tiles into a ring of NS slots.
 template <int DH, int NS>
-__device__ void run_copies(const AttnArgs& a, TilesCtl& C, const CUtensorMap* map, uint32_t ring, unsigned long long* full,
-                           unsigned long long* empty) {
-  const Env E{a, C};
-  const int lane = threadIdx.x & 31, br = a.box_rows, nb = TK / br;
-  const int box = lane % nb, half = lane / nb;
-  const uint32_t dst0 = (uint32_t)half * HALF + (uint32_t)(box * br) * 128u;
-  uint32_t st = 0, par = 0, used = 0;  // par: the phase of each slot's empty barrier that is waited for next
+struct Ring {
+  const AttnArgs& a;
+  const Env E;
+  const CUtensorMap* map;
+  const uint32_t smem;
+  unsigned long long *full, *empty;
+  const int br, box, half;
+  uint32_t st = NS - 1, par = 0, used = 0;  // par: the phase of each slot's empty barrier that is waited for next
+  AttnPages pages;
+
+  __device__ __forceinline__ Ring(const AttnArgs& a_, TilesCtl& C, const CUtensorMap* map_, uint32_t smem_, int first)
+      : a(a_), E{a_, C}, map(map_), smem(smem_), full(C.full + first), empty(C.empty + first), br(a_.box_rows),
+        box((int)(threadIdx.x & 31) % (TK / a_.box_rows)), half((int)(threadIdx.x & 31) / (TK / a_.box_rows)) {}
+  __device__ __forceinline__ void begin(const Walk& w) {
+    pages.begin(a.p.s.table + w.b * a.p.s.ld_table, max(w.key0(), w.keys.lo) >> a.page_shift,
+                (w.keys.hi - 1) >> a.page_shift);
+  }
+  // The tile at `key` into the next slot; `bar` hears of it.
+  __device__ __forceinline__ bool next_slot() {
+    st = st + 1 == NS ? 0 : st + 1;
+    if ((used >> st) & 1u) {
+      if (!E.wait(empty[st], (par >> st) & 1u)) return false;
+      par ^= 1u << st;
+    }
+    used |= 1u << st;
+    return true;
+  }
+  __device__ __forceinline__ void copy(const Walk& w, int key, unsigned long long& bar) {
+    const int lane = threadIdx.x & 31, k = key + box * br;
+    const bool mine = half < DH && k + br > w.keys.lo && k < w.keys.hi;
+    pages.advance(max(key, w.keys.lo) >> a.page_shift);
+    int id = pages.at(min(max(k, w.keys.lo), w.keys.hi - 1) >> a.page_shift);
+    const unsigned boxes = __ballot_sync(0xffffffffu, mine);
+    if (mine && (id < 0 || id >= a.p.c.kv.n_pages)) {
+      atomicOr(a.status, (unsigned)MOE_STATUS_BAD_PAGE);
+      id = a.p.c.kv.n_pages;  // outside: filled with zeros
+    }
+    if (lane == 0) mbar_arrive_expect_tx(attn_bar(bar), (uint32_t)__popc(boxes) * (uint32_t)br * 128u);
+    __syncwarp();
+    if (mine)
+      tma_load_4d(smem + st * Cfg<DH>::SLOT + (uint32_t)half * HALF + (uint32_t)(box * br) * 128u, map, half * 64,
+                  k & (a.p.c.kv.page_size - 1), w.h, id, attn_bar(bar));
+  }
+  // Copies in flight land before the block can exit: each slot's last one (its full
+  // barrier's phase flips with every use, as `par` does from the second use on).
+  __device__ __forceinline__ void drain() {
+    const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
+    for (uint32_t i = 0; i < NS; ++i)
+      if ((used >> i) & 1u) mbar_wait_bounded(attn_bar(full[i]), (par >> i) & 1u, deadline, a.status);
+  }
+};
+
+template <int DH>
+__device__ void run_k(const AttnArgs& a, TilesCtl& C, uint32_t ring) {
+  Ring<DH, Cfg<DH>::NK> K(a, C, &a.map_k, ring, 0);
   bool ok = true;
   for (Walk w(a.p, a.group, C.plan); ok && w.live; w.next()) {
     const int steps = w.key_steps();
     if (!steps) continue;
-    AttnPages pages;
-    int key = w.key0();
-    pages.begin(a.p.s.table + w.b * a.p.s.ld_table, max(key, w.keys.lo) >> a.page_shift, (w.keys.hi - 1) >> a.page_shift);
-    for (int j = 0; j < steps; ++j, key += TK) {
-      if ((used >> st) & 1u) {
-        if (!E.wait(empty[st], (par >> st) & 1u)) {
-          ok = false;
-          break;
-        }
-        par ^= 1u << st;
-      }
-      used |= 1u << st;
-      const int k = key + box * br;
-      const bool mine = half < DH && k + br > w.keys.lo && k < w.keys.hi;
-      pages.advance(max(key, w.keys.lo) >> a.page_shift);
-      int id = pages.at(min(max(k, w.keys.lo), w.keys.hi - 1) >> a.page_shift);
-      const unsigned boxes = __ballot_sync(0xffffffffu, mine);
-      if (mine && (id < 0 || id >= a.p.c.kv.n_pages)) {
-        atomicOr(a.status, (unsigned)MOE_STATUS_BAD_PAGE);
-        id = a.p.c.kv.n_pages;  // outside: filled with zeros
-      }
-      if (lane == 0) mbar_arrive_expect_tx(attn_bar(full[st]), (uint32_t)__popc(boxes) * (uint32_t)br * 128u);
-      __syncwarp();
-      if (mine)
-        tma_load_4d(ring + st * Cfg<DH>::SLOT + dst0, map, half * 64, k & (a.p.c.kv.page_size - 1), w.h, id,
-                    attn_bar(full[st]));
-      st = st + 1 == NS ? 0 : st + 1;
+    K.begin(w);
+    for (int j = 0; j < steps; ++j) {
+      ok = K.next_slot();
+      if (!ok) break;
+      K.copy(w, w.key0() + j * TK, K.full[K.st]);
     }
   }
-  // copies in flight land before the block can exit: each slot's last one
-  const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
-  for (uint32_t i = 0; i < NS; ++i)
-    if ((used >> i) & 1u) mbar_wait_bounded(attn_bar(full[i]), (par >> i) & 1u, deadline, a.status);
+  K.drain();
 }
 
-// ------------------------------------------------------------ queries
-// The row tiles' queries into the swizzled layout, rows and values that there are
+// A row tile's queries into the swizzled layout, rows and values that there are
 // none of as zeros.
 template <int DH>
-__device__ void run_q(const AttnArgs& a, TilesCtl& C, uint32_t q_smem) {
-  const Env E{a, C};
+__device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, const Tile& T, int s, uint32_t q_smem) {
   const int lane = threadIdx.x & 31, D = a.p.c.kv.head_dim;
   constexpr int CH = DH * 8;         // 16-byte pieces of a row
   constexpr int RPI = 32 / CH;       // rows an instruction of the warp covers
   const int ch = lane % CH, rr = lane / CH;
   const bool in = ch * 8 < D;
   const uint16_t* q = static_cast<const uint16_t*>(a.p.q);
-  uint32_t uses[2] = {};
-  for (Walk w(a.p, a.group, C.plan); w.live; w.next()) {
+#pragma unroll 1
+  for (int r0 = 0; r0 < TR; r0 += 32) {
+    // each lane finds one of 32 rows
+    const int r = r0 + lane, row = w.row0() + s * TR + r, tok = row / a.group;
+    const long long at = (w.q.row0 + tok) * a.p.ldq + (long long)(w.h * a.group + row - tok * a.group) * D;
+    const long long off = r < T.rows ? at : -1;
+#pragma unroll 8
+    for (int i = 0; i < 32; i += RPI) {
+      const long long o = __shfl_sync(0xffffffffu, off, i + rr);
+      const bool there = o >= 0 && in;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       q_smem + (uint32_t)(ch / 8) * HALF + swz(r0 + i + rr, ch & 7)),
+                   "l"(there ? q + o + ch * 8 : q), "r"(there ? 16 : 0)
+                   : "memory");
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  fence_async_smem();
+  __syncwarp();
+}
+
+// Value slots of the tile at key0 that the item's rows do not see, in steps of 16
+// that hold some that they see: zeros, whatever the pages hold there.
+struct Edge {
+  int from[2], to[2];
+  __device__ __forceinline__ Edge(int key0, const AttnRange& keys) {
+    to[0] = keys.lo - key0;
+    from[0] = to[0] & ~15;
+    from[1] = keys.hi - key0;
+    to[1] = (from[1] + 15) & ~15;
+  }
+  __device__ __forceinline__ bool has(int side) const { return from[side] >= 0 && to[side] <= TK && from[side] < to[side]; }
+  template <int DH>
+  __device__ __forceinline__ void clear(uint8_t* slot) const {
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      if (!has(side)) continue;
+      const int n = (to[side] - from[side]) * 8;  // 16-byte pieces of 64 values
+      for (int i = threadIdx.x & 31; i < n * DH; i += 32) {
+        const int half = i / n, c = i - half * n;
+        *reinterpret_cast<uint4*>(slot + half * HALF + from[side] * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+  }
+};
+
+template <int DH>
+__device__ void run_qv(const AttnArgs& a, TilesCtl& C, uint32_t q_smem, uint8_t* ring) {
+  const Env E{a, C};
+  Ring<DH, Cfg<DH>::NV> V(a, C, &a.map_v, smem_u32(ring), Cfg<DH>::NK);
+  const int lane = threadIdx.x & 31;
+  uint32_t uses[2] = {}, edges = 0;
+  bool ok = true, flying = false;  // flying: a copy that `landed` was to hear of
+  for (Walk w(a.p, a.group, C.plan); ok && w.live; w.next()) {
+    const int steps = w.key_steps();
+    if (!steps) continue;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const Tile T(a, w, s);
-      if (T.first >= T.end) continue;
-      if (!E.wait(C.q_empty[s], (uses[s]++ & 1u) ^ 1u)) return;  // passes at once the first time
-#pragma unroll 1
-      for (int r0 = 0; r0 < TR; r0 += 32) {
-        // each lane finds one of 32 rows
-        const int r = r0 + lane, row = w.row0() + s * TR + r, tok = row / a.group;
-        const long long at = (w.q.row0 + tok) * a.p.ldq + (long long)(w.h * a.group + row - tok * a.group) * D;
-        const long long off = r < T.rows ? at : -1;
-#pragma unroll 8
-        for (int i = 0; i < 32; i += RPI) {
-          const long long o = __shfl_sync(0xffffffffu, off, i + rr);
-          const bool there = o >= 0 && in;
-          const uint32_t dst = q_smem + (uint32_t)s * Cfg<DH>::SLOT + (uint32_t)(ch / 8) * HALF + swz(r0 + i + rr, ch & 7);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(there ? q + o + ch * 8 : q),
-                       "r"(there ? 16 : 0)
-                       : "memory");
-        }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_async_smem();
-      __syncwarp();
+      if (T.first >= T.end || !ok) continue;
+      ok = E.wait(C.q_empty[s], (uses[s]++ & 1u) ^ 1u);  // passes at once the first time
+      if (!ok) break;
+      copy_q<DH>(a, w, T, s, q_smem + (uint32_t)s * Cfg<DH>::SLOT);
       if (lane == 0) mbar_arrive(attn_bar(C.q_full[s]));
     }
+    if (!ok) break;
+    V.begin(w);
+    for (int j = 0; j < steps; ++j) {
+      ok = V.next_slot();
+      if (!ok) break;
+      const int key = w.key0() + j * TK;
+      const Edge e(key, w.keys);
+      if (!e.has(0) && !e.has(1)) {
+        V.copy(w, key, V.full[V.st]);
+        continue;
+      }
+      V.copy(w, key, C.landed);
+      ok = E.wait(C.landed, edges++ & 1u);
+      if (!ok) {
+        flying = true;
+        V.used &= ~(1u << V.st);
+        break;
+      }
+      e.clear<DH>(ring + V.st * Cfg<DH>::SLOT);
+      if (lane == 0) mbar_arrive(attn_bar(V.full[V.st]));
+    }
   }
+  V.drain();
+  if (flying) mbar_wait_bounded(attn_bar(C.landed), (edges - 1) & 1u, globaltimer_ns() + a.timeout_ns, a.status);
 }
 
 // ------------------------------------------------------------ products
-// Descriptor of V as the second operand of P V: 64 values of a key are one
-// swizzled row of 128 bytes, keys follow one another; the values, not the keys,
-// are contiguous.  8 keys are 1024 bytes, the next 64 values HALF on.
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)(HALF >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Instructions of the issuing warp count: with 100 cycles a product, which generic
+// code takes, they bound the kernel at half its rate.  So descriptors are built from
+// warp-uniform words, whose offsets are constants of unrolled code.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Lower and upper word of a matrix descriptor (128-byte swizzle).  Rows of 128 bytes,
+// eight of them 1024 bytes.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+// K and Q: 64 values of a key or row are one swizzled row, and what is summed over.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+// V as the second operand of P V: 64 values of a key are one swizzled row, keys follow
+// one another; the values, not the keys (which are summed over), are contiguous.  The
+// next 64 values are HALF on.
+__device__ __forceinline__ uint32_t desc_v_lo(uint32_t saddr) { return (saddr >> 4) | ((HALF >> 4) << 16); }
+
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)DESC_HI << 32) | lo; }
+
+// scores = Q K^T over KS steps of 16 values
+template <int KS>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q, uint32_t k, uint32_t id) {
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    const uint32_t off = (uint32_t)(i / 4) * (HALF >> 4) + (uint32_t)(i & 3) * 2u;
+    umma_f16(d, desc(q + off), desc(k + off), id, i > 0);
+  }
 }
 
-// The weights of one row tile against one value tile.
-struct Product {
-  uint32_t slot;   // of the ring
-  int from, to;    // steps of 16 keys that any row sees
-  bool first, last;
-};
-
-template <int DH, bool BF>
-struct Issuer {
+// The key tiles of all items of the run, and what one row tile does with each.
+struct Steps {
   const AttnArgs& a;
-  TilesCtl& C;
-  const uint32_t tmem, ring, q_smem;
-  const Env E;
-  uint32_t par_full = 0;                 // phase of each slot
-  uint32_t uq[2] = {}, up[2] = {}, uo[2] = {};  // uses of the barriers
-  const uint32_t id_qk, id_pv;
-  const int ksteps;
-
-  __device__ __forceinline__ Issuer(const AttnArgs& a_, TilesCtl& C_, uint32_t tmem_, uint32_t ring_, uint32_t q_)
-      : a(a_), C(C_), tmem(tmem_), ring(ring_), q_smem(q_), E{a_, C_}, id_qk(umma_idesc(TK, BF)),
-        id_pv(umma_idesc((a_.p.c.kv.head_dim + 15) & ~15, BF) | (1u << 16)), ksteps((a_.p.c.kv.head_dim + 15) / 16) {}
-
-  __device__ __forceinline__ bool slot_full(uint32_t st) {
-    if (!E.wait(C.full[st], (par_full >> st) & 1u)) return false;
-    par_full ^= 1u << st;
-    return true;
+  const int s;
+  Walk w;
+  Tile T;
+  int k, end;
+  bool live;
+  __device__ __forceinline__ Steps(const AttnArgs& a_, const AttnPlan& plan, int s_)
+      : a(a_), s(s_), w(a_.p, a_.group, plan), T(Tile::none()) {
+    item();
   }
-  __device__ __forceinline__ bool scores(int s, uint32_t kslot, bool first, bool last) {
-    if (first && !E.wait(C.q_full[s], uq[s]++ & 1u)) return false;
-    tc_fence_after();
-    if (elect_one()) {
-      const uint64_t q = umma_desc(q_smem + (uint32_t)s * Cfg<DH>::SLOT), k = umma_desc(ring + kslot * Cfg<DH>::SLOT);
-#pragma unroll
-      for (int i = 0; i < DH * 4; ++i)
-        if (i < ksteps) {
-          const uint64_t off = (uint64_t)((i / 4) * (HALF >> 4) + (i & 3) * 2);
-          umma_f16(tmem + (uint32_t)s * 128u, q + off, k + off, id_qk, i > 0);
-        }
-      umma_commit(attn_bar(C.s_full[s]));
-      if (last) umma_commit(attn_bar(C.q_empty[s]));
-    }
-    __syncwarp();
-    return true;
+  __device__ __forceinline__ void item() {
+    while (w.live && !w.key_steps()) w.next();
+    live = w.live;
+    if (!live) return;
+    T = Tile(a, w, s);
+    k = w.key0() / TK;
+    end = k + w.key_steps();
   }
-  // free: the value slot has no other use
-  __device__ __forceinline__ bool values(int s, const Product& P, bool free) {
-    if (P.first && !E.wait(C.o_free[s], (uo[s]++ & 1u) ^ 1u)) return false;  // passes at once the first time
-    if (!E.wait(C.p_full[s], up[s]++ & 1u)) return false;
-    tc_fence_after();
-    if (elect_one()) {
-      const uint64_t v = v_desc(ring + P.slot * Cfg<DH>::SLOT);
-      const uint32_t o = tmem + 256u + (uint32_t)s * (DH * 64), p = tmem + (uint32_t)s * 128u;
-#pragma unroll
-      for (int i = 0; i < TK / 16; ++i)
-        if (i >= P.from && i < P.to)
-          umma_f16_ta(o, p + (uint32_t)i * 8u, v + (uint64_t)(i * (2048 >> 4)), id_pv, !(P.first && i == P.from));
-      if (free) umma_commit(attn_bar(C.empty[P.slot]));
-      if (P.last) umma_commit(attn_bar(C.o_full[s]));
-    }
-    __syncwarp();
-    return true;
-  }
-  // Value slots of the tile at key0 that the item's rows do not see, in steps of 16
-  // that hold some that they see, hold zeros from here on.
-  __device__ __forceinline__ void clean(uint8_t* slot, int key0, const AttnRange& keys) {
-    const int lane = threadIdx.x & 31;
-    bool any = false;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      int from, to;
-      if (side) {
-        from = keys.hi - key0;
-        to = (from + 15) & ~15;
-      } else {
-        to = keys.lo - key0;
-        from = to & ~15;
-      }
-      if (from < 0 || to > TK || from >= to) continue;
-      any = true;
-      for (int i = lane; i < (to - from) * 8 * DH; i += 32) {
-        const int half = i / ((to - from) * 8), c = i - half * ((to - from) * 8);
-        *reinterpret_cast<uint4*>(slot + half * HALF + from * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    if (any) {
-      fence_async_smem();
-      __syncwarp();
-    }
+  __device__ __forceinline__ void next() {
+    if (++k < end) return;
+    w.next();
+    item();
   }
 };
 
-template <int DH, bool BF>
-__device__ __forceinline__ bool issue_all(Issuer<DH, BF>& I, uint8_t* ring_ptr) {
-  constexpr int NK = Cfg<DH>::NK, NV = Cfg<DH>::NV;
-  const AttnArgs& a = I.a;
-  TilesCtl& C = I.C;
-  uint32_t ks = NK - 1, vs = NK + NV - 1;  // slots
-  bool pending = false;  // the second row tile's product of the tile before
-  Product P1{};
-  for (Walk w(a.p, a.group, C.plan); w.live; w.next()) {
-    const int steps = w.key_steps();
-    if (!steps) continue;
-    const Tile T0(a, w, 0), T1(a, w, 1);
-    const int from = w.key0() / TK;
-    for (int k = from; k < from + steps; ++k) {
-      const int key0 = k * TK;
-      const bool h0 = T0.has(k), h1 = T1.has(k);
-      ks = ks + 1 == NK ? 0 : ks + 1;
-      vs = vs + 1 == NK + NV ? NK : vs + 1;
-      auto product = [&](const Tile& T) {
-        return Product{vs, max(T.keys.lo - key0, 0) / 16, (min(T.keys.hi - key0, TK) + 15) / 16, k == T.first,
-                       k == T.end - 1};
-      };
-      if (!I.slot_full(ks)) return false;
-      if (h0 && !I.scores(0, ks, k == T0.first, k == T0.end - 1)) return false;
-      if (pending && !I.values(1, P1, true)) return false;
-      pending = false;
-      if (h1 && !I.scores(1, ks, k == T1.first, k == T1.end - 1)) return false;
-      if (elect_one()) umma_commit(attn_bar(C.empty[ks]));
-      __syncwarp();
-      if (!I.slot_full(vs)) return false;
-      I.clean(ring_ptr + vs * Cfg<DH>::SLOT, key0, w.keys);
-      if (h0 && !I.values(0, product(T0), !h1)) return false;
-      if (h1) {
-        P1 = product(T1);
-        pending = true;
-      } else if (!h0) {
-        if (elect_one()) umma_commit(attn_bar(C.empty[vs]));
-        __syncwarp();
-      }
-    }
+// A row tile's weights against a value tile, in steps of 16 keys that any row sees.
+struct Product {
+  int from, to;
+  bool active, first, last;
+  __device__ __forceinline__ explicit Product(const Steps& t) {
+    const int key0 = t.k * TK;
+    active = t.T.has(t.k);
+    first = t.k == t.T.first;
+    last = t.k == t.T.end - 1;
+    from = max(t.T.keys.lo - key0, 0) / 16;
+    to = (min(t.T.keys.hi - key0, TK) + 15) / 16;
   }
-  return !pending || I.values(1, P1, true);
+};
+
+// The tensor cores take the products of both issuing warps in turn.  Held while one
+// row tile's are issued, so that they do not mix with the other's: mixed, both tiles'
+// scores come at the end of all of them and both softmaxes run while the tensor
+// cores have nothing (4200 cycles a key tile).  Only the order depends on it, so
+// that a warp goes ahead without it rather than wait for long.
+__device__ __forceinline__ void turn_begin(uint32_t* turn) {
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (atomicCAS(turn, 0u, 1u) == 0u) return;
+}
+__device__ __forceinline__ void turn_end(uint32_t* turn) { atomicExch(turn, 0u); }
+
+// Every slot is waited for and given back, also where this row tile has no use for
+// it: a wait that left one out could take the phase before for done.
+template <int DH, bool BF, int S>
+__device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, uint32_t tmem_, uint32_t ring_, uint32_t q_) {
+  constexpr int NK = Cfg<DH>::NK, NV = Cfg<DH>::NV;
+  const Env E{a, C};
+  const uint32_t tmem = uniform(tmem_), ring = uniform(ring_), q = uniform(desc_lo(q_ + S * Cfg<DH>::SLOT));
+  const uint32_t id_qk = umma_idesc(TK, BF), id_pv = umma_idesc((a.p.c.kv.head_dim + 15) & ~15, BF) | (1u << 16);
+  const uint32_t sp = tmem + S * 128u, o = tmem + 256u + S * (DH * 64);
+  const int ksteps = (a.p.c.kv.head_dim + 15) / 16 + (DH == 2 ? 0 : 4);
+  uint32_t ks = 0, vs = 0, par = 0;             // slots; the phase of each
+  uint32_t uq = 0, up = 0, uo = 0;              // uses of the barriers
+  auto full = [&](uint32_t slot) {
+    if (!E.wait(C.full[slot], (par >> slot) & 1u)) return false;
+    par ^= 1u << slot;
+    return true;
+  };
+  auto scores = [&](uint32_t k, const Product& P) {  // by the elected thread
+    switch (ksteps) {
+      case 8: issue_scores<DH * 4>(sp, q, k, id_qk); break;
+      case 7: issue_scores<DH * 4 - 1>(sp, q, k, id_qk); break;
+      case 6: issue_scores<DH * 4 - 2>(sp, q, k, id_qk); break;
+      default: issue_scores<DH * 4 - 3>(sp, q, k, id_qk);
+    }
+    umma_commit(attn_bar(C.s_full[S]));
+    if (P.last) umma_commit(attn_bar(C.q_empty[S]));
+  };
+  Steps t(a, C.plan, S);
+  if (!t.live) return;
+  Product P(t);
+  if (!full(0)) return;
+  if (P.active) {
+    if (!E.wait(C.q_full[S], uq++ & 1u)) return;
+    tc_fence_after();
+    const uint32_t k = uniform(desc_lo(ring));
+    if (elect_one()) {
+      scores(k, P);
+      umma_commit(attn_bar(C.empty[0]));
+    }
+  } else if (elect_one()) {
+    mbar_arrive(attn_bar(C.empty[0]));
+  }
+  __syncwarp();
+  while (true) {
+    t.next();
+    const Product N(t);
+    const bool more = t.live;
+    ks = ks + 1 == NK ? 0 : ks + 1;
+    if (more && !full(ks)) return;
+    if (!full(NK + vs)) return;
+    const uint32_t k = uniform(desc_lo(ring + ks * Cfg<DH>::SLOT)), v = uniform(desc_v_lo(ring + (NK + vs) * Cfg<DH>::SLOT));
+    const bool straight = more && N.active && !N.first;  // the next scores of the same queries
+    if (P.active) {
+      if (P.first && !E.wait(C.o_free[S], (uo++ & 1u) ^ 1u)) return;  // passes at once the first time
+      if (!E.wait(C.p_full[S], up++ & 1u)) return;
+      tc_fence_after();
+      if (elect_one()) {
+        turn_begin(&C.turn);
+        if (P.from == 0 && P.to == TK / 16) {
+          umma_f16_ta(o, sp, desc(v), id_pv, P.first ? 0u : 1u);
+#pragma unroll
+          for (int i = 1; i < TK / 16; ++i)
+            umma_f16_ta(o, sp + (uint32_t)i * 8u, desc(v + (uint32_t)i * (2048u >> 4)), id_pv, 1u);
+        } else {
+#pragma unroll 1
+          for (int i = P.from; i < P.to; ++i)
+            umma_f16_ta(o, sp + (uint32_t)i * 8u, desc(v + (uint32_t)i * (2048u >> 4)), id_pv, !(P.first && i == P.from));
+        }
+        if (P.last) umma_commit(attn_bar(C.o_full[S]));
+        if (straight) {
+          scores(k, N);
+          umma_commit(attn_bar(C.empty[ks]));
+        }
+        umma_commit(attn_bar(C.empty[NK + vs]));
+        turn_end(&C.turn);
+      }
+    } else if (elect_one()) {
+      mbar_arrive(attn_bar(C.empty[NK + vs]));
+    }
+    __syncwarp();
+    if (!more) return;
+    if (!straight) {
+      if (N.active) {
+        if (!E.wait(C.q_full[S], uq++ & 1u)) return;
+        tc_fence_after();
+        if (elect_one()) {
+          scores(k, N);
+          umma_commit(attn_bar(C.empty[ks]));
+        }
+      } else if (elect_one()) {
+        mbar_arrive(attn_bar(C.empty[ks]));
+      }
+      __syncwarp();
+    }
+    vs = vs + 1 == NV ? 0 : vs + 1;
+    P = N;
+  }
 }
 
 // ------------------------------------------------------------ softmax
@@ -353,6 +476,26 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
       "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
       : "memory");
+}
+
+// Two f32 at once.
+__device__ __forceinline__ uint64_t pack_f32(float x, float y) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ void unpack_f32(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // One key tile of this thread's row.
@@ -396,21 +539,25 @@ __device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, in
     }
   }
   const float ref = (m == -INFINITY ? 0.f : m) - ATTN_BIAS<BF>;
-  float sum[4] = {};
+  const uint64_t c2 = pack_f32(c, c), ref2 = pack_f32(-ref, -ref);
+  uint64_t sum[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t p[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const float x = exp2_fast(fmaf(__uint_as_float(v[32 * i + 2 * j]), c, -ref));
-      const float y = exp2_fast(fmaf(__uint_as_float(v[32 * i + 2 * j + 1]), c, -ref));
-      sum[j & 1] += x;
-      sum[2 + (j & 1)] += y;
+      float x, y;
+      unpack_f32(fma2(pack_f32(__uint_as_float(v[32 * i + 2 * j]), __uint_as_float(v[32 * i + 2 * j + 1])), c2, ref2), x, y);
+      x = exp2_fast(x);
+      y = exp2_fast(y);
+      sum[j & 1] = add2(sum[j & 1], pack_f32(x, y));
       p[j] = attn_pack2<BF>(x, y);
     }
     tmem_st16(ts + 16u * i, p);
   }
-  l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  float x, y;
+  unpack_f32(add2(sum[0], sum[1]), x, y);
+  l += x + y;
   tmem_wait_st();
 }
 
@@ -604,7 +751,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
   if (threadIdx.x == 0) {
     for (int i = 0; i < Cfg<DH>::NS; ++i) {
       mbar_init(attn_bar(C.full[i]), 1);
-      mbar_init(attn_bar(C.empty[i]), 1);
+      mbar_init(attn_bar(C.empty[i]), 2);  // both row tiles
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(attn_bar(C.q_full[i]), 1);
@@ -613,9 +760,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
       mbar_init(attn_bar(C.p_full[i]), 4);
       mbar_init(attn_bar(C.o_full[i]), 1);
       mbar_init(attn_bar(C.o_free[i]), 4);
+      mbar_init(attn_bar(C.done[i]), 1);
     }
-    mbar_init(attn_bar(C.done), 1);
-    C.abort = 0u;
+    mbar_init(attn_bar(C.landed), 1);
+    C.abort = C.turn = 0u;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&C.tmem, 512);
@@ -631,23 +779,21 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
     run_softmax<DH, BF>(a, C, tmem, warp >> 2);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_REST));
-    if (warp == W_MMA) {
-      Issuer<DH, BF> I(a, C, tmem, smem_u32(ring), smem_u32(sm));
-      issue_all<DH, BF>(I, ring);
-      __syncwarp();
-      if (elect_one()) umma_commit(attn_bar(C.done));  // after every product of this thread
-    } else if (warp == W_K) {
-      run_copies<DH, Cfg<DH>::NK>(a, C, &a.map_k, smem_u32(ring), C.full, C.empty);
+    if (warp == W_K) {
+      run_k<DH>(a, C, smem_u32(ring));
     } else if (warp == W_V) {
-      constexpr int NK = Cfg<DH>::NK;
-      run_copies<DH, Cfg<DH>::NV>(a, C, &a.map_v, smem_u32(ring) + NK * Cfg<DH>::SLOT, C.full + NK, C.empty + NK);
+      run_qv<DH>(a, C, smem_u32(sm), ring + Cfg<DH>::NK * Cfg<DH>::SLOT);
     } else {
-      run_q<DH>(a, C, smem_u32(sm));
+      if (warp == W_MMA) run_products<DH, BF, 0>(a, C, tmem, smem_u32(ring), smem_u32(sm));
+      else run_products<DH, BF, 1>(a, C, tmem, smem_u32(ring), smem_u32(sm));
+      __syncwarp();
+      if (elect_one()) umma_commit(attn_bar(C.done[warp - W_MMA]));  // after every product of this thread
     }
   }
   __syncwarp();
   // no product may still be writing tensor memory when it is freed
-  if (threadIdx.x == 0) mbar_wait_bounded(attn_bar(C.done), 0u, globaltimer_ns() + a.timeout_ns, a.status);
+  if (threadIdx.x < 2)
+    mbar_wait_bounded(attn_bar(C.done[threadIdx.x]), 0u, globaltimer_ns() + a.timeout_ns, a.status);
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
