@@ -5,18 +5,20 @@
 //   S = Q K^T,   P = exp2(c S - m),   O += P V   (tcgen05, f32 in tensor memory)
 //
 // Roles of a block (one an SM, persistent over its run of the line):
-//   warps 0-3, 4-7   softmax of the first and second row tile, a row a thread: S out
-//                    of tensor memory, maximum, P as 16-bit values over S, sum
-//   warps 8, 9       issue the products of the first and second row tile
-//   warp 10          copies keys (TMA boxes of a page's slots) into a ring
-//   warp 11          copies queries, and values into a ring
+//   warps 0-7, 8-15  softmax of the first and second row tile, a row a pair of threads,
+//                    64 keys each (one warp alone gets an exponential out every eight
+//                    cycles, two every four): S out of tensor memory, maximum, P as
+//                    16-bit values over S, sum
+//   warps 16, 17     issue the products of the first and second row tile
+//   warp 18          copies keys (TMA boxes of a page's slots) into a ring
+//   warp 19          copies queries, and values into a ring
 // While one row tile is in its softmax the tensor cores work on the other.  A warp
 // issues P V of a key tile and Q K of the next one behind another, as the second
 // overwrites the P of the first.
 // V lies in shared memory as it lies in the cache, [key][value], and is read as an
 // operand whose values, not keys, are contiguous.  A row's output is rescaled only
 // when its maximum has grown by more than 2^8 over the reference, which its own
-// thread then does in place.
+// threads then do in place.
 #include "attn_work.cuh"
 #include "tc.cuh"
 
@@ -25,14 +27,15 @@ namespace moe {
 namespace {
 
 constexpr int R = ATTN_TILES_TILE, TK = ATTN_TILES_KEYS, TR = 128;
-constexpr int W_MMA = 8, W_K = 10, W_V = 11;
+constexpr int W_MMA = 16, W_K = 18, W_V = 19;
 // An item costs about as much as three key tiles beside its own, and so does a join.
 using Work = AttnWork<R, TK, 3, 6, 6>;
 using Walk = AttnWalk<Work>;
-constexpr int NTHR = 384;
-// Registers a thread: 168 at launch; the softmax warps take what the others leave.
-constexpr int REG_LAUNCH = 168, REG_SOFT = 200, REG_REST = 104;
-static_assert(256 * REG_SOFT + 128 * REG_REST <= NTHR * REG_LAUNCH, "register shares exceed the launch's");
+constexpr int NSOFT = 512, NTHR = 640;
+// Registers a thread: 96 at launch; the softmax warps take what the others leave.
+constexpr int REG_LAUNCH = 96, REG_SOFT = 104, REG_REST = 64;
+static_assert(NSOFT * REG_SOFT + (NTHR - NSOFT) * REG_REST <= NTHR * REG_LAUNCH, "register shares exceed the launch's");
+constexpr int KH = TK / 2;           // keys of a softmax thread
 constexpr uint32_t HALF = TK * 128;  // 64 values of 128 keys or rows
 
 template <int DH>
@@ -50,10 +53,11 @@ struct TilesCtl {
   unsigned long long o_full[2], o_free[2];      // an item's output, complete; read
   unsigned long long done[2];
   uint32_t tmem, abort, last[2], turn;
+  float swap[2][2][TR];                         // what a row's two threads tell each other: [row tile][half][row]
   AttnPlan plan;
 };
 template <int DH>
-constexpr uint32_t SMEM_BYTES = 1024 + (2 + Cfg<DH>::NS) * Cfg<DH>::SLOT + ((sizeof(TilesCtl) + 15) & ~15u);
+constexpr uint32_t SMEM_BYTES = (2 + Cfg<DH>::NS) * Cfg<DH>::SLOT + ((sizeof(TilesCtl) + 15) & ~15u);
 static_assert(SMEM_BYTES<1> <= 232448 && SMEM_BYTES<2> <= 232448, "shared memory of a block");
 
 // What one row tile of an item does in this run's part of it.
@@ -347,6 +351,10 @@ struct Product {
   }
 };
 
+// Column of the weights of the 16 keys 16 i .. over the scores: those of either half of
+// the keys lie where that half's scores were.
+__device__ __forceinline__ uint32_t p_col(int i) { return (uint32_t)(i * 8 + (i >= 4 ? 32 : 0)); }
+
 // The tensor cores take the products of both issuing warps in turn.  Held while one
 // row tile's are issued, so that they do not mix with the other's: mixed, both tiles'
 // scores come at the end of all of them and both softmaxes run while the tensor
@@ -421,11 +429,11 @@ __device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, uin
           umma_f16_ta(o, sp, desc(v), id_pv, P.first ? 0u : 1u);
 #pragma unroll
           for (int i = 1; i < TK / 16; ++i)
-            umma_f16_ta(o, sp + (uint32_t)i * 8u, desc(v + (uint32_t)i * (2048u >> 4)), id_pv, 1u);
+            umma_f16_ta(o, sp + p_col(i), desc(v + (uint32_t)i * (2048u >> 4)), id_pv, 1u);
         } else {
 #pragma unroll 1
           for (int i = P.from; i < P.to; ++i)
-            umma_f16_ta(o, sp + (uint32_t)i * 8u, desc(v + (uint32_t)i * (2048u >> 4)), id_pv, !(P.first && i == P.from));
+            umma_f16_ta(o, sp + p_col(i), desc(v + (uint32_t)i * (2048u >> 4)), id_pv, !(P.first && i == P.from));
         }
         if (P.last) umma_commit(attn_bar(C.o_full[S]));
         if (straight) {
@@ -469,7 +477,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads so far are complete; r, which one of them fills, is read behind this.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -498,24 +516,35 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// One key tile of this thread's row.
+// What the row's other thread has, for what this one has.  The next may be told only
+// when both have read this.
+__device__ __forceinline__ float swap_with_other(TilesCtl& C, int s, int half, int row, float mine) {
+  C.swap[s][half][row] = mine;
+  named_bar_sync(1 + s * 4 + (row >> 5), 64);
+  return C.swap[s][half ^ 1][row];
+}
+
+// One key tile of this thread's row, its half of the keys: key0 is the half's first.
 template <int DH, bool BF>
-__device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, int lo, int hi, float c, bool first, float& m,
-                                          float& l) {
-  uint32_t v[TK];
+__device__ __forceinline__ void soft_tile(TilesCtl& C, int s, int half, int row, uint32_t ts, uint32_t to, int key0, int lo,
+                                          int hi, float c, bool first, float& m, float& l) {
+  uint32_t v[KH];
+  tmem_ld32(ts, v);
+  tmem_ld32(ts + 32u, v + 32);
+  tmem_wait_ld32(v);
+  tmem_wait_ld32(v + 32);
+  const int from = lo - key0, end = hi - key0;  // of the keys, what the row sees
+  if (__any_sync(0xffffffffu, from > 0 || end < KH)) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32u * i, v + 32 * i);
-  tmem_wait_ld();
-  const int from = lo - key0, end = hi - key0;  // of the tile's keys, what the row sees
-  if (__any_sync(0xffffffffu, from > 0 || end < TK)) {
-#pragma unroll
-    for (int j = 0; j < TK; ++j)
+    for (int j = 0; j < KH; ++j)
       if (j < from || j >= end) v[j] = 0xff800000u;  // -inf
   }
   float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int j = 0; j < TK; ++j) t[j & 3] = fmaxf(t[j & 3], __uint_as_float(v[j]));
-  const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
+  for (int j = 0; j < KH; j += 2) t[(j / 2) & 3] = fmaxf(fmaxf(t[(j / 2) & 3], __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
+  float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
+  // (the next tile's scores come after both have told that they are done with these)
+  top = fmaxf(top, swap_with_other(C, s, half, row, top));
   const bool rise = top > m + ATTN_SLACK;  // from -inf: by anything
   if (first) {
     m = top;
@@ -525,14 +554,9 @@ __device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, in
     m = next;
     l *= f;
 #pragma unroll 1
-    for (int i = 0; i < DH * 4; ++i) {
+    for (int i = 0; i < DH * 2; ++i) {  // this thread's half of the output
       uint32_t o[16];
-      asm volatile(
-          "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-          : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
-            "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-          : "r"(to + 16u * i));
-      tmem_wait_ld();
+      tmem_ld16(to + 16u * i, reinterpret_cast<float*>(o));
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
       tmem_st16(to + 16u * i, o);
@@ -542,7 +566,7 @@ __device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, in
   const uint64_t c2 = pack_f32(c, c), ref2 = pack_f32(-ref, -ref);
   uint64_t sum[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < KH / 32; ++i) {
     uint32_t p[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -614,10 +638,11 @@ __device__ __forceinline__ void store_32(const AttnArgs& a, long long off, int c
   }
 }
 
-// Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left; this thread's row.
+// Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left; values from .. to - 1
+// of this thread's row.
 template <bool BF>
-__device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int row, bool there, long long off, float* lse) {
-  const int D = a.p.c.kv.head_dim;
+__device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int row, bool there, int from, int to,
+                                         long long off, float* lse) {
   auto part = [&](int x) { return reinterpret_cast<float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot); };
   auto ml = [&](int x) { return there ? __ldcg(reinterpret_cast<const float2*>(part(x)) + row) : make_float2(-INFINITY, 0.f); };
   float m = -INFINITY, l = 0.f;
@@ -631,14 +656,14 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int r
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-  for (int d0 = 0; d0 < D; d0 += 32) {
+  for (int d0 = from; d0 < to; d0 += 32) {
     float acc[32] = {};
-#pragma unroll 2
+#pragma unroll 1
     for (int x = 0; x < n; ++x) {
       float4 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v[i] = there && d0 + 4 * i < D ? __ldcg(part_values(part(x), row, d0 + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[i] = there && d0 + 4 * i < to ? __ldcg(part_values(part(x), row, d0 + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
       const float2 y = ml(x);
       const float f = y.y == 0.f ? 0.f : exp2_fast(y.x - ref);  // (0: nothing seen)
 #pragma unroll
@@ -655,87 +680,95 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int r
 }
 
 template <int DH, bool BF>
-__device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s) {
+__device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s, int half) {
   const Env E{a, C};
-  const int wi = (threadIdx.x >> 5) & 3, tid = threadIdx.x & 127;
-  const int D = a.p.c.kv.head_dim;
-  const uint32_t lanes = (uint32_t)(wi * 32) << 16;
-  const uint32_t ts = tmem + lanes + (uint32_t)s * 128u, to = tmem + lanes + 256u + (uint32_t)s * (DH * 64);
+  const int r = threadIdx.x & 127, D = a.p.c.kv.head_dim;  // row of the row tile
+  const uint32_t lanes = (uint32_t)(r & ~31) << 16;
+  const uint32_t ts = tmem + lanes + (uint32_t)s * 128u + (uint32_t)half * KH;
+  const int d0 = half * DH * 32, d1 = min(D, d0 + DH * 32);  // this thread's values of the output
+  const uint32_t to = tmem + lanes + 256u + (uint32_t)(s * DH * 64 + d0);
   uint32_t us = 0, uo = 0;  // uses of s_full and o_full
   bool ok = true;
   for (Walk w(a.p, a.group, C.plan); w.live; w.next()) {
     const Tile T(a, w, s);
     if (T.rows == 0) continue;
-    const int row = w.row0() + s * TR + tid;  // of the sequence
+    const bool there = r < T.rows;
+    const int row = w.row0() + s * TR + r;  // of the sequence
     int lo = 0, hi = INT_MAX;
-    if (tid < T.rows) {
+    if (there) {
       const AttnRange g = attn_range(a.p, w.q, a.group, row, row + 1);
       lo = g.lo;
       hi = g.hi;
     }
     float m = -INFINITY, l = 0.f;
     for (int k = T.first; k < T.end; ++k) {
-      ok = ok && E.wait(C.s_full[s], us++ & 1u);
-      if (!ok) break;
+      // both warps of a row give up together: they meet at a barrier
+      ok = E.wait(C.s_full[s], us++ & 1u) && ok;
       tc_fence_after();
-      soft_tile<DH, BF>(ts, to, k * TK, lo, hi, a.c, k == T.first, m, l);
+      soft_tile<DH, BF>(C, s, half, r, ts, to, k * TK + half * KH, lo, hi, a.c, k == T.first, m, l);
       warp_arrive(C.p_full[s]);
     }
     const bool some = T.first < T.end;
     if (some) {
-      ok = ok && E.wait(C.o_full[s], uo++ & 1u);
+      ok = E.wait(C.o_full[s], uo++ & 1u) && ok;
       tc_fence_after();
     }
     if (!ok) l = NAN;
+    if (some) {
+      l += swap_with_other(C, s, half, r, l);
+      named_bar_sync(1 + s * 4 + (r >> 5), 64);
+    }
     const bool whole = w.whole();
     float* part = reinterpret_cast<float*>(a.part + (2 * (size_t)blockIdx.x + (w.skip ? 0 : 1)) * a.slot);
-    const int pr = s * TR + tid;
+    const int pr = s * TR + r;
     const int tok = row / a.group, hd = w.h * a.group + row - tok * a.group;
     const long long t = w.q.row0 + tok;
-    const bool there = tid < T.rows;
     const long long off = there ? t * a.p.ldo + (long long)hd * D : -1;
-    float* lse = a.p.lse ? a.p.lse + t * a.p.ld_lse + hd : nullptr;
+    float* lse = a.p.lse && half == 0 ? a.p.lse + t * a.p.ld_lse + hd : nullptr;
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-    for (int c0 = 0; c0 < D; c0 += 32) {
-      float f[32];
-      if (some && ok) {
-        tmem_ld32(to + (uint32_t)c0, reinterpret_cast<uint32_t*>(f));
-        tmem_wait_ld();
+    for (int c0 = d0; c0 < d1; c0 += 32) {
+      uint32_t o[32];
+      if (some) {
+        tmem_ld32(to + (uint32_t)(c0 - d0), o);
+        tmem_wait_ld32(o);
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) f[j] = ok ? 0.f : NAN;
+        for (int j = 0; j < 32; ++j) o[j] = 0u;
       }
+      float f[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) f[j] = ok ? __uint_as_float(o[j]) : NAN;
       if (whole) {
         store_32<BF>(a, off, c0, f, inv);
       } else if (there) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4)
-          if (c0 + j < D) *part_values(part, pr, c0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+          if (c0 + j < d1) *part_values(part, pr, c0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
       }
     }
     if (some) warp_arrive(C.o_free[s]);
-    if (there) {
+    if (there && half == 0) {
       if (!whole) *reinterpret_cast<float2*>(part + 2 * pr) = make_float2(m, l);
       else if (lse) *lse = attn_lse<BF>(m, l);
     }
     if (!whole) {
       int c0;
       const int n = AttnCut<Work::SNAP>::parts(C.plan, w.begin(), w.end(), &c0);
-      named_bar_sync(1 + s, TR);
-      if (tid == 0) {
+      named_bar_sync(9 + s, 2 * TR);
+      if (half == 0 && r == 0) {
         __threadfence();
         unsigned* count = a.count + 2 * c0 + s;
         const bool last = atomicAdd(count, 1u) == (unsigned)(n - 1);
         if (last) *count = 0u;
         C.last[s] = last;
       }
-      named_bar_sync(1 + s, TR);
+      named_bar_sync(9 + s, 2 * TR);
       if (C.last[s]) {
         __threadfence();
-        join_row<BF>(a, c0, n, pr, there, off, lse);
+        join_row<BF>(a, c0, n, pr, there, d0, d1, off, lse);
       }
-      named_bar_sync(1 + s, TR);  // `last` has been read
+      named_bar_sync(9 + s, 2 * TR);  // `last` has been read
     }
   }
 }
@@ -743,7 +776,7 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
 template <int DH, bool BF>
 __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t raw_smem[];
-  uint8_t* sm = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+  uint8_t* sm = raw_smem;  // on its 1024 bytes: there is no room to move it
   uint8_t* ring = sm + 2 * Cfg<DH>::SLOT;
   TilesCtl& C = *reinterpret_cast<TilesCtl*>(ring + Cfg<DH>::NS * Cfg<DH>::SLOT);
   const int warp = threadIdx.x >> 5;
@@ -757,9 +790,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
       mbar_init(attn_bar(C.q_full[i]), 1);
       mbar_init(attn_bar(C.q_empty[i]), 1);
       mbar_init(attn_bar(C.s_full[i]), 1);
-      mbar_init(attn_bar(C.p_full[i]), 4);
+      mbar_init(attn_bar(C.p_full[i]), 8);
       mbar_init(attn_bar(C.o_full[i]), 1);
-      mbar_init(attn_bar(C.o_free[i]), 4);
+      mbar_init(attn_bar(C.o_free[i]), 8);
       mbar_init(attn_bar(C.done[i]), 1);
     }
     mbar_init(attn_bar(C.landed), 1);
@@ -774,9 +807,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = C.tmem;
 
-  if (warp < 8) {
+  if (warp < NSOFT / 32) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFT));
-    run_softmax<DH, BF>(a, C, tmem, warp >> 2);
+    run_softmax<DH, BF>(a, C, tmem, warp >> 3, (warp >> 2) & 1);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_REST));
     if (warp == W_K) {
