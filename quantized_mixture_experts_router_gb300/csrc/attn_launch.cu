@@ -33,6 +33,20 @@ bool make_cache_map(CUtensorMap* m, const moe_v41_kv_cfg& c, const void* base, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as [m][heads][head_dim] in boxes of 64 values x group heads x the tokens
+// that make 128 rows with them.
+bool make_query_map(CUtensorMap* m, const AttnParams& p, int group) {
+  auto fn = encode_fn();
+  const cuuint64_t d = (cuuint64_t)p.c.kv.head_dim, h = (cuuint64_t)p.c.heads;
+  const cuuint64_t dims[3] = {d, h, (cuuint64_t)p.m};
+  const cuuint64_t strides[2] = {d * 2, (p.m > 1 ? (cuuint64_t)p.ldq : d * h) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(p.q), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 size_t attn_workspace_bytes(const moe_v41_attn_cfg& c) { return attn_ws(c).total; }
@@ -62,6 +76,8 @@ int launch_paged_attention(const AttnParams& p, int max_new, void* ws, cudaStrea
   };
   if ((long long)max_new * a.group > ATTN_ROWS_TILE) {
     if (!maps(ATTN_TILES_KEYS)) return MOE_ERR_CUDA;
+    a.q_map = 128 % a.group == 0 && p.ldq < (int64_t(1) << 38);
+    if (a.q_map && !make_query_map(&a.map_q, p, a.group)) return MOE_ERR_CUDA;
     bool taken = false;
     const int rc = launch_attn_tiles(a, ctas, &taken, s);
     if (rc || taken) return rc;

@@ -239,7 +239,7 @@ template <class W>
 struct AttnWalk {
   static constexpr int R = W::R, TK = W::TK;
   const AttnParams& p;
-  const int group;
+  int group;
   long long at, left;      // place of the item's part in the line; what is left of the run from there on
   int b, h, i, row_tiles;
   AttnSeq q;
@@ -326,6 +326,7 @@ inline AttnWs attn_ws(const moe_v41_attn_cfg& c) {
 // What a kernel needs beside the call's parameters.
 struct AttnArgs {
   CUtensorMap map_k, map_v;
+  CUtensorMap map_q;       // kernel for many rows, with q_map
   AttnParams p;
   int group;               // query heads of a key head
   int page_shift, box_rows;
@@ -335,6 +336,7 @@ struct AttnArgs {
   char* part;              // [blocks][2] of slot bytes each
   size_t slot;
   unsigned long long timeout_ns;
+  bool q_map;              // a row tile's queries are one box: the group divides it
 };
 int launch_attn_rows(const AttnArgs& a, int ctas, cudaStream_t s);
 int launch_attn_tiles(const AttnArgs& a, int ctas, bool* taken, cudaStream_t s);  // *taken: whether it was launched
@@ -435,6 +437,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
       "[%6];" ::"r"(dst),
       "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
 

@@ -5,20 +5,20 @@
 //   S = Q K^T,   P = exp2(c S - m),   O += P V   (tcgen05, f32 in tensor memory)
 //
 // Roles of a block (one an SM, persistent over its run of the line):
-//   warps 0-7, 8-15  softmax of the first and second row tile, a row a pair of threads,
-//                    64 keys each (one warp alone gets an exponential out every eight
-//                    cycles, two every four): S out of tensor memory, maximum, P as
-//                    16-bit values over S, sum
-//   warps 16, 17     issue the products of the first and second row tile
-//   warp 18          copies keys (TMA boxes of a page's slots) into a ring
-//   warp 19          copies queries, and values into a ring
+//   warps 0-3, 4-7   softmax of the first and second row tile, a row a thread: S out
+//                    of tensor memory, maximum, P as 16-bit values over S, sum
+//   warps 8, 9       issue the products of the first and second row tile
+//   warp 10          copies keys (TMA boxes of a page's slots) into a ring
+//   warp 11          copies queries, and values into a ring
 // While one row tile is in its softmax the tensor cores work on the other.  A warp
 // issues P V of a key tile and Q K of the next one behind another, as the second
 // overwrites the P of the first.
 // V lies in shared memory as it lies in the cache, [key][value], and is read as an
 // operand whose values, not keys, are contiguous.  A row's output is rescaled only
 // when its maximum has grown by more than 2^8 over the reference, which its own
-// threads then do in place.
+// thread then does in place.
+#include <new>
+
 #include "attn_work.cuh"
 #include "tc.cuh"
 
@@ -27,15 +27,14 @@ namespace moe {
 namespace {
 
 constexpr int R = ATTN_TILES_TILE, TK = ATTN_TILES_KEYS, TR = 128;
-constexpr int W_MMA = 16, W_K = 18, W_V = 19;
+constexpr int W_MMA = 8, W_K = 10, W_V = 11;
 // An item costs about as much as three key tiles beside its own, and so does a join.
 using Work = AttnWork<R, TK, 3, 6, 6>;
 using Walk = AttnWalk<Work>;
-constexpr int NSOFT = 512, NTHR = 640;
-// Registers a thread: 96 at launch; the softmax warps take what the others leave.
-constexpr int REG_LAUNCH = 96, REG_SOFT = 104, REG_REST = 64;
+constexpr int NSOFT = 256, NTHR = 384;
+// Registers a thread: 168 at launch; the softmax warps take what the others leave.
+constexpr int REG_LAUNCH = 168, REG_SOFT = 200, REG_REST = 104;
 static_assert(NSOFT * REG_SOFT + (NTHR - NSOFT) * REG_REST <= NTHR * REG_LAUNCH, "register shares exceed the launch's");
-constexpr int KH = TK / 2;           // keys of a softmax thread
 constexpr uint32_t HALF = TK * 128;  // 64 values of 128 keys or rows
 
 template <int DH>
@@ -53,38 +52,41 @@ struct TilesCtl {
   unsigned long long o_full[2], o_free[2];      // an item's output, complete; read
   unsigned long long done[2];
   uint32_t tmem, abort, last[2], turn;
-  float swap[2][2][TR];                         // what a row's two threads tell each other: [row tile][half][row]
+  float2 hand[TR];                              // (maximum, sum) of a row that the second half hands to the first
   AttnPlan plan;
+  // Where the softmax warps are in the run: not in registers, which hold a tile's scores.
+  alignas(8) unsigned char walk[NSOFT / 32][sizeof(Walk)];
 };
 template <int DH>
 constexpr uint32_t SMEM_BYTES = (2 + Cfg<DH>::NS) * Cfg<DH>::SLOT + ((sizeof(TilesCtl) + 15) & ~15u);
 static_assert(SMEM_BYTES<1> <= 232448 && SMEM_BYTES<2> <= 232448, "shared memory of a block");
 
-// What one row tile of an item does in this run's part of it.
+// What one half of the softmax and issuing warps does in this run's part of an item:
+// one of its two row tiles, or, where there is but one, every other key tile of it.
 struct Tile {
-  int rows;        // rows of the tile that there are
-  AttnRange keys;  // that any of them sees
-  int first, end;  // key tiles to go through
-  __device__ __forceinline__ Tile() {}
-  static __device__ __forceinline__ Tile none() {
-    Tile T;
-    T.rows = T.first = T.end = 0;
-    T.keys = AttnRange{0, 0};
-    return T;
-  }
+  int row0;             // of the item
+  int rows;             // that there are
+  AttnRange keys;       // that any of them sees
+  int first, last;      // key tiles to go through, none if last < first
+  int step;
+  bool split;           // the other half has the same rows
   __device__ __forceinline__ Tile(const AttnArgs& a, const Walk& w, int s) {
-    rows = min(max(w.rows() - s * TR, 0), TR);
-    first = end = 0;
-    keys = AttnRange{0, 0};
-    if (rows == 0) return;
-    const int r0 = w.row0() + s * TR;
+    split = w.rows() <= TR;
+    row0 = split ? 0 : s * TR;
+    rows = min(w.rows() - row0, TR);
+    step = split ? 2 : 1;
+    first = 0;
+    last = -1;
+    const int r0 = w.row0() + row0;
     keys = attn_range(a.p, w.q, a.group, r0, r0 + rows);
     if (keys.hi <= keys.lo) return;
-    const int from = w.key0() / TK, to = from + w.key_steps();
-    first = max(keys.lo / TK, from);
-    end = max(min((keys.hi - 1) / TK + 1, to), first);
+    const int from = w.key0() / TK, to = from + w.key_steps() - 1;
+    first = max(keys.lo / TK, from) + (split ? s : 0);
+    last = min((keys.hi - 1) / TK, to);
+    if (split && ((last - first) & 1)) --last;
   }
-  __device__ __forceinline__ bool has(int k) const { return k >= first && k < end; }
+  __device__ __forceinline__ bool any() const { return first <= last; }
+  __device__ __forceinline__ bool has(int k) const { return k >= first && k <= last && (step == 1 || !((k - first) & 1)); }
 };
 
 struct Env {
@@ -127,7 +129,22 @@ struct Ring {
     pages.begin(a.p.s.table + w.b * a.p.s.ld_table, max(w.key0(), w.keys.lo) >> a.page_shift,
                 (w.keys.hi - 1) >> a.page_shift);
   }
-  // The tile at `key` into the next slot; `bar` hears of it.
+  // The boxes of the tile at `key`: whether this lane has one, of which page; all of them.
+  bool mine;
+  int id, slot0;
+  uint32_t bytes;
+  __device__ __forceinline__ void locate(const Walk& w, int key) {
+    const int k = key + box * br;
+    mine = half < DH && k + br > w.keys.lo && k < w.keys.hi;
+    slot0 = k & (a.p.c.kv.page_size - 1);
+    pages.advance(max(key, w.keys.lo) >> a.page_shift);
+    id = pages.at(min(max(k, w.keys.lo), w.keys.hi - 1) >> a.page_shift);
+    bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * (uint32_t)br * 128u;
+    if (mine && (id < 0 || id >= a.p.c.kv.n_pages)) {
+      atomicOr(a.status, (unsigned)MOE_STATUS_BAD_PAGE);
+      id = a.p.c.kv.n_pages;  // outside: filled with zeros
+    }
+  }
   __device__ __forceinline__ bool next_slot() {
     st = st + 1 == NS ? 0 : st + 1;
     if ((used >> st) & 1u) {
@@ -137,21 +154,13 @@ struct Ring {
     used |= 1u << st;
     return true;
   }
-  __device__ __forceinline__ void copy(const Walk& w, int key, unsigned long long& bar) {
-    const int lane = threadIdx.x & 31, k = key + box * br;
-    const bool mine = half < DH && k + br > w.keys.lo && k < w.keys.hi;
-    pages.advance(max(key, w.keys.lo) >> a.page_shift);
-    int id = pages.at(min(max(k, w.keys.lo), w.keys.hi - 1) >> a.page_shift);
-    const unsigned boxes = __ballot_sync(0xffffffffu, mine);
-    if (mine && (id < 0 || id >= a.p.c.kv.n_pages)) {
-      atomicOr(a.status, (unsigned)MOE_STATUS_BAD_PAGE);
-      id = a.p.c.kv.n_pages;  // outside: filled with zeros
-    }
-    if (lane == 0) mbar_arrive_expect_tx(attn_bar(bar), (uint32_t)__popc(boxes) * (uint32_t)br * 128u);
+  // The boxes into the slot; `bar` hears of them.
+  __device__ __forceinline__ void copy(const Walk& w, unsigned long long& bar) {
+    if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(attn_bar(bar), bytes);
     __syncwarp();
     if (mine)
-      tma_load_4d(smem + st * Cfg<DH>::SLOT + (uint32_t)half * HALF + (uint32_t)(box * br) * 128u, map, half * 64,
-                  k & (a.p.c.kv.page_size - 1), w.h, id, attn_bar(bar));
+      tma_load_4d(smem + st * Cfg<DH>::SLOT + (uint32_t)half * HALF + (uint32_t)(box * br) * 128u, map, half * 64, slot0, w.h,
+                  id, attn_bar(bar));
   }
   // Copies in flight land before the block can exit: each slot's last one (its full
   // barrier's phase flips with every use, as `par` does from the second use on).
@@ -171,19 +180,34 @@ __device__ void run_k(const AttnArgs& a, TilesCtl& C, uint32_t ring) {
     if (!steps) continue;
     K.begin(w);
     for (int j = 0; j < steps; ++j) {
+      K.locate(w, w.key0() + j * TK);
       ok = K.next_slot();
       if (!ok) break;
-      K.copy(w, w.key0() + j * TK, K.full[K.st]);
+      K.copy(w, K.full[K.st]);
     }
   }
   K.drain();
 }
 
-// A row tile's queries into the swizzled layout, rows and values that there are
-// none of as zeros.
+// A row tile's queries into the swizzled layout; `full` hears of them.  By boxes of
+// [tokens][heads of the group] where these make a row tile: rows that there are none
+// of then hold what comes next in memory, or zeros, which concerns nobody.  Else
+// piece by piece, rows and values that there are none of as zeros.
 template <int DH>
-__device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, const Tile& T, int s, uint32_t q_smem) {
+__device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, const Tile& T, uint32_t q_smem,
+                                       unsigned long long& full) {
   const int lane = threadIdx.x & 31, D = a.p.c.kv.head_dim;
+  if (a.q_map) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(attn_bar(full), Cfg<DH>::SLOT);
+      const int tok = w.q.row0 + (w.row0() + T.row0) / a.group;
+#pragma unroll
+      for (int half = 0; half < DH; ++half)
+        tma_load_3d(q_smem + half * HALF, &a.map_q, half * 64, w.h * a.group, tok, attn_bar(full));
+    }
+    __syncwarp();
+    return;
+  }
   constexpr int CH = DH * 8;         // 16-byte pieces of a row
   constexpr int RPI = 32 / CH;       // rows an instruction of the warp covers
   const int ch = lane % CH, rr = lane / CH;
@@ -192,10 +216,10 @@ __device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, const T
 #pragma unroll 1
   for (int r0 = 0; r0 < TR; r0 += 32) {
     // each lane finds one of 32 rows
-    const int r = r0 + lane, row = w.row0() + s * TR + r, tok = row / a.group;
+    const int r = r0 + lane, row = w.row0() + T.row0 + r, tok = row / a.group;
     const long long at = (w.q.row0 + tok) * a.p.ldq + (long long)(w.h * a.group + row - tok * a.group) * D;
     const long long off = r < T.rows ? at : -1;
-#pragma unroll 8
+#pragma unroll 4
     for (int i = 0; i < 32; i += RPI) {
       const long long o = __shfl_sync(0xffffffffu, off, i + rr);
       const bool there = o >= 0 && in;
@@ -208,6 +232,7 @@ __device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, const T
   asm volatile("cp.async.wait_all;" ::: "memory");
   fence_async_smem();
   __syncwarp();
+  if (lane == 0) mbar_arrive(attn_bar(full));
 }
 
 // Value slots of the tile at key0 that the item's rows do not see, in steps of 16
@@ -250,24 +275,25 @@ __device__ void run_qv(const AttnArgs& a, TilesCtl& C, uint32_t q_smem, uint8_t*
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const Tile T(a, w, s);
-      if (T.first >= T.end || !ok) continue;
-      ok = E.wait(C.q_empty[s], (uses[s]++ & 1u) ^ 1u);  // passes at once the first time
+      if (!T.any() || !ok) continue;
+      ok = E.wait(C.q_empty[s], (uses[s] & 1u) ^ 1u);  // passes at once the first time
       if (!ok) break;
-      copy_q<DH>(a, w, T, s, q_smem + (uint32_t)s * Cfg<DH>::SLOT);
-      if (lane == 0) mbar_arrive(attn_bar(C.q_full[s]));
+      ++uses[s];
+      copy_q<DH>(a, w, T, q_smem + (uint32_t)s * Cfg<DH>::SLOT, C.q_full[s]);
     }
     if (!ok) break;
     V.begin(w);
     for (int j = 0; j < steps; ++j) {
+      const int key = w.key0() + j * TK;
+      V.locate(w, key);
       ok = V.next_slot();
       if (!ok) break;
-      const int key = w.key0() + j * TK;
       const Edge e(key, w.keys);
       if (!e.has(0) && !e.has(1)) {
-        V.copy(w, key, V.full[V.st]);
+        V.copy(w, V.full[V.st]);
         continue;
       }
-      V.copy(w, key, C.landed);
+      V.copy(w, C.landed);
       ok = E.wait(C.landed, edges++ & 1u);
       if (!ok) {
         flying = true;
@@ -279,6 +305,9 @@ __device__ void run_qv(const AttnArgs& a, TilesCtl& C, uint32_t q_smem, uint8_t*
     }
   }
   V.drain();
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    if (uses[s]) mbar_wait_bounded(attn_bar(C.q_full[s]), (uses[s] - 1) & 1u, globaltimer_ns() + a.timeout_ns, a.status);
   if (flying) mbar_wait_bounded(attn_bar(C.landed), (edges - 1) & 1u, globaltimer_ns() + a.timeout_ns, a.status);
 }
 
@@ -319,7 +348,7 @@ struct Steps {
   int k, end;
   bool live;
   __device__ __forceinline__ Steps(const AttnArgs& a_, const AttnPlan& plan, int s_)
-      : a(a_), s(s_), w(a_.p, a_.group, plan), T(Tile::none()) {
+      : a(a_), s(s_), w(a_.p, a_.group, plan), T(a_, w, s_) {
     item();
   }
   __device__ __forceinline__ void item() {
@@ -345,15 +374,11 @@ struct Product {
     const int key0 = t.k * TK;
     active = t.T.has(t.k);
     first = t.k == t.T.first;
-    last = t.k == t.T.end - 1;
+    last = t.k == t.T.last;
     from = max(t.T.keys.lo - key0, 0) / 16;
     to = (min(t.T.keys.hi - key0, TK) + 15) / 16;
   }
 };
-
-// Column of the weights of the 16 keys 16 i .. over the scores: those of either half of
-// the keys lie where that half's scores were.
-__device__ __forceinline__ uint32_t p_col(int i) { return (uint32_t)(i * 8 + (i >= 4 ? 32 : 0)); }
 
 // The tensor cores take the products of both issuing warps in turn.  Held while one
 // row tile's are issued, so that they do not mix with the other's: mixed, both tiles'
@@ -418,7 +443,7 @@ __device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, uin
     if (more && !full(ks)) return;
     if (!full(NK + vs)) return;
     const uint32_t k = uniform(desc_lo(ring + ks * Cfg<DH>::SLOT)), v = uniform(desc_v_lo(ring + (NK + vs) * Cfg<DH>::SLOT));
-    const bool straight = more && N.active && !N.first;  // the next scores of the same queries
+    const bool straight = more && P.active && N.active && !N.first;  // the next scores of the same queries
     if (P.active) {
       if (P.first && !E.wait(C.o_free[S], (uo++ & 1u) ^ 1u)) return;  // passes at once the first time
       if (!E.wait(C.p_full[S], up++ & 1u)) return;
@@ -429,11 +454,11 @@ __device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, uin
           umma_f16_ta(o, sp, desc(v), id_pv, P.first ? 0u : 1u);
 #pragma unroll
           for (int i = 1; i < TK / 16; ++i)
-            umma_f16_ta(o, sp + p_col(i), desc(v + (uint32_t)i * (2048u >> 4)), id_pv, 1u);
+            umma_f16_ta(o, sp + (uint32_t)i * 8u, desc(v + (uint32_t)i * (2048u >> 4)), id_pv, 1u);
         } else {
 #pragma unroll 1
           for (int i = P.from; i < P.to; ++i)
-            umma_f16_ta(o, sp + p_col(i), desc(v + (uint32_t)i * (2048u >> 4)), id_pv, !(P.first && i == P.from));
+            umma_f16_ta(o, sp + (uint32_t)i * 8u, desc(v + (uint32_t)i * (2048u >> 4)), id_pv, !(P.first && i == P.from));
         }
         if (P.last) umma_commit(attn_bar(C.o_full[S]));
         if (straight) {
@@ -450,7 +475,7 @@ __device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, uin
     if (!more) return;
     if (!straight) {
       if (N.active) {
-        if (!E.wait(C.q_full[S], uq++ & 1u)) return;
+        if (N.first && !E.wait(C.q_full[S], uq++ & 1u)) return;
         tc_fence_after();
         if (elect_one()) {
           scores(k, N);
@@ -510,41 +535,32 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 
-// What the row's other thread has, for what this one has.  The next may be told only
-// when both have read this.
-__device__ __forceinline__ float swap_with_other(TilesCtl& C, int s, int half, int row, float mine) {
-  C.swap[s][half][row] = mine;
-  named_bar_sync(1 + s * 4 + (row >> 5), 64);
-  return C.swap[s][half ^ 1][row];
-}
-
-// One key tile of this thread's row, its half of the keys: key0 is the half's first.
+// One key tile of this thread's row.
 template <int DH, bool BF>
-__device__ __forceinline__ void soft_tile(TilesCtl& C, int s, int half, int row, uint32_t ts, uint32_t to, int key0, int lo,
-                                          int hi, float c, bool first, float& m, float& l) {
-  uint32_t v[KH];
-  tmem_ld32(ts, v);
-  tmem_ld32(ts + 32u, v + 32);
-  tmem_wait_ld32(v);
-  tmem_wait_ld32(v + 32);
-  const int from = lo - key0, end = hi - key0;  // of the keys, what the row sees
-  if (__any_sync(0xffffffffu, from > 0 || end < KH)) {
+__device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, int lo, int hi, float c, bool first, float& m,
+                                          float& l) {
+  uint32_t v[TK];
 #pragma unroll
-    for (int j = 0; j < KH; ++j)
+  for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32u * i, v + 32 * i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tmem_wait_ld32(v + 32 * i);
+  const int from = lo - key0, end = hi - key0;  // of the tile's keys, what the row sees
+  if (__any_sync(0xffffffffu, from > 0 || end < TK)) {
+#pragma unroll
+    for (int j = 0; j < TK; ++j)
       if (j < from || j >= end) v[j] = 0xff800000u;  // -inf
   }
   float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int j = 0; j < KH; j += 2) t[(j / 2) & 3] = fmaxf(fmaxf(t[(j / 2) & 3], __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
-  float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
-  // (the next tile's scores come after both have told that they are done with these)
-  top = fmaxf(top, swap_with_other(C, s, half, row, top));
+  for (int j = 0; j < TK; j += 2) t[(j / 2) & 3] = fmaxf(fmaxf(t[(j / 2) & 3], __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
+  const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
   const bool rise = top > m + ATTN_SLACK;  // from -inf: by anything
   if (first) {
     m = top;
@@ -554,7 +570,7 @@ __device__ __forceinline__ void soft_tile(TilesCtl& C, int s, int half, int row,
     m = next;
     l *= f;
 #pragma unroll 1
-    for (int i = 0; i < DH * 2; ++i) {  // this thread's half of the output
+    for (int i = 0; i < DH * 4; ++i) {
       uint32_t o[16];
       tmem_ld16(to + 16u * i, reinterpret_cast<float*>(o));
 #pragma unroll
@@ -566,7 +582,7 @@ __device__ __forceinline__ void soft_tile(TilesCtl& C, int s, int half, int row,
   const uint64_t c2 = pack_f32(c, c), ref2 = pack_f32(-ref, -ref);
   uint64_t sum[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < KH / 32; ++i) {
+  for (int i = 0; i < 4; ++i) {
     uint32_t p[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -638,11 +654,10 @@ __device__ __forceinline__ void store_32(const AttnArgs& a, long long off, int c
   }
 }
 
-// Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left; values from .. to - 1
-// of this thread's row.
+// Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left; this thread's row.
 template <bool BF>
-__device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int row, bool there, int from, int to,
-                                         long long off, float* lse) {
+__device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int row, bool there, long long off, float* lse) {
+  const int D = a.p.c.kv.head_dim;
   auto part = [&](int x) { return reinterpret_cast<float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot); };
   auto ml = [&](int x) { return there ? __ldcg(reinterpret_cast<const float2*>(part(x)) + row) : make_float2(-INFINITY, 0.f); };
   float m = -INFINITY, l = 0.f;
@@ -656,14 +671,14 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int r
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-  for (int d0 = from; d0 < to; d0 += 32) {
+  for (int d0 = 0; d0 < D; d0 += 32) {
     float acc[32] = {};
-#pragma unroll 1
+#pragma unroll 2
     for (int x = 0; x < n; ++x) {
       float4 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v[i] = there && d0 + 4 * i < to ? __ldcg(part_values(part(x), row, d0 + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[i] = there && d0 + 4 * i < D ? __ldcg(part_values(part(x), row, d0 + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
       const float2 y = ml(x);
       const float f = y.y == 0.f ? 0.f : exp2_fast(y.x - ref);  // (0: nothing seen)
 #pragma unroll
@@ -680,95 +695,139 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int r
 }
 
 template <int DH, bool BF>
-__device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s, int half) {
+__device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s) {
   const Env E{a, C};
   const int r = threadIdx.x & 127, D = a.p.c.kv.head_dim;  // row of the row tile
   const uint32_t lanes = (uint32_t)(r & ~31) << 16;
-  const uint32_t ts = tmem + lanes + (uint32_t)s * 128u + (uint32_t)half * KH;
-  const int d0 = half * DH * 32, d1 = min(D, d0 + DH * 32);  // this thread's values of the output
-  const uint32_t to = tmem + lanes + 256u + (uint32_t)(s * DH * 64 + d0);
+  const uint32_t ts = tmem + lanes + (uint32_t)s * 128u, to = tmem + lanes + 256u + (uint32_t)(s * DH * 64);
   uint32_t us = 0, uo = 0;  // uses of s_full and o_full
   bool ok = true;
-  for (Walk w(a.p, a.group, C.plan); w.live; w.next()) {
-    const Tile T(a, w, s);
-    if (T.rows == 0) continue;
-    const bool there = r < T.rows;
-    const int row = w.row0() + s * TR + r;  // of the sequence
+  Walk& w = *reinterpret_cast<Walk*>(C.walk[threadIdx.x >> 5]);
+  const bool lead = (threadIdx.x & 31) == 0;
+  if (lead) new (&w) Walk(a.p, a.group, C.plan);
+  __syncwarp();
+  auto next = [&] {
+    __syncwarp();
+    if (lead) w.next();
+    __syncwarp();
+  };
+  for (; w.live; next()) {
     int lo = 0, hi = INT_MAX;
-    if (there) {
-      const AttnRange g = attn_range(a.p, w.q, a.group, row, row + 1);
-      lo = g.lo;
-      hi = g.hi;
+    int first, last, step;
+    {
+      const Tile T(a, w, s);
+      first = T.first;
+      last = T.last;
+      step = T.step;
+      if (r < T.rows) {
+        const int row = w.row0() + T.row0 + r;  // of the sequence
+        const AttnRange g = attn_range(a.p, w.q, a.group, row, row + 1);
+        lo = g.lo;
+        hi = g.hi;
+      }
     }
+    const bool some = first <= last;
     float m = -INFINITY, l = 0.f;
-    for (int k = T.first; k < T.end; ++k) {
-      // both warps of a row give up together: they meet at a barrier
-      ok = E.wait(C.s_full[s], us++ & 1u) && ok;
+    for (int k = first; k <= last; k += step) {
+      ok = ok && E.wait(C.s_full[s], us++ & 1u);
+      if (!ok) break;
       tc_fence_after();
-      soft_tile<DH, BF>(C, s, half, r, ts, to, k * TK + half * KH, lo, hi, a.c, k == T.first, m, l);
+      soft_tile<DH, BF>(ts, to, k * TK, lo, hi, a.c, k == first, m, l);
       warp_arrive(C.p_full[s]);
     }
-    const bool some = T.first < T.end;
     if (some) {
-      ok = E.wait(C.o_full[s], uo++ & 1u) && ok;
+      ok = ok && E.wait(C.o_full[s], uo++ & 1u);
       tc_fence_after();
     }
+    const Tile T(a, w, s);
+    const bool there = r < T.rows;
+    const int row = w.row0() + T.row0 + r;
     if (!ok) l = NAN;
-    if (some) {
-      l += swap_with_other(C, s, half, r, l);
-      named_bar_sync(1 + s * 4 + (r >> 5), 64);
+    // With one row tile the second half hands what it has to the first.
+    float f0 = 1.f, f1 = 0.f;
+    bool other = false;
+    if (T.split) {
+      if (s == 1) {
+        C.hand[r] = make_float2(m, l);
+        tc_fence_before();
+      }
+      named_bar_sync(3, NSOFT);
+      float m1 = 0.f, l1 = 0.f;
+      if (s == 0) {
+        m1 = C.hand[r].x;
+        l1 = C.hand[r].y;
+        tc_fence_after();
+      }
+      named_bar_sync(3, NSOFT);
+      if (s == 1) continue;
+      other = Tile(a, w, 1).any();
+      const float top = fmaxf(m, m1), ref = top == -INFINITY ? 0.f : top;
+      f0 = l == 0.f ? 0.f : exp2_fast(m - ref);
+      f1 = l1 == 0.f ? 0.f : exp2_fast(m1 - ref);
+      l = f0 * l + f1 * l1;
+      m = top;
     }
     const bool whole = w.whole();
     float* part = reinterpret_cast<float*>(a.part + (2 * (size_t)blockIdx.x + (w.skip ? 0 : 1)) * a.slot);
-    const int pr = s * TR + r;
+    const int pr = T.row0 + r;
     const int tok = row / a.group, hd = w.h * a.group + row - tok * a.group;
     const long long t = w.q.row0 + tok;
     const long long off = there ? t * a.p.ldo + (long long)hd * D : -1;
-    float* lse = a.p.lse && half == 0 ? a.p.lse + t * a.p.ld_lse + hd : nullptr;
+    float* lse = a.p.lse ? a.p.lse + t * a.p.ld_lse + hd : nullptr;
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-    for (int c0 = d0; c0 < d1; c0 += 32) {
-      uint32_t o[32];
-      if (some) {
-        tmem_ld32(to + (uint32_t)(c0 - d0), o);
-        tmem_wait_ld32(o);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = 0u;
-      }
+    for (int c0 = 0; c0 < D; c0 += 32) {
       float f[32];
+      {
+        uint32_t o[32];
+        if (some) {
+          tmem_ld32(to + (uint32_t)c0, o);
+          tmem_wait_ld32(o);
+        }
 #pragma unroll
-      for (int j = 0; j < 32; ++j) f[j] = ok ? __uint_as_float(o[j]) : NAN;
+        for (int j = 0; j < 32; ++j) f[j] = !some || f0 == 0.f ? 0.f : f0 * __uint_as_float(o[j]);
+        if (other) {
+          tmem_ld32(to + (uint32_t)(c0 + DH * 64), o);
+          tmem_wait_ld32(o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] += f1 == 0.f ? 0.f : f1 * __uint_as_float(o[j]);
+        }
+      }
+      if (!ok) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) f[j] = NAN;
+      }
       if (whole) {
         store_32<BF>(a, off, c0, f, inv);
       } else if (there) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4)
-          if (c0 + j < d1) *part_values(part, pr, c0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+          if (c0 + j < D) *part_values(part, pr, c0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
       }
     }
     if (some) warp_arrive(C.o_free[s]);
-    if (there && half == 0) {
+    if (other) warp_arrive(C.o_free[1]);
+    if (there) {
       if (!whole) *reinterpret_cast<float2*>(part + 2 * pr) = make_float2(m, l);
       else if (lse) *lse = attn_lse<BF>(m, l);
     }
     if (!whole) {
       int c0;
       const int n = AttnCut<Work::SNAP>::parts(C.plan, w.begin(), w.end(), &c0);
-      named_bar_sync(9 + s, 2 * TR);
-      if (half == 0 && r == 0) {
+      named_bar_sync(1 + s, TR);
+      if (r == 0) {
         __threadfence();
         unsigned* count = a.count + 2 * c0 + s;
         const bool last = atomicAdd(count, 1u) == (unsigned)(n - 1);
         if (last) *count = 0u;
         C.last[s] = last;
       }
-      named_bar_sync(9 + s, 2 * TR);
+      named_bar_sync(1 + s, TR);
       if (C.last[s]) {
         __threadfence();
-        join_row<BF>(a, c0, n, pr, there, d0, d1, off, lse);
+        join_row<BF>(a, c0, n, pr, there, off, lse);
       }
-      named_bar_sync(9 + s, 2 * TR);  // `last` has been read
+      named_bar_sync(1 + s, TR);  // `last` has been read
     }
   }
 }
@@ -790,9 +849,9 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
       mbar_init(attn_bar(C.q_full[i]), 1);
       mbar_init(attn_bar(C.q_empty[i]), 1);
       mbar_init(attn_bar(C.s_full[i]), 1);
-      mbar_init(attn_bar(C.p_full[i]), 8);
+      mbar_init(attn_bar(C.p_full[i]), 4);
       mbar_init(attn_bar(C.o_full[i]), 1);
-      mbar_init(attn_bar(C.o_free[i]), 8);
+      mbar_init(attn_bar(C.o_free[i]), 4);
       mbar_init(attn_bar(C.done[i]), 1);
     }
     mbar_init(attn_bar(C.landed), 1);
@@ -809,7 +868,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
 
   if (warp < NSOFT / 32) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFT));
-    run_softmax<DH, BF>(a, C, tmem, warp >> 3, (warp >> 2) & 1);
+    run_softmax<DH, BF>(a, C, tmem, warp >> 2);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_REST));
     if (warp == W_K) {
