@@ -61,7 +61,7 @@ int launch_paged_attention(const AttnParams& p, int max_new, void* ws, cudaStrea
   uint8_t* base = static_cast<uint8_t*>(ws);
   AttnArgs a{};
   a.p = p;
-  a.group = p.c.heads / kv.kv_heads;
+  a.group = AttnGroup::of(p.c.heads / kv.kv_heads);
   a.page_shift = __builtin_ctz((unsigned)kv.page_size);
   a.c = p.c.scale * 1.4426950408889634f;
   a.status = &reinterpret_cast<Ctrl*>(base)->status;
@@ -74,10 +74,10 @@ int launch_paged_attention(const AttnParams& p, int max_new, void* ws, cudaStrea
     a.box_rows = min(kv.page_size, keys);
     return make_cache_map(&a.map_k, kv, p.k_cache, a.box_rows) && make_cache_map(&a.map_v, kv, p.v_cache, a.box_rows);
   };
-  if ((long long)max_new * a.group > ATTN_ROWS_TILE) {
+  if ((long long)max_new * a.group.n > ATTN_ROWS_TILE) {
     if (!maps(ATTN_TILES_KEYS)) return MOE_ERR_CUDA;
-    a.q_map = 128 % a.group == 0 && p.ldq < (int64_t(1) << 38);
-    if (a.q_map && !make_query_map(&a.map_q, p, a.group)) return MOE_ERR_CUDA;
+    a.q_map = 128 % a.group.n == 0 && p.ldq < (int64_t(1) << 38);
+    if (a.q_map && !make_query_map(&a.map_q, p, a.group.n)) return MOE_ERR_CUDA;
     bool taken = false;
     const int rc = launch_attn_tiles(a, ctas, &taken, s);
     if (rc || taken) return rc;

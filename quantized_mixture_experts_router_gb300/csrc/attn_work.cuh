@@ -20,6 +20,27 @@ constexpr int ATTN_MAX_CTAS = 152;
 // Rows and keys of an item's tiles in the kernel for few rows, and in that for many.
 constexpr int ATTN_ROWS_TILE = 16, ATTN_ROWS_KEYS = 32, ATTN_TILES_TILE = 256, ATTN_TILES_KEYS = 128;
 
+// Query heads of a key head, and division of rows by them: with s = ceil(log2 n) and
+// mul = floor(2^(31 + s) / n) + 1, r mul / 2^(31 + s) is off by less than 1 / n for 0 <= r < 2^31.
+struct AttnGroup {
+  int n;
+  unsigned shift;
+  unsigned long long mul;
+  static AttnGroup of(int n) {
+    AttnGroup g{n, 31, 0};
+    while ((1ull << (g.shift - 31)) < (unsigned)n) ++g.shift;
+    g.mul = (1ull << g.shift) / (unsigned)n + 1;
+    return g;
+  }
+  __device__ __forceinline__ int token(int row) const { return (int)(((unsigned long long)(unsigned)row * mul) >> shift); }
+};
+
+// a / b, quickly where both are small
+__device__ __forceinline__ long long attn_div(long long a, long long b) {
+  if (((unsigned long long)a | (unsigned long long)b) >> 32) return a / b;
+  return (long long)((unsigned)a / (unsigned)b);
+}
+
 // One sequence: its first row, new tokens, cached tokens that can be read, and
 // the first new token's position.
 struct AttnSeq {
@@ -40,11 +61,11 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
 struct AttnRange {
   int lo, hi;
 };
-__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, const AttnSeq& q, int group, int r0, int r1) {
+__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, const AttnSeq& q, const AttnGroup& group, int r0, int r1) {
   AttnRange g{0, q.len};
   if (p.c.causal) {
-    g.hi = min(max(q.pos0 + (r1 - 1) / group + 1, 0), q.len);
-    if (p.c.window) g.lo = min(max(q.pos0 + r0 / group - p.c.window + 1, 0), g.hi);
+    g.hi = min(max(q.pos0 + group.token(r1 - 1) + 1, 0), q.len);
+    if (p.c.window) g.lo = min(max(q.pos0 + group.token(r0) - p.c.window + 1, 0), g.hi);
   }
   return g;
 }
@@ -56,20 +77,20 @@ struct AttnWork {
   static constexpr int SNAP = SNAP_;        // an item is cut this far from its ends at the least
   static constexpr int MIN_RUN = MIN_RUN_;  // more blocks take part only if each has so many places, or an item
   static_assert(OVER >= 1 && SNAP > OVER, "every part of an item has a key tile");
-  static __device__ __forceinline__ int row_tiles(const AttnSeq& q, int group) {
-    return q.n > 0 ? (q.n * group - 1) / R + 1 : 0;
+  static __device__ __forceinline__ int row_tiles(const AttnSeq& q, const AttnGroup& group) {
+    return q.n > 0 ? (q.n * group.n - 1) / R + 1 : 0;
   }
-  static __device__ __forceinline__ AttnRange range(const AttnParams& p, const AttnSeq& q, int group, int i) {
-    return attn_range(p, q, group, i * R, min((i + 1) * R, q.n * group));
+  static __device__ __forceinline__ AttnRange range(const AttnParams& p, const AttnSeq& q, const AttnGroup& group, int i) {
+    return attn_range(p, q, group, i * R, min((i + 1) * R, q.n * group.n));
   }
   static __device__ __forceinline__ int key_tiles(const AttnRange& g) {
     return g.hi > g.lo ? (g.hi - 1) / TK + 1 - g.lo / TK : 0;
   }
-  static __device__ __forceinline__ int cost(const AttnParams& p, const AttnSeq& q, int group, int i) {
+  static __device__ __forceinline__ int cost(const AttnParams& p, const AttnSeq& q, const AttnGroup& group, int i) {
     return OVER + key_tiles(range(p, q, group, i));
   }
   // Places of one key head of each lane's sequence (0 where !valid), and its row tiles, by a whole warp.
-  static __device__ long long seq_cost(const AttnParams& p, int group, int b, bool valid, int* rows = nullptr) {
+  static __device__ long long seq_cost(const AttnParams& p, const AttnGroup& group, int b, bool valid, int* rows = nullptr) {
     const int lane = threadIdx.x & 31;
     AttnSeq q{};
     if (valid) q = attn_seq(p, b);
@@ -116,8 +137,8 @@ struct AttnCut {
   }
   // The runs that hold parts of the item begin .. end - 1: first, and how many.
   static __device__ __forceinline__ int parts(const AttnPlan& S, long long begin, long long end, int* first) {
-    const long long lo = ((begin + SNAP) * S.runs + S.total - 1) / S.total;      // first cut inside
-    const long long hi = ((end - SNAP + 1) * S.runs + S.total - 1) / S.total - 1;  // last cut inside
+    const long long lo = attn_div((begin + SNAP) * S.runs + S.total - 1, S.total);      // first cut inside
+    const long long hi = attn_div((end - SNAP + 1) * S.runs + S.total - 1, S.total) - 1;  // last cut inside
     *first = (int)lo - 1;
     return (int)(hi - lo) + 2;
   }
@@ -125,7 +146,7 @@ struct AttnCut {
 
 // By all NT threads of the block; ends with a barrier.
 template <class W, int NT>
-__device__ void attn_plan(const AttnParams& p, int group, AttnPlan& S) {
+__device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan& S) {
   using Cut = AttnCut<W::SNAP>;
   constexpr int NWARP = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -163,7 +184,7 @@ __device__ void attn_plan(const AttnParams& p, int group, AttnPlan& S) {
   const int run = (int)blockIdx.x;
   if (run < runs) {
     // the items that the even cuts fall into: the run's first and the next run's
-    const long long x[2] = {total * run / runs, total * (run + 1) / runs};
+    const long long x[2] = {attn_div(total * run, runs), attn_div(total * (run + 1), runs)};
     long long base = 0;
     for (int b0 = 0; b0 < batch && base <= x[1]; b0 += NT) {
       const long long c = b0 == 0 ? first : W::seq_cost(p, group, b0 + tid, b0 + tid < batch) * kh;
@@ -187,7 +208,7 @@ __device__ void attn_plan(const AttnParams& p, int group, AttnPlan& S) {
         if (at <= x[e] && x[e] < at + c) {
           S.b[e] = b0 + tid;
           S.base[e] = at;
-          S.per_head[e] = c / kh;
+          S.per_head[e] = attn_div(c, kh);
         }
     }
     __syncthreads();
@@ -199,7 +220,7 @@ __device__ void attn_plan(const AttnParams& p, int group, AttnPlan& S) {
         const AttnSeq q = attn_seq(p, S.b[warp]);
         const int nt = W::row_tiles(q, group);
         long long rem = xe - S.base[warp];
-        const int h = (int)(rem / S.per_head[warp]);
+        const int h = (int)attn_div(rem, S.per_head[warp]);
         rem -= h * S.per_head[warp];
         for (int i0 = 0; i0 < nt; i0 += 32) {
           const int i = i0 + lane;
@@ -239,7 +260,7 @@ template <class W>
 struct AttnWalk {
   static constexpr int R = W::R, TK = W::TK;
   const AttnParams& p;
-  int group;
+  const AttnGroup& group;
   long long at, left;      // place of the item's part in the line; what is left of the run from there on
   int b, h, i, row_tiles;
   AttnSeq q;
@@ -248,7 +269,7 @@ struct AttnWalk {
   int skip, take;          // the part: its first place in the item and how many
   bool live;
 
-  __device__ __forceinline__ AttnWalk(const AttnParams& p_, int group_, const AttnPlan& S) : p(p_), group(group_) {
+  __device__ __forceinline__ AttnWalk(const AttnParams& p_, const AttnGroup& group_, const AttnPlan& S) : p(p_), group(group_) {
     at = S.begin;
     left = S.end - at;
     live = left > 0;
@@ -295,7 +316,7 @@ struct AttnWalk {
   __device__ __forceinline__ bool whole() const { return take == cost(); }
   // of the sequence's rows
   __device__ __forceinline__ int row0() const { return i * R; }
-  __device__ __forceinline__ int rows() const { return min(R, q.n * group - i * R); }
+  __device__ __forceinline__ int rows() const { return min(R, q.n * group.n - i * R); }
   // key tiles of the part: a cut lies behind the item's first OVER places
   __device__ __forceinline__ int first_step() const { return skip ? skip - W::OVER : 0; }
   __device__ __forceinline__ int key_steps() const {
@@ -328,7 +349,7 @@ struct AttnArgs {
   CUtensorMap map_k, map_v;
   CUtensorMap map_q;       // kernel for many rows, with q_map
   AttnParams p;
-  int group;               // query heads of a key head
+  AttnGroup group;
   int page_shift, box_rows;
   float c;                 // scale log2 e
   unsigned* status;
@@ -413,7 +434,7 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
 
 template <bool BF>
 __device__ __forceinline__ void attn_store(const AttnArgs& a, int tok0, int h, int row, int d, const AttnJoined& j) {
-  const int tok = row / a.group, hd = h * a.group + row - tok * a.group;
+  const int tok = a.group.token(row), hd = h * a.group.n + row - tok * a.group.n;
   const long long t = tok0 + tok;
   const float s = j.l == 0.f ? 0.f : 1.f / j.l;
   uint2 v;

@@ -92,10 +92,10 @@ __device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, uint32_
   const int lane = threadIdx.x & 31, ch = lane % CH, D = a.p.c.kv.head_dim, rows = w.rows();
 #pragma unroll
   for (int i = 0; i < R / NP; i += RPI) {
-    const int r = pw + NP * (i + lane / CH), row = w.row0() + r, tok = row / a.group;
+    const int r = pw + NP * (i + lane / CH), row = w.row0() + r, tok = a.group.token(row);
     const bool there = r < rows && ch * 8 < D;
     const uint16_t* src = static_cast<const uint16_t*>(a.p.q);
-    if (there) src += (w.q.row0 + tok) * a.p.ldq + (long long)(w.h * a.group + row - tok * a.group) * D + ch * 8;
+    if (there) src += (w.q.row0 + tok) * a.p.ldq + (long long)(w.h * a.group.n + row - tok * a.group.n) * D + ch * 8;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                      q_smem + (uint32_t)(ch / 8) * QHALF + (uint32_t)r * 128u + (uint32_t)(((ch & 7) ^ (r & 7)) << 4)),
                  "l"(src), "r"(there ? 16 : 0)

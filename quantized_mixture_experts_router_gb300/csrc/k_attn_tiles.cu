@@ -8,7 +8,8 @@
 //   warps 0-3, 4-7   softmax of the first and second row tile, a row a thread: S out
 //                    of tensor memory, maximum, P as 16-bit values over S, sum
 //   warps 8, 9       issue the products of the first and second row tile
-//   warp 10          copies keys (TMA boxes of a page's slots) into a ring
+//   warp 10          walks through the run, tells the others its items, and copies keys
+//                    (TMA boxes of a page's slots) into a ring
 //   warp 11          copies queries, and values into a ring
 // While one row tile is in its softmax the tensor cores work on the other.  A warp
 // issues P V of a key tile and Q K of the next one behind another, as the second
@@ -17,8 +18,6 @@
 // operand whose values, not keys, are contiguous.  A row's output is rescaled only
 // when its maximum has grown by more than 2^8 over the reference, which its own
 // thread then does in place.
-#include <new>
-
 #include "attn_work.cuh"
 #include "tc.cuh"
 
@@ -45,55 +44,76 @@ struct Cfg {
   static constexpr int NS = NK + NV;
 };
 
+// One half of the softmax and issuing warps in this run's part of an item: one of
+// its two row tiles, or, where there is but one, every other key tile of it.
+struct Half {
+  int row0, rows;       // of the item
+  int lo, hi;           // keys that any of them sees
+  int first, last;      // key tiles to go through, none if last < first
+};
+// An item as the warps need it.
+struct Item {
+  int live;             // 0: the run has ended, and nothing else is told
+  int tok0, pos0, len;  // first row, its position, and the tokens of the sequence
+  int row0;             // of the sequence's rows (tokens x heads of the group)
+  int b, h;             // sequence, key head
+  int lo, hi;           // keys that any row sees
+  int from, steps;      // key tiles of the part
+  int whole, slot;      // not cut; which partial result of the block otherwise
+  int c0, n;            // the runs that hold its parts
+  int split;            // one row tile
+  Half half[2];
+};
+constexpr int NITEMS = 4;
+constexpr int ITEM_READERS = NSOFT / 32 + 3;  // softmax, issuing and value warps
+
 struct TilesCtl {
   unsigned long long full[10], empty[10], landed;
+  unsigned long long i_full[NITEMS], i_empty[NITEMS];
   unsigned long long q_full[2], q_empty[2];     // queries of a row tile
   unsigned long long s_full[2], p_full[2];      // scores to the softmax; weights to the products
   unsigned long long o_full[2], o_free[2];      // an item's output, complete; read
   unsigned long long done[2];
   uint32_t tmem, abort, last[2], turn;
+  Item items[NITEMS];
   float2 hand[TR];                              // (maximum, sum) of a row that the second half hands to the first
   AttnPlan plan;
-  // Where the softmax warps are in the run: not in registers, which hold a tile's scores.
-  alignas(8) unsigned char walk[NSOFT / 32][sizeof(Walk)];
 };
 template <int DH>
 constexpr uint32_t SMEM_BYTES = (2 + Cfg<DH>::NS) * Cfg<DH>::SLOT + ((sizeof(TilesCtl) + 15) & ~15u);
 static_assert(SMEM_BYTES<1> <= 232448 && SMEM_BYTES<2> <= 232448, "shared memory of a block");
-
-// What one half of the softmax and issuing warps does in this run's part of an item:
-// one of its two row tiles, or, where there is but one, every other key tile of it.
-struct Tile {
-  int row0;             // of the item
-  int rows;             // that there are
-  AttnRange keys;       // that any of them sees
-  int first, last;      // key tiles to go through, none if last < first
-  int step;
-  bool split;           // the other half has the same rows
-  __device__ __forceinline__ Tile(const AttnArgs& a, const Walk& w, int s) {
-    split = w.rows() <= TR;
-    row0 = split ? 0 : s * TR;
-    rows = min(w.rows() - row0, TR);
-    step = split ? 2 : 1;
-    first = 0;
-    last = -1;
-    const int r0 = w.row0() + row0;
-    keys = attn_range(a.p, w.q, a.group, r0, r0 + rows);
-    if (keys.hi <= keys.lo) return;
-    const int from = w.key0() / TK, to = from + w.key_steps() - 1;
-    first = max(keys.lo / TK, from) + (split ? s : 0);
-    last = min((keys.hi - 1) / TK, to);
-    if (split && ((last - first) & 1)) --last;
-  }
-  __device__ __forceinline__ bool any() const { return first <= last; }
-  __device__ __forceinline__ bool has(int k) const { return k >= first && k <= last && (step == 1 || !((k - first) & 1)); }
-};
 
 struct Env {
   const AttnArgs& a;
   TilesCtl& C;
   __device__ __forceinline__ bool wait(unsigned long long& bar, uint32_t parity) const {
     return attn_wait(bar, parity, &C.abort, a.timeout_ns, a.status);
+  }
+};
+
+// The items, one after the other, as a warp reads them.  They also come when a copy
+// has not landed, so that every output is written.
+struct Reader {
+  const Env E;
+  uint32_t n = 0;
+  __device__ __forceinline__ explicit Reader(const Env& e) : E(e) {}
+  __device__ __forceinline__ const Item& item() const { return E.C.items[n % NITEMS]; }
+  // waits for the next; whether there is one
+  __device__ __forceinline__ bool get() {
+    unsigned long long& bar = E.C.i_full[n % NITEMS];
+    const uint32_t parity = (n / NITEMS) & 1u;
+    if (!__all_sync(0xffffffffu, mbar_try_wait(attn_bar(bar), parity)))
+      __all_sync(0xffffffffu, mbar_wait_for(attn_bar(bar), parity, 4 * E.a.timeout_ns, E.a.status));
+    return item().live;
+  }
+  // has read it
+  __device__ __forceinline__ void done() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(attn_bar(E.C.i_empty[n % NITEMS]));
+    ++n;
+  }
+  __device__ __forceinline__ void skip_rest() {
+    while (get()) done();
   }
 };
 
@@ -125,20 +145,23 @@ struct Ring {
   __device__ __forceinline__ Ring(const AttnArgs& a_, TilesCtl& C, const CUtensorMap* map_, uint32_t smem_, int first)
       : a(a_), E{a_, C}, map(map_), smem(smem_), full(C.full + first), empty(C.empty + first), br(a_.box_rows),
         box((int)(threadIdx.x & 31) % (TK / a_.box_rows)), half((int)(threadIdx.x & 31) / (TK / a_.box_rows)) {}
-  __device__ __forceinline__ void begin(const Walk& w) {
-    pages.begin(a.p.s.table + w.b * a.p.s.ld_table, max(w.key0(), w.keys.lo) >> a.page_shift,
-                (w.keys.hi - 1) >> a.page_shift);
+  int lo, hi, h;  // of the item
+  __device__ __forceinline__ void begin(const Item& it) {
+    lo = it.lo;
+    hi = it.hi;
+    h = it.h;
+    pages.begin(a.p.s.table + it.b * a.p.s.ld_table, max(it.from * TK, lo) >> a.page_shift, (hi - 1) >> a.page_shift);
   }
   // The boxes of the tile at `key`: whether this lane has one, of which page; all of them.
   bool mine;
   int id, slot0;
   uint32_t bytes;
-  __device__ __forceinline__ void locate(const Walk& w, int key) {
+  __device__ __forceinline__ void locate(int key) {
     const int k = key + box * br;
-    mine = half < DH && k + br > w.keys.lo && k < w.keys.hi;
+    mine = half < DH && k + br > lo && k < hi;
     slot0 = k & (a.p.c.kv.page_size - 1);
-    pages.advance(max(key, w.keys.lo) >> a.page_shift);
-    id = pages.at(min(max(k, w.keys.lo), w.keys.hi - 1) >> a.page_shift);
+    pages.advance(max(key, lo) >> a.page_shift);
+    id = pages.at(min(max(k, lo), hi - 1) >> a.page_shift);
     bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * (uint32_t)br * 128u;
     if (mine && (id < 0 || id >= a.p.c.kv.n_pages)) {
       atomicOr(a.status, (unsigned)MOE_STATUS_BAD_PAGE);
@@ -155,12 +178,12 @@ struct Ring {
     return true;
   }
   // The boxes into the slot; `bar` hears of them.
-  __device__ __forceinline__ void copy(const Walk& w, unsigned long long& bar) {
+  __device__ __forceinline__ void copy(unsigned long long& bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(attn_bar(bar), bytes);
     __syncwarp();
     if (mine)
-      tma_load_4d(smem + st * Cfg<DH>::SLOT + (uint32_t)half * HALF + (uint32_t)(box * br) * 128u, map, half * 64, slot0, w.h,
-                  id, attn_bar(bar));
+      tma_load_4d(smem + st * Cfg<DH>::SLOT + (uint32_t)half * HALF + (uint32_t)(box * br) * 128u, map, half * 64, slot0, h, id,
+                  attn_bar(bar));
   }
   // Copies in flight land before the block can exit: each slot's last one (its full
   // barrier's phase flips with every use, as `par` does from the second use on).
@@ -171,19 +194,71 @@ struct Ring {
   }
 };
 
+// The walk's item, by a whole warp (each lane finds the same).
+__device__ __forceinline__ void tell(const AttnArgs& a, const AttnPlan& plan, const Walk& w, Item& it) {
+  const bool lead = (threadIdx.x & 31) == 0;
+  if (!w.live) {
+    if (lead) it.live = 0;
+    return;
+  }
+  Item x;
+  x.live = 1;
+  x.tok0 = w.q.row0;
+  x.pos0 = w.q.pos0;
+  x.len = w.q.len;
+  x.row0 = w.row0();
+  x.b = w.b;
+  x.h = w.h;
+  x.lo = w.keys.lo;
+  x.hi = w.keys.hi;
+  x.from = w.key0() / TK;
+  x.steps = w.key_steps();
+  x.whole = w.whole();
+  x.slot = w.skip ? 0 : 1;
+  x.c0 = x.n = 0;
+  if (!x.whole) x.n = AttnCut<Work::SNAP>::parts(plan, w.begin(), w.end(), &x.c0);
+  x.split = w.rows() <= TR;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    Half& t = x.half[s];
+    t.row0 = x.split ? 0 : s * TR;
+    t.rows = min(w.rows() - t.row0, TR);
+    t.first = 0;
+    t.last = -1;
+    const AttnRange g = attn_range(a.p, w.q, a.group, x.row0 + t.row0, x.row0 + t.row0 + t.rows);
+    t.lo = g.lo;
+    t.hi = g.hi;
+    if (g.hi <= g.lo) continue;
+    t.first = max(g.lo / TK, x.from) + (x.split ? s : 0);
+    t.last = min((g.hi - 1) / TK, x.from + x.steps - 1);
+    if (x.split && ((t.last - t.first) & 1)) --t.last;
+  }
+  if (lead) it = x;
+}
+
 template <int DH>
 __device__ void run_k(const AttnArgs& a, TilesCtl& C, uint32_t ring) {
   Ring<DH, Cfg<DH>::NK> K(a, C, &a.map_k, ring, 0);
   bool ok = true;
-  for (Walk w(a.p, a.group, C.plan); ok && w.live; w.next()) {
+  uint32_t n = 0;
+  for (Walk w(a.p, a.group, C.plan);; w.next()) {
+    const uint32_t e = n % NITEMS;
+    if (n >= NITEMS) mbar_wait_for(attn_bar(C.i_empty[e]), (n / NITEMS - 1) & 1u, 4 * a.timeout_ns, a.status);
+    __syncwarp();
+    tell(a, C.plan, w, C.items[e]);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(attn_bar(C.i_full[e]));
+    ++n;
+    if (!w.live) break;
     const int steps = w.key_steps();
-    if (!steps) continue;
-    K.begin(w);
-    for (int j = 0; j < steps; ++j) {
-      K.locate(w, w.key0() + j * TK);
+    if (!steps || !ok) continue;
+    const Item& it = C.items[e];  // stays until this warp overwrites it
+    K.begin(it);
+    const int from = w.key0();
+    for (int j = 0; ok && j < steps; ++j) {
+      K.locate(from + j * TK);
       ok = K.next_slot();
-      if (!ok) break;
-      K.copy(w, K.full[K.st]);
+      if (ok) K.copy(K.full[K.st]);
     }
   }
   K.drain();
@@ -194,16 +269,15 @@ __device__ void run_k(const AttnArgs& a, TilesCtl& C, uint32_t ring) {
 // of then hold what comes next in memory, or zeros, which concerns nobody.  Else
 // piece by piece, rows and values that there are none of as zeros.
 template <int DH>
-__device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, const Tile& T, uint32_t q_smem,
-                                       unsigned long long& full) {
-  const int lane = threadIdx.x & 31, D = a.p.c.kv.head_dim;
+__device__ __forceinline__ void copy_q(const AttnArgs& a, const Item& it, int s, uint32_t q_smem, unsigned long long& full) {
+  const int lane = threadIdx.x & 31, D = a.p.c.kv.head_dim, first = it.row0 + it.half[s].row0, rows = it.half[s].rows;
   if (a.q_map) {
     if (lane == 0) {
       mbar_arrive_expect_tx(attn_bar(full), Cfg<DH>::SLOT);
-      const int tok = w.q.row0 + (w.row0() + T.row0) / a.group;
+      const int tok = it.tok0 + a.group.token(first);
 #pragma unroll
       for (int half = 0; half < DH; ++half)
-        tma_load_3d(q_smem + half * HALF, &a.map_q, half * 64, w.h * a.group, tok, attn_bar(full));
+        tma_load_3d(q_smem + half * HALF, &a.map_q, half * 64, it.h * a.group.n, tok, attn_bar(full));
     }
     __syncwarp();
     return;
@@ -216,9 +290,9 @@ __device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, const T
 #pragma unroll 1
   for (int r0 = 0; r0 < TR; r0 += 32) {
     // each lane finds one of 32 rows
-    const int r = r0 + lane, row = w.row0() + T.row0 + r, tok = row / a.group;
-    const long long at = (w.q.row0 + tok) * a.p.ldq + (long long)(w.h * a.group + row - tok * a.group) * D;
-    const long long off = r < T.rows ? at : -1;
+    const int r = r0 + lane, row = first + r, tok = a.group.token(row);
+    const long long at = (it.tok0 + tok) * a.p.ldq + (long long)(it.h * a.group.n + row - tok * a.group.n) * D;
+    const long long off = r < rows ? at : -1;
 #pragma unroll 4
     for (int i = 0; i < 32; i += RPI) {
       const long long o = __shfl_sync(0xffffffffu, off, i + rr);
@@ -239,10 +313,10 @@ __device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, const T
 // that hold some that they see: zeros, whatever the pages hold there.
 struct Edge {
   int from[2], to[2];
-  __device__ __forceinline__ Edge(int key0, const AttnRange& keys) {
-    to[0] = keys.lo - key0;
+  __device__ __forceinline__ Edge(int key0, int lo, int hi) {
+    to[0] = lo - key0;
     from[0] = to[0] & ~15;
-    from[1] = keys.hi - key0;
+    from[1] = hi - key0;
     to[1] = (from[1] + 15) & ~15;
   }
   __device__ __forceinline__ bool has(int side) const { return from[side] >= 0 && to[side] <= TK && from[side] < to[side]; }
@@ -269,31 +343,30 @@ __device__ void run_qv(const AttnArgs& a, TilesCtl& C, uint32_t q_smem, uint8_t*
   const int lane = threadIdx.x & 31;
   uint32_t uses[2] = {}, edges = 0;
   bool ok = true, flying = false;  // flying: a copy that `landed` was to hear of
-  for (Walk w(a.p, a.group, C.plan); ok && w.live; w.next()) {
-    const int steps = w.key_steps();
-    if (!steps) continue;
+  Reader items(E);
+  for (; items.get(); items.done()) {
+    const Item& it = items.item();
+    if (!it.steps || !ok) continue;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const Tile T(a, w, s);
-      if (!T.any() || !ok) continue;
+      if (!ok || it.half[s].last < it.half[s].first) continue;
       ok = E.wait(C.q_empty[s], (uses[s] & 1u) ^ 1u);  // passes at once the first time
-      if (!ok) break;
+      if (!ok) continue;
       ++uses[s];
-      copy_q<DH>(a, w, T, q_smem + (uint32_t)s * Cfg<DH>::SLOT, C.q_full[s]);
+      copy_q<DH>(a, it, s, q_smem + (uint32_t)s * Cfg<DH>::SLOT, C.q_full[s]);
     }
-    if (!ok) break;
-    V.begin(w);
-    for (int j = 0; j < steps; ++j) {
-      const int key = w.key0() + j * TK;
-      V.locate(w, key);
+    V.begin(it);
+    for (int j = 0; ok && j < it.steps; ++j) {
+      const int key = (it.from + j) * TK;
+      V.locate(key);
       ok = V.next_slot();
       if (!ok) break;
-      const Edge e(key, w.keys);
+      const Edge e(key, it.lo, it.hi);
       if (!e.has(0) && !e.has(1)) {
-        V.copy(w, V.full[V.st]);
+        V.copy(V.full[V.st]);
         continue;
       }
-      V.copy(w, C.landed);
+      V.copy(C.landed);
       ok = E.wait(C.landed, edges++ & 1u);
       if (!ok) {
         flying = true;
@@ -339,44 +412,46 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q, uint32_t k,
   }
 }
 
-// The key tiles of all items of the run, and what one row tile does with each.
+// The key tiles of all items of the run, and what one half does with each.
 struct Steps {
-  const AttnArgs& a;
+  Reader items;
   const int s;
-  Walk w;
-  Tile T;
-  int k, end;
+  int k, end, lo, hi, first, last, split;
   bool live;
-  __device__ __forceinline__ Steps(const AttnArgs& a_, const AttnPlan& plan, int s_)
-      : a(a_), s(s_), w(a_.p, a_.group, plan), T(a_, w, s_) {
-    item();
-  }
+  __device__ __forceinline__ Steps(const Env& E, int s_) : items(E), s(s_) { item(); }
   __device__ __forceinline__ void item() {
-    while (w.live && !w.key_steps()) w.next();
-    live = w.live;
-    if (!live) return;
-    T = Tile(a, w, s);
-    k = w.key0() / TK;
-    end = k + w.key_steps();
+    while (true) {
+      live = items.get();
+      if (!live) return;
+      const Item& it = items.item();
+      const int steps = it.steps;
+      k = it.from;
+      end = k + steps;
+      lo = it.half[s].lo;
+      hi = it.half[s].hi;
+      first = it.half[s].first;
+      last = it.half[s].last;
+      split = it.split;
+      items.done();
+      if (steps) return;
+    }
   }
   __device__ __forceinline__ void next() {
-    if (++k < end) return;
-    w.next();
-    item();
+    if (++k == end) item();
   }
 };
 
-// A row tile's weights against a value tile, in steps of 16 keys that any row sees.
+// Weights against a value tile, in steps of 16 keys that any row sees.
 struct Product {
   int from, to;
   bool active, first, last;
   __device__ __forceinline__ explicit Product(const Steps& t) {
     const int key0 = t.k * TK;
-    active = t.T.has(t.k);
-    first = t.k == t.T.first;
-    last = t.k == t.T.last;
-    from = max(t.T.keys.lo - key0, 0) / 16;
-    to = (min(t.T.keys.hi - key0, TK) + 15) / 16;
+    active = t.k >= t.first && t.k <= t.last && !(t.split && ((t.k - t.first) & 1));
+    first = t.k == t.first;
+    last = t.k == t.last;
+    from = max(t.lo - key0, 0) / 16;
+    to = (min(t.hi - key0, TK) + 15) / 16;
   }
 };
 
@@ -395,7 +470,8 @@ __device__ __forceinline__ void turn_end(uint32_t* turn) { atomicExch(turn, 0u);
 // Every slot is waited for and given back, also where this row tile has no use for
 // it: a wait that left one out could take the phase before for done.
 template <int DH, bool BF, int S>
-__device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, uint32_t tmem_, uint32_t ring_, uint32_t q_) {
+__device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, Steps& t, uint32_t tmem_, uint32_t ring_,
+                                             uint32_t q_) {
   constexpr int NK = Cfg<DH>::NK, NV = Cfg<DH>::NV;
   const Env E{a, C};
   const uint32_t tmem = uniform(tmem_), ring = uniform(ring_), q = uniform(desc_lo(q_ + S * Cfg<DH>::SLOT));
@@ -419,7 +495,6 @@ __device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, uin
     umma_commit(attn_bar(C.s_full[S]));
     if (P.last) umma_commit(attn_bar(C.q_empty[S]));
   };
-  Steps t(a, C.plan, S);
   if (!t.live) return;
   Product P(t);
   if (!full(0)) return;
@@ -607,59 +682,30 @@ __device__ __forceinline__ float4* part_values(float* part, int row, int d) {
   return reinterpret_cast<float4*>(part + 2 * R) + (d / 4) * R + row;
 }
 
-// Eight values of a row, rounded, of each of four 8-value pieces; the four threads
-// of a quad trade theirs, so that each writes a piece of every row of the quad and
-// they write 64 bytes side by side.
-__device__ __forceinline__ void quad_transpose(uint4 (&x)[4]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int b = 1; b < 4; b <<= 1) {
-    const bool up = lane & b;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i & b) continue;
-      // keeps piece (i | own bit), gives the other away
-      uint4 give = up ? x[i] : x[i | b];
-      give.x = __shfl_xor_sync(0xffffffffu, give.x, b);
-      give.y = __shfl_xor_sync(0xffffffffu, give.y, b);
-      give.z = __shfl_xor_sync(0xffffffffu, give.z, b);
-      give.w = __shfl_xor_sync(0xffffffffu, give.w, b);
-      if (up) x[i] = give;
-      else x[i | b] = give;
-    }
-  }
-}
-
-// 32 values of this thread's row from value c0 on, times inv, out of the row tile's
-// rows that there are; by whole warps.  off: where each row's output begins, -1 for none.
+// 32 values of a row from value c0 on, times inv (a row that saw nothing, or scores of
+// -inf alone: zeros).
 template <bool BF>
-__device__ __forceinline__ void store_32(const AttnArgs& a, long long off, int c0, const float (&f)[32], float inv) {
-  const int lane = threadIdx.x & 31, D = a.p.c.kv.head_dim;
-  uint4 x[4];
+__device__ __forceinline__ void store_32(uint16_t* out, int c0, int D, const float (&f)[32], float inv) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // a row that saw nothing, or scores of -inf alone: zeros
     const float* g = f + 8 * i;
-    x[i].x = inv == 0.f ? 0u : attn_pack2<BF>(g[0] * inv, g[1] * inv);
-    x[i].y = inv == 0.f ? 0u : attn_pack2<BF>(g[2] * inv, g[3] * inv);
-    x[i].z = inv == 0.f ? 0u : attn_pack2<BF>(g[4] * inv, g[5] * inv);
-    x[i].w = inv == 0.f ? 0u : attn_pack2<BF>(g[6] * inv, g[7] * inv);
-  }
-  quad_transpose(x);  // now piece lane & 3 of the quad's rows
-  const int d = c0 + 8 * (lane & 3);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long o = __shfl_sync(0xffffffffu, off, (lane & ~3) + i);
-    if (o >= 0 && d < D) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.p.out) + o + d) = x[i];
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (inv != 0.f) {
+      x.x = attn_pack2<BF>(g[0] * inv, g[1] * inv);
+      x.y = attn_pack2<BF>(g[2] * inv, g[3] * inv);
+      x.z = attn_pack2<BF>(g[4] * inv, g[5] * inv);
+      x.w = attn_pack2<BF>(g[6] * inv, g[7] * inv);
+    }
+    if (c0 + 8 * i < D) *reinterpret_cast<uint4*>(out + c0 + 8 * i) = x;
   }
 }
 
 // Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left; this thread's row.
 template <bool BF>
-__device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int row, bool there, long long off, float* lse) {
+__device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int row, uint16_t* out, float* lse) {
   const int D = a.p.c.kv.head_dim;
   auto part = [&](int x) { return reinterpret_cast<float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot); };
-  auto ml = [&](int x) { return there ? __ldcg(reinterpret_cast<const float2*>(part(x)) + row) : make_float2(-INFINITY, 0.f); };
+  auto ml = [&](int x) { return __ldcg(reinterpret_cast<const float2*>(part(x)) + row); };
   float m = -INFINITY, l = 0.f;
 #pragma unroll 4
   for (int x = 0; x < n; ++x) m = fmaxf(m, ml(x).x);
@@ -678,7 +724,7 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int r
       float4 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v[i] = there && d0 + 4 * i < D ? __ldcg(part_values(part(x), row, d0 + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[i] = d0 + 4 * i < D ? __ldcg(part_values(part(x), row, d0 + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
       const float2 y = ml(x);
       const float f = y.y == 0.f ? 0.f : exp2_fast(y.x - ref);  // (0: nothing seen)
 #pragma unroll
@@ -689,9 +735,9 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int r
         acc[4 * i + 3] = fmaf(f, v[i].w, acc[4 * i + 3]);
       }
     }
-    store_32<BF>(a, off, d0, acc, inv);
+    store_32<BF>(out, d0, D, acc, inv);
   }
-  if (there && lse) *lse = attn_lse<BF>(m, l);
+  if (lse) *lse = attn_lse<BF>(m, l);
 }
 
 template <int DH, bool BF>
@@ -702,29 +748,17 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
   const uint32_t ts = tmem + lanes + (uint32_t)s * 128u, to = tmem + lanes + 256u + (uint32_t)(s * DH * 64);
   uint32_t us = 0, uo = 0;  // uses of s_full and o_full
   bool ok = true;
-  Walk& w = *reinterpret_cast<Walk*>(C.walk[threadIdx.x >> 5]);
-  const bool lead = (threadIdx.x & 31) == 0;
-  if (lead) new (&w) Walk(a.p, a.group, C.plan);
-  __syncwarp();
-  auto next = [&] {
-    __syncwarp();
-    if (lead) w.next();
-    __syncwarp();
-  };
-  for (; w.live; next()) {
-    int lo = 0, hi = INT_MAX;
-    int first, last, step;
-    {
-      const Tile T(a, w, s);
-      first = T.first;
-      last = T.last;
-      step = T.step;
-      if (r < T.rows) {
-        const int row = w.row0() + T.row0 + r;  // of the sequence
-        const AttnRange g = attn_range(a.p, w.q, a.group, row, row + 1);
-        lo = g.lo;
-        hi = g.hi;
-      }
+  Reader items(E);
+  for (; items.get(); items.done()) {
+    const Item& it = items.item();
+    const Half& t = it.half[s];
+    const int step = it.split ? 2 : 1, first = t.first, last = t.last;
+    int lo = 0, hi = INT_MAX;  // what the row sees
+    if (r < t.rows) {
+      const int row = it.row0 + t.row0 + r;  // of the sequence
+      const AttnRange g = attn_range(a.p, AttnSeq{0, 0, it.len, it.pos0}, a.group, row, row + 1);
+      lo = g.lo;
+      hi = g.hi;
     }
     const bool some = first <= last;
     float m = -INFINITY, l = 0.f;
@@ -739,14 +773,11 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
       ok = ok && E.wait(C.o_full[s], uo++ & 1u);
       tc_fence_after();
     }
-    const Tile T(a, w, s);
-    const bool there = r < T.rows;
-    const int row = w.row0() + T.row0 + r;
     if (!ok) l = NAN;
     // With one row tile the second half hands what it has to the first.
     float f0 = 1.f, f1 = 0.f;
     bool other = false;
-    if (T.split) {
+    if (it.split) {
       if (s == 1) {
         C.hand[r] = make_float2(m, l);
         tc_fence_before();
@@ -760,50 +791,51 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
       }
       named_bar_sync(3, NSOFT);
       if (s == 1) continue;
-      other = Tile(a, w, 1).any();
+      other = it.half[1].first <= it.half[1].last;
       const float top = fmaxf(m, m1), ref = top == -INFINITY ? 0.f : top;
       f0 = l == 0.f ? 0.f : exp2_fast(m - ref);
       f1 = l1 == 0.f ? 0.f : exp2_fast(m1 - ref);
       l = f0 * l + f1 * l1;
       m = top;
     }
-    const bool whole = w.whole();
-    float* part = reinterpret_cast<float*>(a.part + (2 * (size_t)blockIdx.x + (w.skip ? 0 : 1)) * a.slot);
-    const int pr = T.row0 + r;
-    const int tok = row / a.group, hd = w.h * a.group + row - tok * a.group;
-    const long long t = w.q.row0 + tok;
-    const long long off = there ? t * a.p.ldo + (long long)hd * D : -1;
-    float* lse = a.p.lse ? a.p.lse + t * a.p.ld_lse + hd : nullptr;
+    const bool there = r < t.rows, whole = it.whole;
+    float* part = reinterpret_cast<float*>(a.part + (2 * (size_t)blockIdx.x + it.slot) * a.slot);
+    const int pr = t.row0 + r, row = it.row0 + pr;
+    const int tok = a.group.token(row), hd = it.h * a.group.n + row - tok * a.group.n;
+    uint16_t* out = static_cast<uint16_t*>(a.p.out) + (it.tok0 + tok) * a.p.ldo + (long long)hd * D;
+    float* lse = a.p.lse ? a.p.lse + (it.tok0 + tok) * a.p.ld_lse + hd : nullptr;
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32) {
+      uint32_t o[32];
       float f[32];
-      {
-        uint32_t o[32];
-        if (some) {
-          tmem_ld32(to + (uint32_t)c0, o);
-          tmem_wait_ld32(o);
-        }
+      if (some) {
+        tmem_ld32(to + (uint32_t)c0, o);
+        tmem_wait_ld32(o);
+      }
+      const bool zero = !some || f0 == 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) f[j] = !some || f0 == 0.f ? 0.f : f0 * __uint_as_float(o[j]);
-        if (other) {
-          tmem_ld32(to + (uint32_t)(c0 + DH * 64), o);
-          tmem_wait_ld32(o);
+      for (int j = 0; j < 32; ++j) f[j] = zero ? 0.f : f0 * __uint_as_float(o[j]);
+      if (other) {
+        tmem_ld32(to + (uint32_t)(c0 + DH * 64), o);
+        tmem_wait_ld32(o);
+        if (f1 != 0.f) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] += f1 == 0.f ? 0.f : f1 * __uint_as_float(o[j]);
+          for (int j = 0; j < 32; ++j) f[j] += f1 * __uint_as_float(o[j]);
         }
       }
       if (!ok) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) f[j] = NAN;
       }
-      if (whole) {
-        store_32<BF>(a, off, c0, f, inv);
+      if (there && whole) {
+        store_32<BF>(out, c0, D, f, inv);
       } else if (there) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4)
           if (c0 + j < D) *part_values(part, pr, c0 + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
       }
+      __syncwarp();
     }
     if (some) warp_arrive(C.o_free[s]);
     if (other) warp_arrive(C.o_free[1]);
@@ -812,20 +844,18 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
       else if (lse) *lse = attn_lse<BF>(m, l);
     }
     if (!whole) {
-      int c0;
-      const int n = AttnCut<Work::SNAP>::parts(C.plan, w.begin(), w.end(), &c0);
       named_bar_sync(1 + s, TR);
       if (r == 0) {
         __threadfence();
-        unsigned* count = a.count + 2 * c0 + s;
-        const bool last = atomicAdd(count, 1u) == (unsigned)(n - 1);
+        unsigned* count = a.count + 2 * it.c0 + s;
+        const bool last = atomicAdd(count, 1u) == (unsigned)(it.n - 1);
         if (last) *count = 0u;
         C.last[s] = last;
       }
       named_bar_sync(1 + s, TR);
       if (C.last[s]) {
         __threadfence();
-        join_row<BF>(a, c0, n, pr, there, off, lse);
+        if (there) join_row<BF>(a, it.c0, it.n, pr, out, lse);
       }
       named_bar_sync(1 + s, TR);  // `last` has been read
     }
@@ -855,6 +885,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
       mbar_init(attn_bar(C.done[i]), 1);
     }
     mbar_init(attn_bar(C.landed), 1);
+    for (int i = 0; i < NITEMS; ++i) {
+      mbar_init(attn_bar(C.i_full[i]), 1);
+      mbar_init(attn_bar(C.i_empty[i]), ITEM_READERS);
+    }
     C.abort = C.turn = 0u;
     fence_mbar_init();
   }
@@ -876,8 +910,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
     } else if (warp == W_V) {
       run_qv<DH>(a, C, smem_u32(sm), ring + Cfg<DH>::NK * Cfg<DH>::SLOT);
     } else {
-      if (warp == W_MMA) run_products<DH, BF, 0>(a, C, tmem, smem_u32(ring), smem_u32(sm));
-      else run_products<DH, BF, 1>(a, C, tmem, smem_u32(ring), smem_u32(sm));
+      Steps t(Env{a, C}, warp - W_MMA);
+      if (warp == W_MMA) run_products<DH, BF, 0>(a, C, t, tmem, smem_u32(ring), smem_u32(sm));
+      else run_products<DH, BF, 1>(a, C, t, tmem, smem_u32(ring), smem_u32(sm));
+      if (t.live) t.items.skip_rest();  // a wait ran out
       __syncwarp();
       if (elect_one()) umma_commit(attn_bar(C.done[warp - W_MMA]));  // after every product of this thread
     }
