@@ -460,12 +460,15 @@ struct Product {
 // scores come at the end of all of them and both softmaxes run while the tensor
 // cores have nothing (4200 cycles a key tile).  Only the order depends on it, so
 // that a warp goes ahead without it rather than wait for long.
-__device__ __forceinline__ void turn_begin(uint32_t* turn) {
+__device__ __forceinline__ void turn_begin(uint32_t turn) {
 #pragma unroll 1
-  for (int i = 0; i < 256; ++i)
-    if (atomicCAS(turn, 0u, 1u) == 0u) return;
+  for (int i = 0; i < 256; ++i) {
+    uint32_t was;
+    asm volatile("atom.shared.cas.b32 %0, [%1], 0, 1;" : "=r"(was) : "r"(turn) : "memory");
+    if (was == 0u) return;
+  }
 }
-__device__ __forceinline__ void turn_end(uint32_t* turn) { atomicExch(turn, 0u); }
+__device__ __forceinline__ void turn_end(uint32_t turn) { asm volatile("st.shared.u32 [%0], 0;" ::"r"(turn) : "memory"); }
 
 // Every slot is waited for and given back, also where this row tile has no use for
 // it: a wait that left one out could take the phase before for done.
@@ -476,6 +479,7 @@ __device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, Ste
   const Env E{a, C};
   const uint32_t tmem = uniform(tmem_), ring = uniform(ring_), q = uniform(desc_lo(q_ + S * Cfg<DH>::SLOT));
   const uint32_t id_qk = umma_idesc(TK, BF), id_pv = umma_idesc((a.p.c.kv.head_dim + 15) & ~15, BF) | (1u << 16);
+  const uint32_t turn = smem_u32(&C.turn);
   const uint32_t sp = tmem + S * 128u, o = tmem + 256u + S * (DH * 64);
   const int ksteps = (a.p.c.kv.head_dim + 15) / 16 + (DH == 2 ? 0 : 4);
   uint32_t ks = 0, vs = 0, par = 0;             // slots; the phase of each
@@ -524,7 +528,7 @@ __device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, Ste
       if (!E.wait(C.p_full[S], up++ & 1u)) return;
       tc_fence_after();
       if (elect_one()) {
-        turn_begin(&C.turn);
+        turn_begin(turn);
         if (P.from == 0 && P.to == TK / 16) {
           umma_f16_ta(o, sp, desc(v), id_pv, P.first ? 0u : 1u);
 #pragma unroll
@@ -541,7 +545,7 @@ __device__ __forceinline__ void run_products(const AttnArgs& a, TilesCtl& C, Ste
           umma_commit(attn_bar(C.empty[ks]));
         }
         umma_commit(attn_bar(C.empty[NK + vs]));
-        turn_end(&C.turn);
+        turn_end(turn);
       }
     } else if (elect_one()) {
       mbar_arrive(attn_bar(C.empty[NK + vs]));
