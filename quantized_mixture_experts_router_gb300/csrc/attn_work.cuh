@@ -119,7 +119,6 @@ struct AttnWork {
 
 // The cut, and where this block's run begins and ends.
 struct AttnPlan {
-  long long sum[32], items[32];
   long long total;           // places of the line
   int runs;                  // blocks that have work
   long long base[2], per_head[2];  // of the sequences in which the run begins and ends: place, a head's places
@@ -144,9 +143,9 @@ struct AttnCut {
   }
 };
 
-// By all NT threads of the block; ends with a barrier.
+// By all NT threads of the block; ends with a barrier.  scratch: two numbers a warp.
 template <class W, int NT>
-__device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan& S) {
+__device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan& S, long long (*scratch)[2]) {
   using Cut = AttnCut<W::SNAP>;
   constexpr int NWARP = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -165,14 +164,14 @@ __device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan&
     items += __shfl_xor_sync(0xffffffffu, items, d);
   }
   if (lane == 0) {
-    S.sum[warp] = mine;
-    S.items[warp] = items;
+    scratch[warp][0] = mine;
+    scratch[warp][1] = items;
   }
   __syncthreads();
   long long total = 0, all = 0;
   for (int w = 0; w < NWARP; ++w) {
-    total += S.sum[w];
-    all += S.items[w];
+    total += scratch[w][0];
+    all += scratch[w][1];
   }
   __syncthreads();
   const int runs = (int)min((long long)gridDim.x, max(total / W::MIN_RUN, all));
@@ -194,12 +193,12 @@ __device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan&
         const long long v = __shfl_up_sync(0xffffffffu, s, d);
         if (lane >= d) s += v;
       }
-      if (lane == 31) S.sum[warp] = s;
+      if (lane == 31) scratch[warp][0] = s;
       __syncthreads();
       long long before = base;
       for (int w = 0; w < NWARP; ++w) {
-        if (w < warp) before += S.sum[w];
-        base += S.sum[w];
+        if (w < warp) before += scratch[w][0];
+        base += scratch[w][0];
       }
       __syncthreads();
       const long long at = before + s - c;

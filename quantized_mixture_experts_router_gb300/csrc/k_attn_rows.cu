@@ -46,8 +46,8 @@ template <int DH>
 struct Shared {
   alignas(1024) uint8_t ring[Cfg<DH>::NS * Cfg<DH>::STAGE];
   alignas(1024) uint8_t q[2][DH * QHALF];  // queries of this item and the next
-  float o[NW][R][Cfg<DH>::OPITCH];
-  float ml[NW][R][2];
+  alignas(16) float o[NW][R][Cfg<DH>::OPITCH];
+  alignas(16) float ml[NW][R][2];
   unsigned long long full[Cfg<DH>::NS], empty[Cfg<DH>::NS];
   unsigned long long q_full[2], q_empty[2];
   AttnPlan plan;
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_rows(const __grid_constant__ A
     fence_mbar_init();
   }
   grid_wait();
-  attn_plan<Work, NTHR>(a.p, a.group, S.plan);
+  attn_plan<Work, NTHR>(a.p, a.group, S.plan, reinterpret_cast<long long(*)[2]>(S.ml));
   if (threadIdx.x < NW * 32) run_rows<DH, BF>(a, S);
   else run_copies<DH>(a, S, (int)(threadIdx.x >> 5) - NW);
 }

@@ -32,7 +32,7 @@ using Work = AttnWork<R, TK, 3, 6, 6>;
 using Walk = AttnWalk<Work>;
 constexpr int NSOFT = 256, NTHR = 384;
 // Registers a thread: 168 at launch; the softmax warps take what the others leave.
-constexpr int REG_LAUNCH = 168, REG_SOFT = 200, REG_REST = 104;
+constexpr int REG_LAUNCH = 168, REG_SOFT = 184, REG_REST = 136;
 static_assert(NSOFT * REG_SOFT + (NTHR - NSOFT) * REG_REST <= NTHR * REG_LAUNCH, "register shares exceed the launch's");
 constexpr uint32_t HALF = TK * 128;  // 64 values of 128 keys or rows
 
@@ -76,7 +76,7 @@ struct TilesCtl {
   unsigned long long done[2];
   uint32_t tmem, abort, last[2], turn;
   Item items[NITEMS];
-  float2 hand[TR];                              // (maximum, sum) of a row that the second half hands to the first
+  alignas(16) float2 hand[TR];                              // (maximum, sum) of a row that the second half hands to the first
   AttnPlan plan;
 };
 template <int DH>
@@ -581,24 +581,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// The loads so far are complete; r, which one of them fills, is read behind this.
-__device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
-               :
-               : "memory");
-  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
-      "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
-      : "memory");
-}
+// The loads so far are complete.
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Two f32 at once.
 __device__ __forceinline__ uint64_t pack_f32(float x, float y) {
@@ -621,25 +605,95 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+__device__ __forceinline__ void tmem_ld16_later(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Of 16 scores, those outside from .. end - 1 as -inf.
+template <bool MASKED>
+__device__ __forceinline__ void mask_16(uint32_t (&v)[16], int from, int end) {
+  if (MASKED) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < from || j >= end) v[j] = 0xff800000u;
+  }
+}
+
+// The scores at ts, 16 at a time, each time the next 16 on their way.  A rolled loop:
+// unrolled, the warps' instructions come from farther away than they are used (2100
+// cycles a tile of 128 keys where this takes half).
+template <bool MASKED, class F>
+__device__ __forceinline__ void each_16(uint32_t ts, int from, int end, F use) {
+  uint32_t a[16], b[16];
+  tmem_ld16_later(ts, a);
+#pragma unroll 1
+  for (int i = 0; i < TK; i += 32) {
+    tmem_wait_ld();
+    tmem_ld16_later(ts + (uint32_t)i + 16u, b);
+    mask_16<MASKED>(a, from - i, end - i);
+    use(a, i);
+    tmem_wait_ld();
+    tmem_ld16_later(ts + ((uint32_t)i + 32u) % TK, a);  // the last time for nothing, but without a branch
+    mask_16<MASKED>(b, from - i - 16, end - i - 16);
+    use(b, i + 16);
+  }
+  tmem_wait_ld();
+}
+
+// The largest of this thread's row's scores, times c.
+__device__ __forceinline__ float largest(uint32_t ts, float c) {
+  uint32_t v[TK];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32u * i, v + 32 * i);
+  tmem_wait_ld();
+  float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 0; j < TK; j += 2) t[(j / 2) & 3] = fmaxf(fmaxf(t[(j / 2) & 3], __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
+}
+__device__ __forceinline__ float largest_masked(uint32_t ts, int from, int end, float c) {
+  float t = -INFINITY;
+  each_16<true>(ts, from, end, [&](uint32_t (&v)[16], int) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) t = fmaxf(t, __uint_as_float(v[j]));
+  });
+  return t * c;
+}
+
+// exp2(c s - ref) of the scores, packed over them (8 columns over 16 that have been
+// read); their sum.
+template <bool BF, bool MASKED>
+__device__ __forceinline__ float weigh(uint32_t ts, int from, int end, float c, float ref) {
+  const uint64_t c2 = pack_f32(c, c), ref2 = pack_f32(-ref, -ref);
+  uint64_t sum[2] = {0, 0};
+  each_16<MASKED>(ts, from, end, [&](uint32_t (&v)[16], int at) {
+    uint32_t p[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float x, y;
+      unpack_f32(fma2(pack_f32(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), c2, ref2), x, y);
+      x = exp2_fast(x);
+      y = exp2_fast(y);
+      sum[j & 1] = add2(sum[j & 1], pack_f32(x, y));
+      p[j] = attn_pack2<BF>(x, y);
+    }
+    tmem_st8(ts + (uint32_t)at / 2u, p);
+  });
+  float x, y;
+  unpack_f32(add2(sum[0], sum[1]), x, y);
+  return x + y;
+}
+
 // One key tile of this thread's row.
 template <int DH, bool BF>
 __device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, int lo, int hi, float c, bool first, float& m,
                                           float& l) {
-  uint32_t v[TK];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32u * i, v + 32 * i);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) tmem_wait_ld32(v + 32 * i);
   const int from = lo - key0, end = hi - key0;  // of the tile's keys, what the row sees
-  if (__any_sync(0xffffffffu, from > 0 || end < TK)) {
-#pragma unroll
-    for (int j = 0; j < TK; ++j)
-      if (j < from || j >= end) v[j] = 0xff800000u;  // -inf
-  }
-  float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int j = 0; j < TK; j += 2) t[(j / 2) & 3] = fmaxf(fmaxf(t[(j / 2) & 3], __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
-  const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
+  const bool masked = __any_sync(0xffffffffu, from > 0 || end < TK);
+  const float top = masked ? largest_masked(ts, from, end, c) : largest(ts, c);
   const bool rise = top > m + ATTN_SLACK;  // from -inf: by anything
   if (first) {
     m = top;
@@ -651,32 +705,16 @@ __device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, in
 #pragma unroll 1
     for (int i = 0; i < DH * 4; ++i) {
       uint32_t o[16];
-      tmem_ld16(to + 16u * i, reinterpret_cast<float*>(o));
+      tmem_ld16_later(to + 16u * i, o);
+      tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-      tmem_st16(to + 16u * i, o);
+      tmem_st8(to + 16u * i, o);
+      tmem_st8(to + 16u * i + 8u, o + 8);
     }
   }
   const float ref = (m == -INFINITY ? 0.f : m) - ATTN_BIAS<BF>;
-  const uint64_t c2 = pack_f32(c, c), ref2 = pack_f32(-ref, -ref);
-  uint64_t sum[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t p[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float x, y;
-      unpack_f32(fma2(pack_f32(__uint_as_float(v[32 * i + 2 * j]), __uint_as_float(v[32 * i + 2 * j + 1])), c2, ref2), x, y);
-      x = exp2_fast(x);
-      y = exp2_fast(y);
-      sum[j & 1] = add2(sum[j & 1], pack_f32(x, y));
-      p[j] = attn_pack2<BF>(x, y);
-    }
-    tmem_st16(ts + 16u * i, p);
-  }
-  float x, y;
-  unpack_f32(add2(sum[0], sum[1]), x, y);
-  l += x + y;
+  l += masked ? weigh<BF, true>(ts, from, end, c, ref) : weigh<BF, false>(ts, from, end, c, ref);
   tmem_wait_st();
 }
 
@@ -815,14 +853,14 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
       float f[32];
       if (some) {
         tmem_ld32(to + (uint32_t)c0, o);
-        tmem_wait_ld32(o);
+        tmem_wait_ld();
       }
       const bool zero = !some || f0 == 0.f;
 #pragma unroll
       for (int j = 0; j < 32; ++j) f[j] = zero ? 0.f : f0 * __uint_as_float(o[j]);
       if (other) {
         tmem_ld32(to + (uint32_t)(c0 + DH * 64), o);
-        tmem_wait_ld32(o);
+        tmem_wait_ld();
         if (f1 != 0.f) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) f[j] += f1 * __uint_as_float(o[j]);
@@ -898,7 +936,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
   }
   if (warp == 0) tmem_alloc(&C.tmem, 512);
   grid_wait();
-  attn_plan<Work, NTHR>(a.p, a.group, C.plan);
+  attn_plan<Work, NTHR>(a.p, a.group, C.plan, reinterpret_cast<long long(*)[2]>(C.hand));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
