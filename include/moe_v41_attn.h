@@ -81,8 +81,8 @@ typedef struct {
 /* The sequences of a call; the arrays are on the device, so that a captured step
  * serves every length.  New token i of sequence b is row cu_new[b] + i of the
  * call's tensors, and its position is kv_len[b] - n + i, n = cu_new[b + 1] -
- * cu_new[b] of them.  Rows behind the last sequence's belong to nobody: they are
- * not read, and their outputs stay as they were.  A length below 0 counts as 0;
+ * cu_new[b] of them.  Rows behind the last sequence's belong to nobody: what
+ * they hold has no influence, and their outputs stay as they were.  A length below 0 counts as 0;
  * rows from m on are left out. */
 typedef struct {
   int32_t batch;           /* sequences: 0..65536 */
@@ -120,7 +120,9 @@ MOE_API int moe_v41_kv_append(const moe_v41_kv_cfg* kv, const moe_v41_rope_cfg* 
  *  - A token that sees nothing (or only scores of -inf): out 0, lse -inf.
  *  - What lies in slots that none of a sequence's new tokens sees has no
  *    influence, whatever it holds; pages that hold no slot that one of them sees
- *    are not looked up.
+ *    are not looked up.  A key that a token does not see has none on it either;
+ *    but an infinity or a NaN among the values that one new token sees may make
+ *    NaN of the outputs of the sequence's others (a product with weight zero).
  *  - Scores, maxima and sums are f32.  exp(score - maximum) is rounded once to the
  *    cache's type, as the tensor cores take it with the values; outputs are
  *    rounded once more to that type.

@@ -9,7 +9,7 @@
 // sincospi in f32.  Values move eight at a time
 // wherever the head's parts begin at multiples of eight (both halves' vectors in
 // one thread), else one pair at a time.
-#include "attn.h"
+#include "attn_work.cuh"
 
 namespace moe {
 
@@ -25,6 +25,7 @@ struct RopeArgs {
   int units;           // all units of a head
   int heads;           // of a token: queries, keys, values
   int page_shift;
+  AttnGroup per_token, per_head;  // units of a token, of a head
 };
 
 template <class T>
@@ -73,6 +74,15 @@ __device__ __forceinline__ void store_v(T* p, const float (&f)[V]) {
   }
 }
 
+// (cos, sin) of two neighbouring pairs at once.
+__device__ __forceinline__ float4 two(const float2* cs) { return *reinterpret_cast<const float4*>(cs); }
+
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float r = x * c - y * s;
+  y = y * c + x * s;
+  x = r;
+}
+
 // One unit of a head.  cs: the token's (cos, sin) per pair, or NULL for a head
 // that is copied (values).
 template <class IN, class OUT, int V>
@@ -85,12 +95,15 @@ __device__ __forceinline__ void do_unit(const RopeArgs& a, const IN* x, OUT* y, 
       load_v<V>(x + lo, s);
       load_v<V>(x + hi, t);
       if (cs) {
+        if constexpr (V == 1) {
+          turn(s[0], t[0], cs[i].x, cs[i].y);
+        } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float2 c = cs[i + j];
-          const float r = s[j] * c.x - t[j] * c.y;
-          t[j] = t[j] * c.x + s[j] * c.y;
-          s[j] = r;
+          for (int j = 0; j < V; j += 2) {
+            const float4 c = two(cs + i + j);
+            turn(s[j], t[j], c.x, c.y);
+            turn(s[j + 1], t[j + 1], c.z, c.w);
+          }
         }
       }
       store_v<V>(y + lo, s);
@@ -106,12 +119,15 @@ __device__ __forceinline__ void do_unit(const RopeArgs& a, const IN* x, OUT* y, 
         load_v<2 * P>(x + at, s);
       }
       if (cs) {
+        if constexpr (V == 1) {
+          turn(s[0], s[1], cs[u].x, cs[u].y);
+        } else {
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-          const float2 c = cs[P * u + j];
-          const float r = s[2 * j] * c.x - s[2 * j + 1] * c.y;
-          s[2 * j + 1] = s[2 * j + 1] * c.x + s[2 * j] * c.y;
-          s[2 * j] = r;
+          for (int j = 0; j < P; j += 2) {
+            const float4 c = two(cs + P * u + j);
+            turn(s[2 * j], s[2 * j + 1], c.x, c.y);
+            turn(s[2 * j + 2], s[2 * j + 3], c.z, c.w);
+          }
         }
       }
       if constexpr (V == 1) {
@@ -155,7 +171,7 @@ __device__ __forceinline__ int find_sequence(const int* cu, int batch, int t) {
 
 template <class IN, class OUT, int V, bool APPEND>
 __global__ void __launch_bounds__(NTHR) k_rope(const __grid_constant__ RopeArgs a) {
-  extern __shared__ float2 cs[];  // [tokens][pairs]
+  extern __shared__ __align__(16) float2 cs[];  // [tokens][pairs]
   __shared__ Token tok[8];
   const RopeParams& p = a.p;
   const int t0 = (int)blockIdx.x * a.tokens, nt = min(a.tokens, p.m - t0);
@@ -193,10 +209,9 @@ __global__ void __launch_bounds__(NTHR) k_rope(const __grid_constant__ RopeArgs 
     cs[i] = make_float2(cn * p.c.magnitude, (p.c.inverse ? -sn : sn) * p.c.magnitude);
   }
   __syncthreads();
-  const int per_token = a.heads * a.units;
-  for (int i = (int)blockIdx.y * NTHR + threadIdx.x; i < nt * per_token; i += (int)gridDim.y * NTHR) {
-    const int w = i / per_token, r = i - w * per_token;
-    const int h = r / a.units, u = r - h * a.units;
+  for (int i = (int)blockIdx.y * NTHR + threadIdx.x; i < nt * a.per_token.n; i += (int)gridDim.y * NTHR) {
+    const int w = a.per_token.token(i), r = i - w * a.per_token.n;
+    const int h = a.per_head.token(r), u = r - h * a.per_head.n;
     const long long t = t0 + w;
     if (APPEND && !tok[w].live) continue;
     const float2* c = cs + w * a.pairs;
@@ -220,8 +235,10 @@ int launch(const RopeArgs& a, dim3 grid, cudaStream_t s) {
 }
 
 template <class IN, class OUT, bool APPEND>
-int launch_v(const RopeArgs& a, bool vec, dim3 grid, cudaStream_t s) {
-  return vec ? launch<IN, OUT, 8, APPEND>(a, grid, s) : launch<IN, OUT, 1, APPEND>(a, grid, s);
+int launch_v(const RopeArgs& a, int v, dim3 grid, cudaStream_t s) {
+  if constexpr (sizeof(IN) == 2)
+    if (v == 16) return launch<IN, OUT, 16, APPEND>(a, grid, s);
+  return v == 8 ? launch<IN, OUT, 8, APPEND>(a, grid, s) : launch<IN, OUT, 1, APPEND>(a, grid, s);
 }
 
 }  // namespace
@@ -239,8 +256,11 @@ int launch_rope(const RopeParams& p, cudaStream_t s) {
              (!p.heads_q || (fits(p.q, p.ldq) && fits(p.q_out, p.ldo)));
   if (p.heads_q > 1) vec = vec && p.ldq_head % 8 == 0 && p.ldo_head % 8 == 0;
   if (append) vec = vec && fits(p.k, p.ldk) && fits(p.v, p.ldv);
-  const int v = vec ? 8 : 1;
-  a.units_rot = half || !vec ? a.pairs / (half ? v : 1) : c.rot_dim / 8;
+  // 16-bit pairs that are neighbours: 16 values, so that as many bytes are on their way
+  // as with halves (8192 x 32 heads of 128, bf16: 35 us with eight)
+  const bool wide = vec && !half && c.x_type != MOE_T_F32 && c.head_dim % 16 == 0 && c.rot_first % 16 == 0 && c.rot_dim % 16 == 0;
+  const int v = wide ? 16 : vec ? 8 : 1;
+  a.units_rot = half || !vec ? a.pairs / (half ? v : 1) : c.rot_dim / v;
   // in place, what is not rotated stays where it is
   a.units = a.units_rot + (!append && p.q == p.q_out && c.rot_dim ? 0 : (c.head_dim - c.rot_dim) / v);
   if (!append && p.q == p.q_out && !c.rot_dim) return MOE_OK;
@@ -250,23 +270,25 @@ int launch_rope(const RopeParams& p, cudaStream_t s) {
   const long long units = (long long)a.heads * a.units;
   a.tokens = (int)(units >= 512 ? 1 : 1024 / units > 8 ? 8 : 1024 / units);
   while (a.tokens > 1 && (p.m + a.tokens - 1) / a.tokens < 152 * 4) a.tokens /= 2;
+  a.per_token = AttnGroup::of((int)units);
+  a.per_head = AttnGroup::of(a.units);
   const int blocks = (p.m + a.tokens - 1) / a.tokens;
   long long split = (units * a.tokens + NTHR - 1) / NTHR;
   if (split * blocks > 152 * 8) split = blocks >= 152 * 8 ? 1 : (152 * 8 + blocks - 1) / blocks;
   const dim3 grid((unsigned)blocks, (unsigned)(split < 65535 ? split : 65535));
   if (!append) {
-    if (c.x_type == MOE_T_F32) return launch_v<float, float, false>(a, vec, grid, s);
-    if (c.x_type == MOE_T_BF16) return launch_v<__nv_bfloat16, __nv_bfloat16, false>(a, vec, grid, s);
-    return launch_v<__half, __half, false>(a, vec, grid, s);
+    if (c.x_type == MOE_T_F32) return launch_v<float, float, false>(a, v, grid, s);
+    if (c.x_type == MOE_T_BF16) return launch_v<__nv_bfloat16, __nv_bfloat16, false>(a, v, grid, s);
+    return launch_v<__half, __half, false>(a, v, grid, s);
   }
   if (p.out_type == MOE_T_BF16) {
-    if (c.x_type == MOE_T_F32) return launch_v<float, __nv_bfloat16, true>(a, vec, grid, s);
-    if (c.x_type == MOE_T_BF16) return launch_v<__nv_bfloat16, __nv_bfloat16, true>(a, vec, grid, s);
-    return launch_v<__half, __nv_bfloat16, true>(a, vec, grid, s);
+    if (c.x_type == MOE_T_F32) return launch_v<float, __nv_bfloat16, true>(a, v, grid, s);
+    if (c.x_type == MOE_T_BF16) return launch_v<__nv_bfloat16, __nv_bfloat16, true>(a, v, grid, s);
+    return launch_v<__half, __nv_bfloat16, true>(a, v, grid, s);
   }
-  if (c.x_type == MOE_T_F32) return launch_v<float, __half, true>(a, vec, grid, s);
-  if (c.x_type == MOE_T_BF16) return launch_v<__nv_bfloat16, __half, true>(a, vec, grid, s);
-  return launch_v<__half, __half, true>(a, vec, grid, s);
+  if (c.x_type == MOE_T_F32) return launch_v<float, __half, true>(a, v, grid, s);
+  if (c.x_type == MOE_T_BF16) return launch_v<__nv_bfloat16, __half, true>(a, v, grid, s);
+  return launch_v<__half, __half, true>(a, v, grid, s);
 }
 
 }  // namespace moe
