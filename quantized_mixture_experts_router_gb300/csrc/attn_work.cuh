@@ -40,6 +40,21 @@ __device__ __forceinline__ long long attn_div(long long a, long long b) {
   if (((unsigned long long)a | (unsigned long long)b) >> 32) return a / b;
   return (long long)((unsigned)a / (unsigned)b);
 }
+__device__ __forceinline__ long long attn_warp_sum(long long v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+// of this lane's and all lower lanes' values
+__device__ __forceinline__ long long attn_warp_scan(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
 
 // One sequence: its first row, new tokens, cached tokens that can be read, and
 // the first new token's position.
@@ -109,8 +124,7 @@ struct AttnWork {
       const int n = __shfl_sync(0xffffffffu, nt, src);
       long long sum = 0;
       for (int i = lane; i < n; i += 32) sum += cost(p, o, group, i);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      sum = attn_warp_sum(sum);
       if (lane == src) c = sum;
     }
     return c;
@@ -158,17 +172,15 @@ __device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan&
     items += (long long)n * kh;
     if (b0 == 0) first = c;
   }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    mine += __shfl_xor_sync(0xffffffffu, mine, d);
-    items += __shfl_xor_sync(0xffffffffu, items, d);
-  }
+  mine = attn_warp_sum(mine);
+  items = attn_warp_sum(items);
   if (lane == 0) {
     scratch[warp][0] = mine;
     scratch[warp][1] = items;
   }
   __syncthreads();
   long long total = 0, all = 0;
+#pragma unroll
   for (int w = 0; w < NWARP; ++w) {
     total += scratch[w][0];
     all += scratch[w][1];
@@ -187,15 +199,11 @@ __device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan&
     long long base = 0;
     for (int b0 = 0; b0 < batch && base <= x[1]; b0 += NT) {
       const long long c = b0 == 0 ? first : W::seq_cost(p, group, b0 + tid, b0 + tid < batch) * kh;
-      long long s = c;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d) s += v;
-      }
+      const long long s = attn_warp_scan(c);
       if (lane == 31) scratch[warp][0] = s;
       __syncthreads();
       long long before = base;
+#pragma unroll
       for (int w = 0; w < NWARP; ++w) {
         if (w < warp) before += scratch[w][0];
         base += scratch[w][0];
@@ -224,12 +232,7 @@ __device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan&
         for (int i0 = 0; i0 < nt; i0 += 32) {
           const int i = i0 + lane;
           const long long c = i < nt ? W::cost(p, q, group, i) : 0;
-          long long s = c;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d) s += v;
-          }
+          const long long s = attn_warp_scan(c);
           const unsigned past = __ballot_sync(0xffffffffu, rem < s);
           if (past) {
             if (lane == __ffs((int)past) - 1) {
@@ -398,29 +401,53 @@ constexpr float ATTN_SLACK = 8.0f;
 template <bool BF>
 constexpr float ATTN_BIAS = BF ? 0.f : 6.f;
 
+// 2^x; 0 for -inf
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Four values of a row, over n parts of its keys: part i has reference maximum and
 // sum ml(i) and unscaled values o(i).
 struct AttnJoined {
   float m, l;
   float4 o;
 };
-template <class ML, class O>
+template <int U, class ML, class O>
 __device__ __forceinline__ AttnJoined attn_join(int n, ML ml, O o) {
   AttnJoined j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int i = 0; i < n; ++i) j.m = fmaxf(j.m, ml(i).x);
-  const float ref = j.m == -INFINITY ? 0.f : j.m;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float2 v = ml(i);
-    const float4 x = o(i);
-    if (v.y == 0.f) continue;  // nothing seen: its outputs may never have been written
-    float f;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(v.x - ref));
-    j.l += f * v.y;
-    j.o.x += f * x.x;
-    j.o.y += f * x.y;
-    j.o.z += f * x.z;
-    j.o.w += f * x.w;
+#pragma unroll 1
+  for (int x0 = 0; x0 < n; x0 += U) {  // U parts on their way at once
+    float2 v[U];
+    float4 x[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int at = min(x0 + i, n - 1);
+      v[i] = ml(at);
+      x[i] = o(at);
+    }
+    float top = j.m;
+#pragma unroll
+    for (int i = 0; i < U; ++i) top = fmaxf(top, v[i].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float f0 = exp2_fast(j.m - ref);
+    j.m = top;
+    j.l *= f0;
+    j.o.x *= f0;
+    j.o.y *= f0;
+    j.o.z *= f0;
+    j.o.w *= f0;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (x0 + i >= n || v[i].y == 0.f) continue;  // (0: nothing seen, its values may never have been written)
+      const float f = exp2_fast(v[i].x - ref);
+      j.l += f * v[i].y;
+      j.o.x += f * x[i].x;
+      j.o.y += f * x[i].y;
+      j.o.z += f * x[i].z;
+      j.o.w += f * x[i].w;
+    }
   }
   return j;
 }
@@ -441,13 +468,6 @@ __device__ __forceinline__ void attn_store(const AttnArgs& a, int tok0, int h, i
   v.y = attn_pack2<BF>(j.o.z * s, j.o.w * s);
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.p.out) + t * a.p.ldo + (long long)hd * a.p.c.kv.head_dim + d) = v;
   if (d == 0 && a.p.lse) a.p.lse[t * a.p.ld_lse + hd] = attn_lse<BF>(j.m, j.l);
-}
-
-// 2^x; 0 for -inf
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // Box {64 values, rows of a page, 1, 1} of the cache seen as [page][head][slot][value].

@@ -25,7 +25,7 @@ constexpr int NTHR = (NW + NP) * 32;
 // An item costs about as much as six tiles from memory beside its own, a join twice
 // that; a block's warps work on eight tiles at once, so that a run of fewer is no
 // shorter.
-using Work = AttnWork<R, TK, 6, 12, 14>;
+using Work = AttnWork<R, TK, 6, 12, 8>;
 using Walk = AttnWalk<Work>;
 constexpr uint32_t HALF = TK * 128;        // 64 values of a tile's keys
 constexpr uint32_t QHALF = R * 128;        // 64 values of an item's queries
@@ -104,19 +104,20 @@ __device__ __forceinline__ void copy_q(const AttnArgs& a, const Walk& w, uint32_
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full)) : "memory");
 }
 
-// A warp issues one box after the other, about 100 cycles each, which for small
-// pages is more than a tile may take: each copies a quarter of a tile's boxes, those
-// of its half of the keys' or values' widths, or every other page's.
+// Tile u is copying warp u % NP's, which always fills the same stages.  A warp takes
+// some 250 ns a tile, and 100 cycles more for each box of a small page.
 template <int DH>
 __device__ void run_copies(const AttnArgs& a, Shared<DH>& S, int pw) {
   constexpr int NS = Cfg<DH>::NS;
+  static_assert(NS % NP == 0, "a stage is one copying warp's");
   const int lane = threadIdx.x & 31;
   const int br = a.box_rows, nb = TK / br;
-  const int val = pw & 1, half = DH == 2 ? pw >> 1 : 0, box = DH == 2 ? lane : 2 * lane + (pw >> 1);
+  const int box = lane % nb, half = lane / nb % DH, val = lane / nb / DH;
   const uint32_t ring = smem_u32(S.ring);
   const uint32_t dst0 = (uint32_t)(val * DH + half) * HALF + (uint32_t)(box * br) * 128u;
-  uint32_t st = 0, par = 0, used = 0;  // par: the phase of each stage's empty barrier that is waited for next
-  uint32_t items = 0;                  // with keys, so far
+  uint32_t st = (uint32_t)pw, par = 0, used = 0;  // par: the phase of each stage's empty barrier that is waited for next
+  uint32_t u = 0;                                 // tiles of the run so far
+  uint32_t items = 0;                             // with keys, so far
   bool ok = true;
   for (Walk w(a.p, a.group, S.plan); ok && w.live; w.next()) {
     const int steps = w.key_steps();
@@ -124,10 +125,22 @@ __device__ void run_copies(const AttnArgs& a, Shared<DH>& S, int pw) {
     if (items >= 2 && !attn_wait(S.q_empty[items & 1], (items / 2 - 1) & 1u, &S.abort, a.timeout_ns, a.status)) break;
     copy_q<DH>(a, w, smem_u32(S.q[items & 1]), pw, S.q_full[items & 1]);
     ++items;
+    const int first = (int)((uint32_t)(pw + NP - (int)(u % NP)) % NP);  // this warp's first tile of the item
+    u += (uint32_t)steps;
+    if (first >= steps) continue;
     AttnPages pages;
-    int key = w.key0();
+    int key = w.key0() + first * TK;
     pages.begin(a.p.s.table + w.b * a.p.s.ld_table, max(key, w.keys.lo) >> a.page_shift, (w.keys.hi - 1) >> a.page_shift);
-    for (int j = 0; j < steps; ++j, key += TK) {
+    for (int j = first; j < steps; j += NP, key += NP * TK) {
+      const int k = key + box * br;
+      const bool mine = val < 2 && k + br > w.keys.lo && k < w.keys.hi;
+      pages.advance(max(key, w.keys.lo) >> a.page_shift);
+      int id = pages.at(min(max(k, w.keys.lo), w.keys.hi - 1) >> a.page_shift);
+      const unsigned boxes = __ballot_sync(0xffffffffu, mine);
+      if (mine && (id < 0 || id >= a.p.c.kv.n_pages)) {
+        atomicOr(a.status, (unsigned)MOE_STATUS_BAD_PAGE);
+        id = a.p.c.kv.n_pages;  // outside: filled with zeros
+      }
       if ((used >> st) & 1u) {
         if (!attn_wait(S.empty[st], (par >> st) & 1u, &S.abort, a.timeout_ns, a.status)) {
           ok = false;
@@ -136,21 +149,12 @@ __device__ void run_copies(const AttnArgs& a, Shared<DH>& S, int pw) {
         par ^= 1u << st;
       }
       used |= 1u << st;
-      const int k = key + box * br;
-      const bool mine = box < nb && k + br > w.keys.lo && k < w.keys.hi;
-      pages.advance(max(key, w.keys.lo) >> a.page_shift);
-      int id = pages.at(min(max(k, w.keys.lo), w.keys.hi - 1) >> a.page_shift);
-      const unsigned boxes = __ballot_sync(0xffffffffu, mine);
-      if (mine && (id < 0 || id >= a.p.c.kv.n_pages)) {
-        atomicOr(a.status, (unsigned)MOE_STATUS_BAD_PAGE);
-        id = a.p.c.kv.n_pages;  // outside: filled with zeros
-      }
       if (lane == 0) mbar_arrive_expect_tx(attn_bar(S.full[st]), (uint32_t)__popc(boxes) * (uint32_t)br * 128u);
       __syncwarp();
       if (mine)
         tma_load_4d(ring + st * Cfg<DH>::STAGE + dst0, val ? &a.map_v : &a.map_k, half * 64,
                     k & (a.p.c.kv.page_size - 1), w.h, id, attn_bar(S.full[st]));
-      st = st + 1 == NS ? 0 : st + 1;
+      st = st + NP >= NS ? (uint32_t)pw : st + NP;
     }
   }
   // Copies in flight land before the block can exit: each stage's last one (its full
@@ -342,7 +346,7 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
     float* part = reinterpret_cast<float*>(a.part + (2 * (size_t)blockIdx.x + (w.skip ? 0 : 1)) * a.slot);
     for (int i = tid; i < rows * d4; i += NW * 32) {
       const int r = i / d4, d = (i - r * d4) * 4;
-      const AttnJoined v = attn_join(
+      const AttnJoined v = attn_join<1>(
           NW, [&](int x) { return *reinterpret_cast<const float2*>(S.ml[x][r]); },
           [&](int x) { return *reinterpret_cast<const float4*>(&S.o[x][r][d]); });
       if (whole) {
@@ -368,16 +372,10 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
         auto at = [&](int x) {
           return reinterpret_cast<const float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot);
         };
-        float2* ml = reinterpret_cast<float2*>(&S.o[0][0][0]);  // [n][rows]
-        for (int i = tid; i < n * rows; i += NW * 32) {
-          const int x = i / rows;
-          ml[i] = __ldcg(reinterpret_cast<const float2*>(at(x)) + i - x * rows);
-        }
-        named_bar_sync(1, NW * 32);
         for (int i = tid; i < rows * d4; i += NW * 32) {
           const int r = i / d4, d = (i - r * d4) * 4;
-          const AttnJoined v = attn_join(
-              n, [&](int x) { return ml[x * rows + r]; },
+          const AttnJoined v = attn_join<4>(
+              n, [&](int x) { return __ldcg(reinterpret_cast<const float2*>(at(x)) + r); },
               [&](int x) { return __ldcg(reinterpret_cast<const float4*>(at(x) + R * 2 + r * D + d)); });
           attn_store<BF>(a, w.q.row0, w.h, w.row0() + r, d, v);
         }
@@ -394,7 +392,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_rows(const __grid_constant__ A
   grid_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < Cfg<DH>::NS; ++i) {
-      mbar_init(attn_bar(S.full[i]), NP);
+      mbar_init(attn_bar(S.full[i]), 1);
       mbar_init(attn_bar(S.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
