@@ -126,8 +126,9 @@ MOE_API int moe_v41_kv_append(const moe_v41_kv_cfg* kv, const moe_v41_rope_cfg* 
  *  - Scores, maxima and sums are f32.  exp(score - maximum) is rounded once to the
  *    cache's type, as the tensor cores take it with the values; outputs are
  *    rounded once more to that type.
- *  - A page outside 0 .. n_pages - 1, or beyond the table, reads as zeros and sets
- *    MOE_STATUS_BAD_PAGE in the workspace.
+ *  - A page outside 0 .. n_pages - 1 reads as zeros, and what lies beyond the table
+ *    (kv_len > max_pages * page_size) is not seen; either sets MOE_STATUS_BAD_PAGE
+ *    in the workspace.
  *  - A wait that runs out (a copy that never lands) sets MOE_STATUS_TIMEOUT;
  *    what it concerns is NaN, and the workspace is ready for the next call.
  *  - Results do not depend on the order in which blocks run. */
@@ -136,7 +137,7 @@ typedef struct {
   int32_t heads;   /* query heads: a multiple of kv_heads, up to 4096 */
   int32_t causal;
   int32_t window;  /* 0: all; else causal, 1..2^30 */
-  float scale;     /* > 0, finite */
+  float scale;     /* 1e-36..1e36 */
 } moe_v41_attn_cfg;
 
 /* Bytes of workspace (0 for an invalid configuration): whatever the number of

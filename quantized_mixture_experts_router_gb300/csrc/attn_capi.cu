@@ -53,7 +53,8 @@ int check_attn(const moe_v41_attn_cfg* c) {
   if (rc) return rc;
   if (c->heads < 1 || c->heads > 4096 || c->heads % c->kv.kv_heads) return MOE_ERR_ARG;
   if (c->window < 0 || c->window > (1 << 30) || (c->window > 0 && !c->causal)) return MOE_ERR_ARG;
-  if (!(c->scale > 0.0f) || !std::isfinite(c->scale)) return MOE_ERR_ARG;
+  // scale log2 e is a normal number
+  if (!(c->scale >= 1.0e-36f) || !(c->scale <= 1.0e36f)) return MOE_ERR_ARG;
   return MOE_OK;
 }
 

@@ -159,7 +159,8 @@ struct AttnCut {
 
 // By all NT threads of the block; ends with a barrier.  scratch: two numbers a warp.
 template <class W, int NT>
-__device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan& S, long long (*scratch)[2]) {
+__device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan& S, long long (*scratch)[2],
+                          unsigned* status) {
   using Cut = AttnCut<W::SNAP>;
   constexpr int NWARP = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -167,6 +168,8 @@ __device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan&
   long long mine = 0, first = 0, items = 0;  // all of this thread's sequences; the first
   for (int b0 = 0; b0 < batch; b0 += NT) {
     int n = 0;
+    if (blockIdx.x == 0 && b0 + tid < batch && p.s.kv_len[b0 + tid] > p.s.max_pages * p.c.kv.page_size)
+      atomicOr(status, (unsigned)MOE_STATUS_BAD_PAGE);  // a length beyond the table
     const long long c = W::seq_cost(p, group, b0 + tid, b0 + tid < batch, &n) * kh;
     mine += c;
     items += (long long)n * kh;

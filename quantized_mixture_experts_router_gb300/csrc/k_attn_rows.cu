@@ -11,7 +11,6 @@
 // m16n8k16: with at most 16 rows the 128-row tiles of tcgen05 would be mostly
 // empty, and p would have to pass through tensor memory; here it goes from the
 // accumulators of the first product straight into the operands of the second.
-//
 #include "attn_work.cuh"
 
 namespace moe {
@@ -142,7 +141,9 @@ __device__ void run_copies(const AttnArgs& a, Shared<DH>& S, int pw) {
         id = a.p.c.kv.n_pages;  // outside: filled with zeros
       }
       if ((used >> st) & 1u) {
-        if (!attn_wait(S.empty[st], (par >> st) & 1u, &S.abort, a.timeout_ns, a.status)) {
+        // a stage that was given back because its copies have not landed is not used again
+        if (!attn_wait(S.empty[st], (par >> st) & 1u, &S.abort, a.timeout_ns, a.status) ||
+            *(volatile uint32_t*)&S.abort) {
           ok = false;
           break;
         }
@@ -282,13 +283,14 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
   const uint32_t ring = smem_u32(S.ring);
   uint32_t u = 0;      // tiles of the run so far; tile u is warp u % NW's, in stage u % NS
   uint32_t items = 0;  // with keys, so far
+  bool ok = true;      // until a wait runs out: then every phase from there on is in doubt
   for (Walk w(a.p, a.group, S.plan); w.live; w.next()) {
     const int steps = w.key_steps(), rows = w.rows();
     uint32_t j = (uint32_t)(warp + NW - (int)(u % NW)) % NW;  // this warp's first tile of the item
     if (j < (uint32_t)steps) {
       uint32_t qf[DH * 4][4];
       float o[DH * 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {};
-      bool ok = attn_wait(S.q_full[items & 1], (items / 2) & 1u, &S.abort, a.timeout_ns, a.status);
+      ok = attn_wait(S.q_full[items & 1], (items / 2) & 1u, &S.abort, a.timeout_ns, a.status) && ok;
       load_q<DH>(smem_u32(S.q[items & 1]), qf);
       int lo[2], hi[2], lo_all = 0, hi_all = 0;
 #pragma unroll
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_rows(const __grid_constant__ A
     fence_mbar_init();
   }
   grid_wait();
-  attn_plan<Work, NTHR>(a.p, a.group, S.plan, reinterpret_cast<long long(*)[2]>(S.ml));
+  attn_plan<Work, NTHR>(a.p, a.group, S.plan, reinterpret_cast<long long(*)[2]>(S.ml), a.status);
   if (threadIdx.x < NW * 32) run_rows<DH, BF>(a, S);
   else run_copies<DH>(a, S, (int)(threadIdx.x >> 5) - NW);
 }

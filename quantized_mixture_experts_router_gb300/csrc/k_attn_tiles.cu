@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
   }
   if (warp == 0) tmem_alloc(&C.tmem, 512);
   grid_wait();
-  attn_plan<Work, NTHR>(a.p, a.group, C.plan, reinterpret_cast<long long(*)[2]>(C.hand));
+  attn_plan<Work, NTHR>(a.p, a.group, C.plan, reinterpret_cast<long long(*)[2]>(C.hand), a.status);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

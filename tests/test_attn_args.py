@@ -167,7 +167,7 @@ def _attn(Q, cfg=None, seqs=None, **kw):  # noqa: F811
 
 @pytest.mark.parametrize("bad", [dict(heads=0), dict(heads=3), dict(heads=4098), dict(window=-1), dict(window=(1 << 30) + 1),
                                  dict(window=5, causal=False), dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN),
-                                 dict(scale=INF)], ids=str)
+                                 dict(scale=INF), dict(scale=9e-37), dict(scale=1.1e36)], ids=str)
 def test_attention_refuses_a_bad_configuration(Q, bad):  # noqa: F811
     cfg = Q.make_attn_cfg(_kv(Q), **{**dict(heads=4), **bad})
     assert _attn(Q, cfg) == Q.MOE_ERR_ARG

@@ -485,6 +485,21 @@ def test_attention_of_bad_pages(Q, max_new):  # noqa: F811
     assert torch.equal(a.out[1:41], got[1:41])
 
 
+@pytest.mark.parametrize("max_new", [1, 5000])
+def test_attention_of_a_length_beyond_the_table(Q, max_new):  # noqa: F811
+    """what has no entry in the table is not seen, and the status says so"""
+    a = Attn(Q, [3, 40], [100, 64], 4, 2, 64, page=16, max_new=max_new)
+    more = 16 * a.cols + 30
+    a.ints[1][0] = more
+    a.call()
+    assert Q.moe_v41_read_status(a.ws, clear=True) == Q.MOE_STATUS_BAD_PAGE
+    a.kv[0] = 16 * a.cols                                             # the three tokens lie behind these, and see all of them
+    ok = torch.ones((3, a.kv[0]), dtype=torch.bool, device="cuda")
+    visible = a.visible
+    a.visible = lambda b: ok if b == 0 else visible(b)
+    a.check()
+
+
 # ------------------------------------------------------------------ append
 
 APPEND = [
