@@ -605,38 +605,45 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-__device__ __forceinline__ void tmem_ld16_later(uint32_t taddr, uint32_t* r) {
+__device__ __forceinline__ void tmem_ld16_later(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-// The scores at ts, 16 at a time, each time the next 16 on their way.  A rolled loop:
-// unrolled, the warps' instructions come from farther away than they are used (2100
-// cycles a tile of 128 keys where this takes half).
+// The scores at ts, 16 at a time, each time the next 16 on their way.  How far the loop
+// is unrolled decides: beyond 32 scores the warps' instructions come from farther away
+// than they are used (a prompt's chunk, 2048 tokens over 10000: 262 us with 16 scores a
+// turn, 256 with 32, 250 with 64; seven prompts of up to 2500: 108, 108, 116 us).
 template <class F>
 __device__ __forceinline__ void each_16(uint32_t ts, F use) {
-  uint32_t a[16];
+  uint32_t a[16], b[16];
   tmem_ld16_later(ts, a);
 #pragma unroll 1
-  for (int i = 0; i < TK; i += 16) {
+  for (int i = 0; i < TK; i += 32) {
     tmem_wait_ld();
+    tmem_ld16_later(ts + (uint32_t)i + 16u, b);
     use(a, i);
-    tmem_ld16_later(ts + ((uint32_t)i + 16u) % TK, a);  // the last time for nothing, but without a branch
+    tmem_wait_ld();
+    tmem_ld16_later(ts + ((uint32_t)i + 32u) % TK, a);  // the last time for nothing, but without a branch
+    use(b, i + 16);
   }
   tmem_wait_ld();
 }
 
 // The largest of this thread's row's scores, times c.
 __device__ __forceinline__ float largest(uint32_t ts, float c) {
-  uint32_t v[TK];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32u * i, v + 32 * i);
-  tmem_wait_ld();
+  uint32_t v[64];
   float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+  for (int i = 0; i < TK; i += 64) {
+    tmem_ld32(ts + (uint32_t)i, v);
+    tmem_ld32(ts + (uint32_t)i + 32u, v + 32);
+    tmem_wait_ld();
 #pragma unroll
-  for (int j = 0; j < TK; j += 2) t[(j / 2) & 3] = fmaxf(fmaxf(t[(j / 2) & 3], __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
+    for (int j = 0; j < 64; j += 2) t[(j / 2) & 3] = fmaxf(fmaxf(t[(j / 2) & 3], __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
+  }
   return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;
 }
 
@@ -662,85 +669,28 @@ __device__ __forceinline__ float total(const uint64_t (&sum)[2]) {
   return x + y;
 }
 
-// The weights that a warp has written (columns ts .. ts + n - 1, two a column; what lies
-// behind them up to a multiple of 16 has been read) and the n_out outputs at `to`, times f.
-template <bool BF>
-__device__ __forceinline__ void rescale(uint32_t ts, int n, uint32_t to, int n_out, float f) {
-  tmem_wait_st();
+// Scores of keys outside from .. end - 1 become -inf, where the warp's rows do not see
+// all 16 of some: a pass of its own over the few columns that need it, so that every tile
+// runs through the same instructions (seven prompts: 109 us; with masks in both passes,
+// whose instructions are rarer and come from farther away, 122).
+__device__ __forceinline__ void hide(uint32_t ts, int from, int end) {
 #pragma unroll 1
-  for (int i = 0; i < n; i += 16) {
-    uint32_t p[16];
-    tmem_ld16_later(ts + (uint32_t)i, p);
-    tmem_wait_ld();
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float2 x = BF ? __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&p[j]))
-                          : __half22float2(*reinterpret_cast<__half2*>(&p[j]));
-      p[j] = attn_pack2<BF>(x.x * f, x.y * f);
+  for (int i = 0; i < TK; i += 16) {
+    if (!__any_sync(0xffffffffu, from > i || end < i + 16)) continue;
+    // bit j: score i + j is seen
+    const uint32_t lo = (uint32_t)min(max(from - i, 0), 16), hi = (uint32_t)min(max(end - i, 0), 16);
+    const uint32_t seen = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+    uint32_t v[16];
+    if (__any_sync(0xffffffffu, seen)) {
+      tmem_ld16_later(ts + (uint32_t)i, v);
+      tmem_wait_ld();
     }
-    tmem_st8(ts + (uint32_t)i, p);
-    tmem_st8(ts + (uint32_t)i + 8u, p + 8);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (!(seen >> j & 1u)) v[j] = 0xff800000u;
+    tmem_st8(ts + (uint32_t)i, v);
+    tmem_st8(ts + (uint32_t)i + 8u, v + 8);
   }
-#pragma unroll 1
-  for (int i = 0; i < n_out; i += 16) {
-    uint32_t o[16];
-    tmem_ld16_later(to + (uint32_t)i, o);
-    tmem_wait_ld();
-#pragma unroll
-    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-    tmem_st8(to + (uint32_t)i, o);
-    tmem_st8(to + (uint32_t)i + 8u, o + 8);
-  }
-}
-
-// Scores 16 at a time, those outside from .. end - 1 as -inf; their maximum.
-__device__ __forceinline__ float mask_16(uint32_t (&v)[16], int from, int end) {
-  float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (j < from || j >= end) v[j] = 0xff800000u;
-#pragma unroll
-  for (int j = 0; j < 16; j += 2)
-    t[(j / 2) & 3] = fmaxf(fmaxf(t[(j / 2) & 3], __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
-  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-}
-
-// A key tile of which this thread's row sees keys from .. end - 1, or another of the
-// warp's rows not all: in one pass, 16 scores at a time their maximum, then
-// exp2(c s - m), packed over scores that have been read.  Masking twice, in a pass for
-// the maximum and one for the weights, takes longer (seven prompts: 122 us, with this
-// 112); for whole tiles, whose masking costs nothing, one pass does (2048 tokens over
-// 10000: 265 us in two, 307 in one).  An item's first tile has the pass for the maximum:
-// where one key outweighs the others, its weight is 1, without a rounding.
-template <int DH, bool BF>
-__device__ __forceinline__ void masked_tile(uint32_t ts, uint32_t to, int from, int end, float c, bool first, float& m,
-                                            float& l) {
-  if (first) {
-    float top = -INFINITY;
-    each_16(ts, [&](uint32_t (&v)[16], int i) { top = fmaxf(top, mask_16(v, from - i, end - i)); });
-    m = top * c;
-  }
-  uint64_t sum[2] = {pack_f32(l, 0.f), 0};
-  each_16(ts, [&](uint32_t (&v)[16], int i) {
-    const float top = mask_16(v, from - i, end - i) * c;
-    const bool rise = top > m + ATTN_SLACK;  // from -inf: by anything
-    if (__any_sync(0xffffffffu, rise)) {
-      // weights of this tile are scaled by a power of two, so that none is rounded twice
-      const float next = !rise ? m : i && m != -INFINITY ? m + ceilf(top - m) : top;
-      const float f = rise ? exp2_fast(m - next) : 1.f;
-      m = next;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float x, y;
-        unpack_f32(sum[j], x, y);
-        sum[j] = pack_f32(x * f, y * f);
-      }
-      rescale<BF>(ts, i / 2, to, DH * 64, f);
-    }
-    const float ref = (m == -INFINITY ? 0.f : m) - ATTN_BIAS<BF>;
-    weigh_16<BF>(v, ts + (uint32_t)i / 2u, c, ref, sum);
-  });
-  l = total(sum);
   tmem_wait_st();
 }
 
@@ -749,10 +699,7 @@ template <int DH, bool BF>
 __device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, int lo, int hi, float c, bool first, float& m,
                                           float& l) {
   const int from = lo - key0, end = hi - key0;  // of the tile's keys, what the row sees
-  if (__any_sync(0xffffffffu, from > 0 || end < TK)) {
-    masked_tile<DH, BF>(ts, to, from, end, c, first, m, l);
-    return;
-  }
+  if (__any_sync(0xffffffffu, from > 0 || end < TK)) hide(ts, from, end);
   const float top = largest(ts, c);
   const bool rise = top > m + ATTN_SLACK;  // from -inf: by anything
   if (first) {
@@ -761,7 +708,16 @@ __device__ __forceinline__ void soft_tile(uint32_t ts, uint32_t to, int key0, in
     const float next = rise ? top : m, f = rise ? exp2_fast(m - next) : 1.f;
     m = next;
     l *= f;
-    rescale<BF>(ts, 0, to, DH * 64, f);
+#pragma unroll 1
+    for (int i = 0; i < DH * 4; ++i) {
+      uint32_t o[16];
+      tmem_ld16_later(to + 16u * i, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+      tmem_st8(to + 16u * i, o);
+      tmem_st8(to + 16u * i + 8u, o + 8);
+    }
   }
   const float ref = (m == -INFINITY ? 0.f : m) - ATTN_BIAS<BF>;
   uint64_t sum[2] = {0, 0};
