@@ -147,6 +147,7 @@ MOE_API size_t moe_v41_attn_workspace_bytes(const moe_v41_attn_cfg* cfg);
 
 /* q and out [m, heads, head_dim] of kv.type (pitches ldq, a multiple of 8 with q
  * 16-B aligned, and ldo, the same), lse f32 [m, heads] (pitch ld_lse) or NULL.
+ * out overlaps nothing that the call reads.
  * max_new: about how many new tokens the longest sequence has; it chooses the
  * kernel, and results are right for any.  m * heads <= 2^30. */
 MOE_API int moe_v41_paged_attention(const moe_v41_attn_cfg* cfg, const moe_v41_seqs* seqs, int m, int max_new,
