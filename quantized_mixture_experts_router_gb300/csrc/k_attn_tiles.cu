@@ -751,41 +751,51 @@ __device__ __forceinline__ void store_32(uint16_t* out, int c0, int D, const flo
 }
 
 // Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left; this thread's row.
+// It takes what its rounds of loads that wait for one another take: maxima, sums and
+// values of two parts are on their way at once.
 template <bool BF>
 __device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int row, uint16_t* out, float* lse) {
   const int D = a.p.c.kv.head_dim;
   auto part = [&](int x) { return reinterpret_cast<float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot); };
-  auto ml = [&](int x) { return __ldcg(reinterpret_cast<const float2*>(part(x)) + row); };
   float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-  for (int x = 0; x < n; ++x) m = fmaxf(m, ml(x).x);
-  const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-  for (int x = 0; x < n; ++x) {
-    const float2 v = ml(x);
-    l += v.y == 0.f ? 0.f : exp2_fast(v.x - ref) * v.y;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
   for (int d0 = 0; d0 < D; d0 += 32) {
     float acc[32] = {};
-#pragma unroll 2
-    for (int x = 0; x < n; ++x) {
-      float4 v[8];
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll 1
+    for (int x0 = 0; x0 < n; x0 += 2) {
+      float2 y[2];
+      float4 v[2][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = d0 + 4 * i < D ? __ldcg(part_values(part(x), row, d0 + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float2 y = ml(x);
-      const float f = y.y == 0.f ? 0.f : exp2_fast(y.x - ref);  // (0: nothing seen)
+      for (int x = 0; x < 2; ++x) {
+        const bool is = x0 + x < n;
+        float* at = part(is ? x0 + x : x0);
+        y[x] = is ? __ldcg(reinterpret_cast<const float2*>(at) + row) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[4 * i] = fmaf(f, v[i].x, acc[4 * i]);
-        acc[4 * i + 1] = fmaf(f, v[i].y, acc[4 * i + 1]);
-        acc[4 * i + 2] = fmaf(f, v[i].z, acc[4 * i + 2]);
-        acc[4 * i + 3] = fmaf(f, v[i].w, acc[4 * i + 3]);
+        for (int i = 0; i < 8; ++i)
+          v[x][i] = is && d0 + 4 * i < D ? __ldcg(part_values(at, row, d0 + 4 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      const float top = fmaxf(m, fmaxf(y[0].x, y[1].x)), ref = top == -INFINITY ? 0.f : top;
+      const float w = exp2_fast(m - ref);
+      m = top;
+      l *= w;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) acc[j] *= w;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float f = y[x].y == 0.f ? 0.f : exp2_fast(y[x].x - ref);  // (0: nothing seen)
+        l += f * y[x].y;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc[4 * i] = fmaf(f, v[x][i].x, acc[4 * i]);
+          acc[4 * i + 1] = fmaf(f, v[x][i].y, acc[4 * i + 1]);
+          acc[4 * i + 2] = fmaf(f, v[x][i].z, acc[4 * i + 2]);
+          acc[4 * i + 3] = fmaf(f, v[x][i].w, acc[4 * i + 3]);
+        }
       }
     }
-    store_32<BF>(out, d0, D, acc, inv);
+    store_32<BF>(out, d0, D, acc, l == 0.f ? 0.f : 1.f / l);
   }
   if (lse) *lse = attn_lse<BF>(m, l);
 }
