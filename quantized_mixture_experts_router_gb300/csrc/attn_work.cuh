@@ -85,12 +85,13 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, const AttnS
   return g;
 }
 
-template <int R_, int TK_, int OVER_, int SNAP_, int MIN_RUN_>
+template <int R_, int TK_, int OVER_, int SNAP_, int MIN_RUN_, int JOIN_>
 struct AttnWork {
   static constexpr int R = R_, TK = TK_;
   static constexpr int OVER = OVER_;        // places of an item beside its key tiles
   static constexpr int SNAP = SNAP_;        // an item is cut this far from its ends at the least
   static constexpr int MIN_RUN = MIN_RUN_;  // more blocks take part only if each has so many places, or an item
+  static constexpr int JOIN = JOIN_;        // what a part costs who joins them, in hundredths of a place; 0: nothing
   static_assert(OVER >= 1 && SNAP > OVER, "every part of an item has a key tile");
   static __device__ __forceinline__ int row_tiles(const AttnSeq& q, const AttnGroup& group) {
     return q.n > 0 ? (q.n * group.n - 1) / R + 1 : 0;
@@ -189,7 +190,10 @@ __device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan&
     all += scratch[w][1];
   }
   __syncthreads();
-  const int runs = (int)min((long long)gridDim.x, max(total / W::MIN_RUN, all));
+  long long least = W::MIN_RUN;
+  // an item of T places in n parts takes T / n and then n joins: least where n^2 is T over the join's places
+  if (W::JOIN && total > 0) least = max(least, (long long)sqrtf((float)total / (float)all * (W::JOIN * 0.01f)));
+  const int runs = (int)min((long long)gridDim.x, max(attn_div(total, least), all));
   if (tid == 0) {
     S.total = total;
     S.runs = runs;

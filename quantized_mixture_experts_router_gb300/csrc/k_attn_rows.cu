@@ -24,7 +24,7 @@ constexpr int NTHR = (NW + NP) * 32;
 // An item costs about as much as six tiles from memory beside its own, a join twice
 // that; a block's warps work on eight tiles at once, so that a run of fewer is no
 // shorter.
-using Work = AttnWork<R, TK, 6, 12, 8>;
+using Work = AttnWork<R, TK, 6, 12, 8, 0>;
 using Walk = AttnWalk<Work>;
 constexpr uint32_t HALF = TK * 128;        // 64 values of a tile's keys
 constexpr uint32_t QHALF = R * 128;        // 64 values of an item's queries

@@ -27,8 +27,11 @@ namespace {
 
 constexpr int R = ATTN_TILES_TILE, TK = ATTN_TILES_KEYS, TR = 128;
 constexpr int W_MMA = 8, W_K = 10, W_V = 11;
-// An item costs about as much as three key tiles beside its own, and so does a join.
-using Work = AttnWork<R, TK, 3, 6, 6>;
+// An item costs about as much as three key tiles beside its own, and so does a join (with
+// two or four, a window of 1000 took 59 and 55 us instead of 54).  Parts of a join cost
+// half a tile each: 100 tokens over 30000 of two key heads, 69 us, 92 with as many runs
+// as blocks; eight over 60000 of one, 52 and 66.
+using Work = AttnWork<R, TK, 3, 6, 6, 50>;
 using Walk = AttnWalk<Work>;
 constexpr int NSOFT = 256, NTHR = 384;
 // Registers a thread: 168 at launch; the softmax warps take what the others leave.
@@ -750,16 +753,18 @@ __device__ __forceinline__ void store_32(uint16_t* out, int c0, int D, const flo
   }
 }
 
-// Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left; this thread's row.
+// Joins the n parts of a row tile that runs c0 .. c0 + n - 1 have left: a row's values
+// first .. first + 31, and every `step` on.
 // It takes what its rounds of loads that wait for one another take: maxima, sums and
 // values of two parts are on their way at once.
 template <bool BF>
-__device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int row, uint16_t* out, float* lse) {
+__device__ __forceinline__ void join_row(const AttnArgs& a, int c0, int n, int row, int first, int step, uint16_t* out,
+                                         float* lse) {
   const int D = a.p.c.kv.head_dim;
   auto part = [&](int x) { return reinterpret_cast<float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot); };
   float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-  for (int d0 = 0; d0 < D; d0 += 32) {
+  for (int d0 = first; d0 < D; d0 += step) {
     float acc[32] = {};
     m = -INFINITY;
     l = 0.f;
@@ -860,10 +865,18 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
     }
     const bool there = r < t.rows, whole = it.whole;
     float* part = reinterpret_cast<float*>(a.part + (2 * (size_t)blockIdx.x + it.slot) * a.slot);
-    const int pr = t.row0 + r, row = it.row0 + pr;
-    const int tok = a.group.token(row), hd = it.h * a.group.n + row - tok * a.group.n;
-    uint16_t* out = static_cast<uint16_t*>(a.p.out) + (it.tok0 + tok) * a.p.ldo + (long long)hd * D;
-    float* lse = a.p.lse ? a.p.lse + (it.tok0 + tok) * a.p.ld_lse + hd : nullptr;
+    const int pr = t.row0 + r;
+    // where a row of the item goes
+    struct Place {
+      uint16_t* out;
+      float* lse;
+    };
+    auto place = [&](int at) {
+      const int row = it.row0 + at, tok = a.group.token(row), hd = it.h * a.group.n + row - tok * a.group.n;
+      return Place{static_cast<uint16_t*>(a.p.out) + (it.tok0 + tok) * a.p.ldo + (long long)hd * D,
+                   a.p.lse ? a.p.lse + (it.tok0 + tok) * a.p.ld_lse + hd : nullptr};
+    };
+    const Place mine = place(pr);
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32) {
@@ -889,7 +902,7 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
         for (int j = 0; j < 32; ++j) f[j] = NAN;
       }
       if (there && whole) {
-        store_32<BF>(out, c0, D, f, inv);
+        store_32<BF>(mine.out, c0, D, f, inv);
       } else if (there) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4)
@@ -901,7 +914,7 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
     if (other) warp_arrive(C.o_free[1]);
     if (there) {
       if (!whole) *reinterpret_cast<float2*>(part + 2 * pr) = make_float2(m, l);
-      else if (lse) *lse = attn_lse<BF>(m, l);
+      else if (mine.lse) *mine.lse = attn_lse<BF>(m, l);
     }
     if (!whole) {
       named_bar_sync(1 + s, TR);
@@ -915,7 +928,13 @@ __device__ void run_softmax(const AttnArgs& a, TilesCtl& C, uint32_t tmem, int s
       named_bar_sync(1 + s, TR);
       if (C.last[s]) {
         __threadfence();
-        if (there) join_row<BF>(a, it.c0, it.n, pr, out, lse);
+        // where the rows are but one or two warps', the others take their share of the values
+        const int warps = (t.rows + 31) / 32, shares = 4 / warps, share = (r >> 5) / warps;
+        const int at = (r >> 5) % warps * 32 + (r & 31);
+        if (at < t.rows && share < shares) {
+          const Place to = place(t.row0 + at);
+          join_row<BF>(a, it.c0, it.n, t.row0 + at, share * 32, shares * 32, to.out, share ? nullptr : to.lse);
+        }
       }
       named_bar_sync(1 + s, TR);  // `last` has been read
     }
