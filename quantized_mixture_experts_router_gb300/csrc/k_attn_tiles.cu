@@ -18,6 +18,12 @@
 // operand whose values, not keys, are contiguous.  A row's output is rescaled only
 // when its maximum has grown by more than 2^8 over the reference, which its own
 // thread then does in place.
+//
+// Bound by the softmax between a tile's two products: at 2048 tokens over 10000 (32 heads
+// over 8 key heads of 128, 301 GFLOP) 251 us, 1200 TFLOP/s, the tensor pipe busy 53% of
+// the time; by bytes where the rows are few (five tokens of 16 sequences over 3000 to
+// 7400: 79 us, 4.8 TB/s); by what an item takes beside its tiles (first copies, the end,
+// joins) where items are short (seven prompts of up to 2500: 104 us).
 #include "attn_work.cuh"
 #include "tc.cuh"
 
@@ -34,7 +40,8 @@ constexpr int W_MMA = 8, W_K = 10, W_V = 11;
 using Work = AttnWork<R, TK, 3, 6, 6, 50>;
 using Walk = AttnWalk<Work>;
 constexpr int NSOFT = 256, NTHR = 384;
-// Registers a thread: 168 at launch; the softmax warps take what the others leave.
+// Registers a thread: 168 at launch; the softmax warps take what the others leave (200
+// and 104 take the same time).
 constexpr int REG_LAUNCH = 168, REG_SOFT = 184, REG_REST = 136;
 static_assert(NSOFT * REG_SOFT + (NTHR - NSOFT) * REG_REST <= NTHR * REG_LAUNCH, "register shares exceed the launch's");
 constexpr uint32_t HALF = TK * 128;  // 64 values of 128 keys or rows
@@ -461,8 +468,9 @@ struct Product {
 // The tensor cores take the products of both issuing warps in turn.  Held while one
 // row tile's are issued, so that they do not mix with the other's: mixed, both tiles'
 // scores come at the end of all of them and both softmaxes run while the tensor
-// cores have nothing (4200 cycles a key tile).  Only the order depends on it, so
-// that a warp goes ahead without it rather than wait for long.
+// cores have nothing (2048 tokens over 10000: 294 us, 264 with the turn when it was
+// added).  Only the order depends on it, so that a warp goes ahead without it rather
+// than wait for long.
 __device__ __forceinline__ void turn_begin(uint32_t turn) {
 #pragma unroll 1
   for (int i = 0; i < 256; ++i) {

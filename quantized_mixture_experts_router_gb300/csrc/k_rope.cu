@@ -6,9 +6,10 @@
 // tokens; a thread of it computes a pair's sine and cosine once per token into
 // shared memory, and all its heads use them.  The angle is reduced in 64 bits:
 // pos f / 2 pi minus its nearest whole number (exact to 2^-52 of the turns), then
-// sincospi in f32.  Values move eight at a time
-// wherever the head's parts begin at multiples of eight (both halves' vectors in
-// one thread), else one pair at a time.
+// sincospi in f32.  Values move eight at a time (16-bit neighbours 16) wherever the
+// head's parts begin at multiples of it (both halves' vectors in one thread), else one
+// pair at a time.  One row of 32 heads of 128 takes 1.8 us, a launch; 4096 rows of 16
+// heads of 192, f32 (101 MB), 17 us, 88% of a copy's rate.
 #include "attn_work.cuh"
 
 namespace moe {
@@ -257,7 +258,7 @@ int launch_rope(const RopeParams& p, cudaStream_t s) {
   if (p.heads_q > 1) vec = vec && p.ldq_head % 8 == 0 && p.ldo_head % 8 == 0;
   if (append) vec = vec && fits(p.k, p.ldk) && fits(p.v, p.ldv);
   // 16-bit pairs that are neighbours: 16 values, so that as many bytes are on their way
-  // as with halves (8192 x 32 heads of 128, bf16: 35 us with eight)
+  // as with halves (8192 x 32 heads of 128, bf16: 32 us, 35 with eight)
   const bool wide = vec && !half && c.x_type != MOE_T_F32 && c.head_dim % 16 == 0 && c.rot_first % 16 == 0 && c.rot_dim % 16 == 0;
   const int v = wide ? 16 : vec ? 8 : 1;
   a.units_rot = half || !vec ? a.pairs / (half ? v : 1) : c.rot_dim / v;
