@@ -91,7 +91,7 @@ struct AttnWork {
   static constexpr int OVER = OVER_;        // places of an item beside its key tiles
   static constexpr int SNAP = SNAP_;        // an item is cut this far from its ends at the least
   static constexpr int MIN_RUN = MIN_RUN_;  // more blocks take part only if each has so many places, or an item
-  static constexpr int JOIN = JOIN_;        // what a part costs who joins them, in hundredths of a place; 0: nothing
+  static constexpr int JOIN = JOIN_;        // what a part costs who joins them, in hundredths of a place
   static_assert(OVER >= 1 && SNAP > OVER, "every part of an item has a key tile");
   static __device__ __forceinline__ int row_tiles(const AttnSeq& q, const AttnGroup& group) {
     return q.n > 0 ? (q.n * group.n - 1) / R + 1 : 0;
@@ -192,7 +192,8 @@ __device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan&
   __syncthreads();
   long long least = W::MIN_RUN;
   // an item of T places in n parts takes T / n and then n joins: least where n^2 is T over the join's places
-  if (W::JOIN && total > 0) least = max(least, (long long)sqrtf((float)total / (float)all * (W::JOIN * 0.01f)));
+  if (total * W::JOIN > all * (100ll * W::MIN_RUN * W::MIN_RUN))
+    least = (long long)sqrtf((float)total / (float)all * (W::JOIN * 0.01f));
   const int runs = (int)min((long long)gridDim.x, max(attn_div(total, least), all));
   if (tid == 0) {
     S.total = total;

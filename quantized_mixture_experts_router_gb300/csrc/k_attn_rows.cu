@@ -27,8 +27,9 @@ constexpr int NP = 4;                      // warps that copy
 constexpr int NTHR = (NW + NP) * 32;
 // An item costs about as much as six tiles from memory beside its own, a join twice
 // that; a block's warps work on eight tiles at once, so that a run of fewer is no
-// shorter.
-using Work = AttnWork<R, TK, 6, 12, 8, 0>;
+// shorter.  Eight parts are joined at once; one costs half a tile (one token over 131000,
+// 16 heads on one key head: 34 us, 39 with as many runs as blocks, 49 with four at once).
+using Work = AttnWork<R, TK, 6, 12, 8, 50>;
 using Walk = AttnWalk<Work>;
 constexpr uint32_t HALF = TK * 128;        // 64 values of a tile's keys
 constexpr uint32_t QHALF = R * 128;        // 64 values of an item's queries
@@ -380,7 +381,7 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
         };
         for (int i = tid; i < rows * d4; i += NW * 32) {
           const int r = i / d4, d = (i - r * d4) * 4;
-          const AttnJoined v = attn_join<4>(
+          const AttnJoined v = attn_join<8>(
               n, [&](int x) { return __ldcg(reinterpret_cast<const float2*>(at(x)) + r); },
               [&](int x) { return __ldcg(reinterpret_cast<const float4*>(at(x) + R * 2 + r * D + d)); });
           attn_store<BF>(a, w.q.row0, w.h, w.row0() + r, d, v);
