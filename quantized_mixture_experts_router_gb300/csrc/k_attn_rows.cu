@@ -12,8 +12,8 @@
 // empty, and p would have to pass through tensor memory; here it goes from the
 // accumulators of the first product straight into the operands of the second.
 //
-// Measured: one token over 131000 (64 heads over 8 key heads of 128, 537 MB) 87.5 us, 91%
-// of a copy's rate; 60 of 40 to 7300 tokens each 75 us (85%); one over 700, 10.7 us:
+// Measured: one token over 131000 (64 heads over 8 key heads of 128, 537 MB) 89 us, 89%
+// of a copy's rate; 60 of 40 to 7300 tokens each 76 us (84%); one over 700, 11.6 us:
 // the cut 2.5, the first box 1.5, its tile, the end of an item and the join.
 #include "attn_work.cuh"
 
