@@ -350,12 +350,19 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
     }
     named_bar_sync(1, NW * 32);
     const bool whole = w.whole();
+    // A copying warp that gave up leaves its arrivals out: from there on a phase of the queries' barrier is not one
+    // item's, and a warp that had waited for nothing yet may have taken other queries for this item's.  `abort` is
+    // set before such a phase ends, as it ends only after this block's warps have given an item back whose queries
+    // were not all there.  (A stage's barrier hears of one copying warp, and one computing warp waits for its
+    // every use in turn.)
+    const bool gone = *(volatile uint32_t*)&S.abort != 0u;
     float* part = reinterpret_cast<float*>(a.part + (2 * (size_t)blockIdx.x + (w.skip ? 0 : 1)) * a.slot);
     for (int i = tid; i < rows * d4; i += NW * 32) {
       const int r = i / d4, d = (i - r * d4) * 4;
-      const AttnJoined v = attn_join<1>(
+      AttnJoined v = attn_join<1>(
           NW, [&](int x) { return *reinterpret_cast<const float2*>(S.ml[x][r]); },
           [&](int x) { return *reinterpret_cast<const float4*>(&S.o[x][r][d]); });
+      if (gone) v.l = NAN;
       if (whole) {
         attn_store<BF>(a, w.q.row0, w.h, w.row0() + r, d, v);
       } else {
