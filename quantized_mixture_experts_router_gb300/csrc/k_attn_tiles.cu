@@ -63,7 +63,7 @@ struct Half {
 };
 // An item as the warps need it.
 struct Item {
-  int live;             // 0: the run has ended, and nothing else is told
+  int number;           // of the run, from 1 on; 0: the run has ended, and nothing else is told
   int tok0, pos0, len;  // first row, its position, and the tokens of the sequence
   int row0;             // of the sequence's rows (tokens x heads of the group)
   int b, h;             // sequence, key head
@@ -75,6 +75,10 @@ struct Item {
   Half half[2];
 };
 constexpr int NITEMS = 4;
+// `told` counts the items that the walking warp has told, and the one that it will tell next.  Who waited too long,
+// a reader for an item that is not among these or the walking warp for a reader, sets NO_MORE.  Then no other item
+// is told, and as this is one word, all warps agree on the last: they meet at barriers within an item.
+constexpr uint32_t NO_MORE = 0x80000000u;
 constexpr int ITEM_READERS = NSOFT / 32 + 3;  // softmax, issuing and value warps
 
 struct TilesCtl {
@@ -84,7 +88,7 @@ struct TilesCtl {
   unsigned long long s_full[2], p_full[2];      // scores to the softmax; weights to the products
   unsigned long long o_full[2], o_free[2];      // an item's output, complete; read
   unsigned long long done[2];
-  uint32_t tmem, abort, last[2], turn;
+  uint32_t tmem, abort, last[2], turn, told;
   Item items[NITEMS];
   alignas(16) float2 hand[TR];                              // (maximum, sum) of a row that the second half hands to the first
   AttnPlan plan;
@@ -108,14 +112,19 @@ struct Reader {
   uint32_t n = 0;
   __device__ __forceinline__ explicit Reader(const Env& e) : E(e) {}
   __device__ __forceinline__ const Item& item() const { return E.C.items[n % NITEMS]; }
-  // waits for the next; whether there is one
+  // waits for the next, until it is told or it is certain that it will not be; whether there is one.  What lies in
+  // a slot that was not told is another item's, or none.
   __device__ __forceinline__ bool get() {
     unsigned long long& bar = E.C.i_full[n % NITEMS];
     const uint32_t parity = (n / NITEMS) & 1u;
     if (!__all_sync(0xffffffffu, mbar_try_wait(attn_bar(bar), parity)))
-      __all_sync(0xffffffffu, mbar_wait_for(attn_bar(bar), parity, 4 * E.a.timeout_ns, E.a.status));
-    return item().live;
+      while (!__all_sync(0xffffffffu, mbar_wait_for(attn_bar(bar), parity, 4 * E.a.timeout_ns, E.a.status)))
+        if (none()) return false;
+    return item().number == (int)n + 1;
   }
+  // That there will be no item n (for all lanes as for the first).  One that is announced comes: the walking warp's
+  // own waits end.
+  __device__ __forceinline__ bool none() const { return (atomicCAS(&E.C.told, n, n | NO_MORE) & ~NO_MORE) == n; }
   // has read it
   __device__ __forceinline__ void done() {
     __syncwarp();
@@ -199,20 +208,17 @@ struct Ring {
   // barrier's phase flips with every use, as `par` does from the second use on).
   __device__ __forceinline__ void drain() {
     const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
+#pragma unroll 1
     for (uint32_t i = 0; i < NS; ++i)
       if ((used >> i) & 1u) mbar_wait_bounded(attn_bar(full[i]), (par >> i) & 1u, deadline, a.status);
   }
 };
 
 // The walk's item, by a whole warp (each lane finds the same).
-__device__ __forceinline__ void tell(const AttnArgs& a, const AttnPlan& plan, const Walk& w, Item& it) {
-  const bool lead = (threadIdx.x & 31) == 0;
-  if (!w.live) {
-    if (lead) it.live = 0;
-    return;
-  }
-  Item x;
-  x.live = 1;
+__device__ __forceinline__ Item describe(const AttnArgs& a, const AttnPlan& plan, const Walk& w, int number) {
+  Item x{};
+  if (!w.live) return x;
+  x.number = number;
   x.tok0 = w.q.row0;
   x.pos0 = w.q.pos0;
   x.len = w.q.len;
@@ -243,7 +249,43 @@ __device__ __forceinline__ void tell(const AttnArgs& a, const AttnPlan& plan, co
     t.last = min((g.hi - 1) / TK, x.from + x.steps - 1);
     if (x.split && ((t.last - t.first) & 1)) --t.last;
   }
-  if (lead) it = x;
+  return x;
+}
+
+constexpr uint32_t NAN2 = 0x7fff7fffu;  // two NaNs, bf16 or fp16
+
+// An item that is not told, by a whole warp: NaN, and its part counted all the same, so that the counters are ready
+// for the next call.  (In rolled loops, as all code that is hardly run: the kernel's instructions fill their caches,
+// and 10 KB more of them cost seven prompts 3%.)
+__device__ __forceinline__ void lose(const AttnArgs& a, const Item& it) {
+  const int lane = threadIdx.x & 31, D = a.p.c.kv.head_dim;
+#pragma unroll 1
+  for (int s = 0; s < (it.split ? 1 : 2); ++s) {
+    const int first = s ? it.half[1].row0 : it.half[0].row0, end = first + (s ? it.half[1].rows : it.half[0].rows);
+    if (!it.whole) {
+      float* part = reinterpret_cast<float*>(a.part + (2 * (size_t)blockIdx.x + it.slot) * a.slot);
+#pragma unroll 1
+      for (int r = first + lane; r < end; r += 32) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(0.f, NAN);
+      __threadfence();
+      __syncwarp();
+      bool last = false;
+      if (lane == 0) {
+        unsigned* count = a.count + 2 * it.c0 + s;
+        last = atomicAdd(count, 1u) == (unsigned)(it.n - 1);
+        if (last) *count = 0u;
+      }
+      if (!__any_sync(0xffffffffu, last)) continue;  // (a part of NaN makes the whole of it)
+    }
+#pragma unroll 1
+    for (int r = first + lane; r < end; r += 32) {
+      const int row = it.row0 + r, tok = a.group.token(row), hd = it.h * a.group.n + row - tok * a.group.n;
+      const long long t = it.tok0 + tok;
+      uint16_t* out = static_cast<uint16_t*>(a.p.out) + t * a.p.ldo + (long long)hd * D;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(out + d) = make_uint4(NAN2, NAN2, NAN2, NAN2);
+      if (a.p.lse) a.p.lse[t * a.p.ld_lse + hd] = NAN;
+    }
+  }
 }
 
 template <int DH>
@@ -251,15 +293,32 @@ __device__ void run_k(const AttnArgs& a, TilesCtl& C, uint32_t ring) {
   Ring<DH, Cfg<DH>::NK> K(a, C, &a.map_k, ring, 0);
   bool ok = true;
   uint32_t n = 0;
+  uint32_t was = 0;  // of `told`, when this item was announced (the first lane's)
+  bool telling = true;
   for (Walk w(a.p, a.group, C.plan);; w.next()) {
+    const bool lead = (threadIdx.x & 31) == 0;
     const uint32_t e = n % NITEMS;
-    if (n >= NITEMS) mbar_wait_for(attn_bar(C.i_empty[e]), (n / NITEMS - 1) & 1u, 4 * a.timeout_ns, a.status);
+    if (telling) {
+      telling = __all_sync(0xffffffffu, !lead || was == n);  // not if a reader gave up before
+      if (telling && n >= NITEMS) {
+        telling = __all_sync(0xffffffffu, mbar_wait_for(attn_bar(C.i_empty[e]), (n / NITEMS - 1) & 1u, 4 * a.timeout_ns, a.status));
+        if (!telling && lead) atomicExch(&C.told, n | NO_MORE);
+      }
+    }
+    const Item x = describe(a, C.plan, w, (int)n + 1);
+    if (!telling) {
+      if (!w.live) break;
+      lose(a, x);
+      continue;
+    }
+    if (lead) {
+      C.items[e] = x;
+      mbar_arrive(attn_bar(C.i_full[e]));
+    }
     __syncwarp();
-    tell(a, C.plan, w, C.items[e]);
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(attn_bar(C.i_full[e]));
     ++n;
     if (!w.live) break;
+    if (lead) was = atomicCAS(&C.told, n, n + 1);  // announces the next; the answer comes while keys are copied
     const int steps = w.key_steps();
     if (!steps || !ok) continue;
     const Item& it = C.items[e];  // stays until this warp overwrites it
@@ -975,8 +1034,10 @@ __global__ void __launch_bounds__(NTHR, 1) k_attn_tiles(const __grid_constant__ 
     for (int i = 0; i < NITEMS; ++i) {
       mbar_init(attn_bar(C.i_full[i]), 1);
       mbar_init(attn_bar(C.i_empty[i]), ITEM_READERS);
+      C.items[i].number = 0;
     }
     C.abort = C.turn = 0u;
+    C.told = 1u;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&C.tmem, 512);
