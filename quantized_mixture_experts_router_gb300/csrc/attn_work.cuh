@@ -190,11 +190,11 @@ __device__ void attn_plan(const AttnParams& p, const AttnGroup& group, AttnPlan&
     all += scratch[w][1];
   }
   __syncthreads();
-  long long least = W::MIN_RUN;
+  long long most = total / W::MIN_RUN;
   // an item of T places in n parts takes T / n and then n joins: least where n^2 is T over the join's places
   if (total * W::JOIN > all * (100ll * W::MIN_RUN * W::MIN_RUN))
-    least = (long long)sqrtf((float)total / (float)all * (W::JOIN * 0.01f));
-  const int runs = (int)min((long long)gridDim.x, max(attn_div(total, least), all));
+    most = attn_div(total, (long long)sqrtf((float)total / (float)all * (W::JOIN * 0.01f)));
+  const int runs = (int)min((long long)gridDim.x, max(most, all));
   if (tid == 0) {
     S.total = total;
     S.runs = runs;

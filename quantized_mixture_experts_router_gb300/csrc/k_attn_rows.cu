@@ -280,6 +280,22 @@ __device__ __forceinline__ void do_tile(const uint32_t base, int key, const Attn
   }
 }
 
+// Joins the n parts of an item's rows that runs c0 .. c0 + n - 1 have left, U at once.  Most items that are cut have
+// two: asking for eight whatever there are took 11.6 us for one token over 700 and 76.2 for 60 of 40 to 7300, as
+// many as there are 11.4 and 75.8.
+template <int U, bool BF>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, int c0, int n, int tok0, int h, int row0, int rows) {
+  const int D = a.p.c.kv.head_dim, d4 = D / 4;
+  auto at = [&](int x) { return reinterpret_cast<const float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot); };
+  for (int i = threadIdx.x; i < rows * d4; i += NW * 32) {
+    const int r = i / d4, d = (i - r * d4) * 4;
+    const AttnJoined v = attn_join<U>(
+        n, [&](int x) { return __ldcg(reinterpret_cast<const float2*>(at(x)) + r); },
+        [&](int x) { return __ldcg(reinterpret_cast<const float4*>(at(x) + R * 2 + r * D + d)); });
+    attn_store<BF>(a, tok0, h, row0 + r, d, v);
+  }
+}
+
 template <int DH, bool BF>
 __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
   constexpr int NS = Cfg<DH>::NS;
@@ -383,16 +399,8 @@ __device__ void run_rows(const AttnArgs& a, Shared<DH>& S) {
       named_bar_sync(1, NW * 32);
       if (S.last) {
         __threadfence();
-        auto at = [&](int x) {
-          return reinterpret_cast<const float*>(a.part + (2 * (size_t)(c0 + x) + (x ? 0 : 1)) * a.slot);
-        };
-        for (int i = tid; i < rows * d4; i += NW * 32) {
-          const int r = i / d4, d = (i - r * d4) * 4;
-          const AttnJoined v = attn_join<8>(
-              n, [&](int x) { return __ldcg(reinterpret_cast<const float2*>(at(x)) + r); },
-              [&](int x) { return __ldcg(reinterpret_cast<const float4*>(at(x) + R * 2 + r * D + d)); });
-          attn_store<BF>(a, w.q.row0, w.h, w.row0() + r, d, v);
-        }
+        if (n <= 2) join_parts<2, BF>(a, c0, n, w.q.row0, w.h, w.row0(), rows);
+        else join_parts<8, BF>(a, c0, n, w.q.row0, w.h, w.row0(), rows);
       }
     }
     named_bar_sync(1, NW * 32);
