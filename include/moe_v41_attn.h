@@ -49,7 +49,11 @@ typedef struct {
  *           is stretched by factor, the fastest not at all
  *   PARTS   g f_i + (1 - g) f_i / factor, where g goes from 0 at one turn within
  *           the trained positions to 1 at 32 turns; magnitude 0.1 ln(factor) + 1
- *           (the by-parts scaling of YaRN, Peng et al. 2023) */
+ *           (the by-parts scaling of YaRN, Peng et al. 2023, as the paper writes it).
+ *           g is linear in the turns, and 1 and 32 are fixed.  Model code that
+ *           interpolates over the pair's number i between two rounded bounds, or has
+ *           other bounds or another magnitude, gives other angles for the same
+ *           factor: its checkpoints need a table of its own making. */
 enum { MOE_ROPE_SCALE_NONE = 0, MOE_ROPE_SCALE_LINEAR = 1, MOE_ROPE_SCALE_BASE = 2, MOE_ROPE_SCALE_PARTS = 3 };
 MOE_API int moe_v41_rope_freqs(int rot_dim, double base, int kind, double factor, int trained, double* freqs,
                                float* magnitude);

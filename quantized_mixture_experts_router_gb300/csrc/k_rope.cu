@@ -17,6 +17,9 @@ namespace moe {
 namespace {
 
 constexpr int NTHR = 256;
+// SMs of the GPU that the library is built for.  It only spreads the work: asking the device would cost a call whose
+// time is the host's, and another count is served as rightly.
+constexpr int SMS = 152;
 
 struct RopeArgs {
   RopeParams p;
@@ -270,12 +273,12 @@ int launch_rope(const RopeParams& p, cudaStream_t s) {
   // About four units a thread; but a token's heads are shared by several blocks while there are few tokens.
   const long long units = (long long)a.heads * a.units;
   a.tokens = (int)(units >= 512 ? 1 : 1024 / units > 8 ? 8 : 1024 / units);
-  while (a.tokens > 1 && (p.m + a.tokens - 1) / a.tokens < 152 * 4) a.tokens /= 2;
+  while (a.tokens > 1 && (p.m + a.tokens - 1) / a.tokens < SMS * 4) a.tokens /= 2;
   a.per_token = AttnGroup::of((int)units);
   a.per_head = AttnGroup::of(a.units);
   const int blocks = (p.m + a.tokens - 1) / a.tokens;
   long long split = (units * a.tokens + NTHR - 1) / NTHR;
-  if (split * blocks > 152 * 8) split = blocks >= 152 * 8 ? 1 : (152 * 8 + blocks - 1) / blocks;
+  if (split * blocks > SMS * 8) split = blocks >= SMS * 8 ? 1 : (SMS * 8 + blocks - 1) / blocks;
   const dim3 grid((unsigned)blocks, (unsigned)(split < 65535 ? split : 65535));
   if (!append) {
     if (c.x_type == MOE_T_F32) return launch_v<float, float, false>(a, v, grid, s);
