@@ -408,17 +408,22 @@ def moe_v41_token_logprobs(cfg, logits, m, ld, allowed, ld_allowed, target, logp
 
 # ------------------------------------- operators of an attention block (moe_v41_attn.h)
 
-def _type(t, dtype, what):
-    """refuses lengths, positions and angles of another type than the kernels read (an address does not say which, and
-    torch's default types are others)"""
-    if t is not None and not isinstance(t, int) and _dtypes.get(t.dtype) is not dtype:
+_I32, _F32, _F64 = "int32", "float32", "float64"
+_dtypes = {}  # by torch's dtype, its name as above (a look-up costs a tenth of making the name)
+
+
+def _typed(t, dtype, what):
+    """_p of lengths, positions or angles, which are refused in another type than the kernels read (an address does not
+    say which, and torch's default types are others)"""
+    if t is None:
+        return None
+    if isinstance(t, int):
+        return t
+    if _dtypes.get(t.dtype) is not dtype:
         if str(t.dtype) != "torch." + dtype:
             raise MoeError(MOE_ERR_ARG, f"{what} is {t.dtype}, not {dtype}")
         _dtypes[t.dtype] = dtype
-
-
-_dtypes = {}  # by torch's dtype, its name as it stands below (a look-up costs a tenth of making the name)
-_I32, _F32, _F64 = "int32", "float32", "float64"
+    return t.data_ptr()
 
 
 def moe_v41_rope_freqs(rot_dim, base=10000.0, kind=MOE_ROPE_SCALE_NONE, factor=1.0, trained=0):
@@ -436,10 +441,9 @@ def make_rope_cfg(head_dim, rot_dim=None, rot_first=0, layout=MOE_ROPE_HALF, x_t
 
 
 def moe_v41_rope(cfg, m, heads, x, ldx, ldx_head, pos, freqs, out, ldo, ldo_head, stream=None):
-    _type(pos, _I32, "moe_v41_rope: pos")
-    _type(freqs, _F64, "moe_v41_rope: freqs")
-    _check(lib().moe_v41_rope(ctypes.byref(cfg), m, heads, _p(x), ldx, ldx_head, _p(pos), _p(freqs), _p(out), ldo,
-                              ldo_head, _s(stream)), "moe_v41_rope")
+    _check(lib().moe_v41_rope(ctypes.byref(cfg), m, heads, _p(x), ldx, ldx_head, _typed(pos, _I32, "moe_v41_rope: pos"),
+                              _typed(freqs, _F64, "moe_v41_rope: freqs"), _p(out), ldo, ldo_head, _s(stream)),
+           "moe_v41_rope")
 
 
 def make_kv_cfg(kv_heads, head_dim, page_size, n_pages, type=MOE_T_BF16, page_pitch=None, token_pitch=None,
@@ -453,23 +457,23 @@ def make_kv_cfg(kv_heads, head_dim, page_size, n_pages, type=MOE_T_BF16, page_pi
 
 def make_seqs(batch, cu_new, kv_len, table, max_pages, ld_table=None) -> moe_v41_seqs:
     """int32 tensors on the device; holds their addresses, and the tensors themselves as long as it lives"""
-    for name, t in (("cu_new", cu_new), ("kv_len", kv_len), ("table", table)):
-        _type(t, _I32, f"make_seqs: {name}")
+    given = {"cu_new": cu_new, "kv_len": kv_len, "table": table}
+    at = [_typed(t, _I32, f"make_seqs: {name}") for name, t in given.items()]
+    for name, t in given.items():
         if t is not None and not isinstance(t, int) and t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
             raise MoeError(MOE_ERR_ARG, f"make_seqs: {name} has gaps")
-    s = moe_v41_seqs(batch, max_pages, _p(cu_new), _p(kv_len), _p(table),
-                     max_pages if ld_table is None else ld_table)
+    s = moe_v41_seqs(batch, max_pages, *at, max_pages if ld_table is None else ld_table)
     s.keep = (cu_new, kv_len, table)
     return s
 
 
 def moe_v41_kv_append(kv, rope, seqs, m, k, ldk, v, ldv, k_cache, v_cache, q_heads, q, ldq, q_out, ldq_out, freqs,
                       pos, status, stream=None):
-    _type(pos, _I32, "moe_v41_kv_append: pos")
-    _type(freqs, _F64, "moe_v41_kv_append: freqs")
     _check(lib().moe_v41_kv_append(ctypes.byref(kv), ctypes.byref(rope), ctypes.byref(seqs), m, _p(k), ldk, _p(v),
-                                   ldv, _p(k_cache), _p(v_cache), q_heads, _p(q), ldq, _p(q_out), ldq_out, _p(freqs),
-                                   _p(pos), _p(status), _s(stream)), "moe_v41_kv_append")
+                                   ldv, _p(k_cache), _p(v_cache), q_heads, _p(q), ldq, _p(q_out), ldq_out,
+                                   _typed(freqs, _F64, "moe_v41_kv_append: freqs"),
+                                   _typed(pos, _I32, "moe_v41_kv_append: pos"), _p(status), _s(stream)),
+           "moe_v41_kv_append")
 
 
 def make_attn_cfg(kv, heads, causal=True, window=0, scale=1.0) -> moe_v41_attn_cfg:
@@ -481,7 +485,7 @@ def moe_v41_attn_workspace_bytes(cfg: moe_v41_attn_cfg) -> int:
 
 
 def moe_v41_paged_attention(cfg, seqs, m, max_new, q, ldq, k_cache, v_cache, out, ldo, lse, ld_lse, ws, stream=None):
-    _type(lse, _F32, "moe_v41_paged_attention: lse")
     _check(lib().moe_v41_paged_attention(ctypes.byref(cfg), ctypes.byref(seqs), m, max_new, _p(q), ldq, _p(k_cache),
-                                         _p(v_cache), _p(out), ldo, _p(lse), ld_lse, _p(ws), _nbytes(ws),
+                                         _p(v_cache), _p(out), ldo,
+                                         _typed(lse, _F32, "moe_v41_paged_attention: lse"), ld_lse, _p(ws), _nbytes(ws),
                                          _s(stream)), "moe_v41_paged_attention")
