@@ -373,15 +373,21 @@ int launch_attn_rows(const AttnArgs& a, int ctas, cudaStream_t s);
 int launch_attn_tiles(const AttnArgs& a, int ctas, bool* taken, cudaStream_t s);  // *taken: whether it was launched
 __device__ __forceinline__ uint64_t* attn_bar(unsigned long long& b) { return reinterpret_cast<uint64_t*>(&b); }
 
-// Bounded wait of a warp; once one ran out, the block's later waits do not wait.
+// Bounded wait of a warp.  Once one ran out, the block's others give up as well, those under way and those to come.
 __device__ __forceinline__ bool attn_wait_long(uint64_t* bar, uint32_t parity, volatile uint32_t* abort,
                                                    uint64_t timeout_ns, unsigned* status) {
   bool ok = false;
 #pragma unroll 1
   for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
   if (!ok && !*abort) {
-    ok = mbar_wait_for(bar, parity, timeout_ns, status);
-    if (!ok) *abort = 1u;
+    const uint64_t deadline = globaltimer_ns() + timeout_ns;
+#pragma unroll 1
+    do ok = mbar_try_wait_sleep(bar, parity, 20000u);
+    while (!ok && !*abort && globaltimer_ns() < deadline);
+    if (!ok) {
+      atomicOr(status, (unsigned)MOE_STATUS_TIMEOUT);
+      *abort = 1u;
+    }
   }
   return __all_sync(0xffffffffu, ok);
 }
