@@ -75,9 +75,9 @@ int launch_paged_attention(const AttnParams& p, int max_new, void* ws, cudaStrea
     return make_cache_map(&a.map_k, kv, p.k_cache, a.box_rows) && make_cache_map(&a.map_v, kv, p.v_cache, a.box_rows);
   };
   // Up to 16 rows of a key head (tokens of a sequence x heads) or more.  Both sides, 8 heads
-  // a key head: two tokens of 16 sequences over 6000, 44 us by the kernel for few rows and
-  // 53 by the other; four, 64 and 52; eight, 134 and 54; two of 64 sequences over 600, 50
-  // and 62; four, 89 and 62.
+  // a key head: two tokens of 16 sequences over 6000, 45 us by the kernel for few rows and
+  // 51 by the other; four, 64 and 52; eight, 135 and 54; two of 64 sequences over 600, 50
+  // and 61; four, 89 and 61.
   if ((long long)max_new * a.group.n > ATTN_ROWS_TILE) {
     if (!maps(ATTN_TILES_KEYS)) return MOE_ERR_CUDA;
     a.q_map = 128 % a.group.n == 0 && p.ldq < (int64_t(1) << 38);

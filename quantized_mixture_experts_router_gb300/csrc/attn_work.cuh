@@ -4,9 +4,11 @@
 // The items, numbered sequence by sequence, in it head by head, in it row tile by
 // row tile, make one line, of which an item takes OVER places (what it costs
 // whatever its length, in key tiles) and one for each of its key tiles.  The line
-// is cut into about equal runs, one for each block: whatever the lengths, the
-// blocks have the same work.  An item that a cut goes through is joined
-// by the last of its blocks to finish, in the order of the runs.
+// is cut into about equal runs, one for each block.  A cut near an item's end is moved
+// there, each for itself, so that a run can gain at both ends: the longest has about a fifth
+// more than an even share where items are many, and half as much again where there are
+// as many as blocks; and one of fewer than SNAP places may come out empty.  An item that
+// a cut goes through is joined by the last of its blocks to finish, in the order of the runs.
 //
 // Lengths are on the device, so every block works the cut out for itself.
 #pragma once

@@ -12,9 +12,10 @@
 // empty, and p would have to pass through tensor memory; here it goes from the
 // accumulators of the first product straight into the operands of the second.
 //
-// Measured: one token over 131000 (64 heads over 8 key heads of 128, 537 MB) 89 us, 89%
-// of a copy's rate; 60 of 40 to 7300 tokens each 76 us (84%); one over 700, 11.6 us:
-// the cut 2.5, the first box 1.5, its tile, the end of an item and the join.
+// Measured in a graph: one token over 131000 (64 heads over 8 key heads of 128, 537 MB) 89 us, 89%
+// of a copy's rate; 60 of 40 to 7300 tokens each 76 us (84%), the longest run 11% over an even
+// share; one over 700, 11.3 us: the cut 2.5, the first box 1.5, its tile, the end of an item and
+// the join.  Heads above 64 values take all 168 registers and spill 16 to 28 bytes.
 #include "attn_work.cuh"
 
 namespace moe {

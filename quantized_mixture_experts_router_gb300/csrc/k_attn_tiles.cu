@@ -19,11 +19,12 @@
 // when its maximum has grown by more than 2^8 over the reference, which its own
 // thread then does in place.
 //
-// Bound by the softmax between a tile's two products: at 2048 tokens over 10000 (32 heads
-// over 8 key heads of 128, 301 GFLOP) 251 us, 1200 TFLOP/s, the tensor pipe busy 53% of
-// the time; by bytes where the rows are few (five tokens of 16 sequences over 3000 to
-// 7400: 79 us, 4.8 TB/s); by what an item takes beside its tiles (first copies, the end,
-// joins) where items are short (seven prompts of up to 2500: 104 us).
+// Bound (times among calls of its kind in a graph) by the softmax between a tile's two
+// products: at 2048 tokens over 10000 (32 heads over 8 key heads of 128, 301 GFLOP) 224 us,
+// 1340 TFLOP/s, the tensor pipe busy 58% of the time; by bytes where the rows are few (five
+// tokens of 16 sequences over 3000 to 7400: 79 us, 4.8 TB/s); where items are short by runs
+// that come out uneven and by what an item takes beside its tiles, first copies, the end,
+// joins (seven prompts of up to 2500: 106 us; the longest run has 56 places, an even share 46).
 #include "attn_work.cuh"
 #include "tc.cuh"
 

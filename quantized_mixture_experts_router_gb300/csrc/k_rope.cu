@@ -8,8 +8,10 @@
 // pos f / 2 pi minus its nearest whole number (exact to 2^-52 of the turns), then
 // sincospi in f32.  Values move eight at a time (16-bit neighbours 16) wherever the
 // head's parts begin at multiples of it (both halves' vectors in one thread), else one
-// pair at a time.  One row of 32 heads of 128 takes 1.8 us, a launch; 4096 rows of 16
-// heads of 192, f32 (101 MB), 17 us, 88% of a copy's rate.
+// pair at a time.  Among its kind in a graph, inputs partly in L2, one row of 32 heads of 128
+// takes 1.8 us, a launch, and 4096 rows of 16 heads of 192, f32 (101 MB), 17 us.  As a call
+// on data that is not there it takes 22 us, 68% of a copy's rate: a thread has one unit on
+// its way, and the first waits for look-ups and angles that it does not need.
 #include "attn_work.cuh"
 
 namespace moe {
