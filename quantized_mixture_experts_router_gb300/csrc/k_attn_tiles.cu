@@ -20,11 +20,11 @@
 // thread then does in place.
 //
 // Bound (times among calls of its kind in a graph) by the softmax between a tile's two
-// products: at 2048 tokens over 10000 (32 heads over 8 key heads of 128, 301 GFLOP) 224 us,
-// 1340 TFLOP/s, the tensor pipe busy 58% of the time; by bytes where the rows are few (five
+// products: at 2048 tokens over 10000 (32 heads over 8 key heads of 128, 301 GFLOP) 218 us,
+// 1380 TFLOP/s, the tensor pipe busy 58% of the time; by bytes where the rows are few (five
 // tokens of 16 sequences over 3000 to 7400: 79 us, 4.8 TB/s); where items are short by runs
 // that come out uneven and by what an item takes beside its tiles, first copies, the end,
-// joins (seven prompts of up to 2500: 106 us; the longest run has 56 places, an even share 46).
+// joins (seven prompts of up to 2500: 105 us; the longest run has 56 places, an even share 46).
 #include "attn_work.cuh"
 #include "tc.cuh"
 
@@ -120,11 +120,11 @@ struct Reader {
     const uint32_t parity = (n / NITEMS) & 1u;
     if (!__all_sync(0xffffffffu, mbar_try_wait(attn_bar(bar), parity)))
       while (!__all_sync(0xffffffffu, mbar_wait_for(attn_bar(bar), parity, 4 * E.a.timeout_ns, E.a.status)))
-        if (none()) return false;
+        if (__shfl_sync(0xffffffffu, (int)none(), 0)) return false;
     return item().number == (int)n + 1;
   }
-  // That there will be no item n (for all lanes as for the first).  One that is announced comes: the walking warp's
-  // own waits end.
+  // That there will be no item n.  One that is announced comes or is taken back, as the walking warp's own waits end;
+  // so that the answer may change between the lanes, and the first one's counts.
   __device__ __forceinline__ bool none() const { return (atomicCAS(&E.C.told, n, n | NO_MORE) & ~NO_MORE) == n; }
   // has read it
   __device__ __forceinline__ void done() {
